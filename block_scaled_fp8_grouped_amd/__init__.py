@@ -33,6 +33,13 @@ OUT_BF16 = 1
 STATUS_NEGATIVE_SPLIT = 1
 STATUS_EXCEEDS_CAPACITY = 2
 MAX_GROUPS = 1024
+F32 = 0  # BSFP8_F32
+BF16 = 1  # BSFP8_BF16
+GATE_NONE = 0
+GATE_CHANNEL = 1  # gate[cols]
+GATE_TOKEN = 2  # gate[rows]
+STATE_F32 = 0
+STATE_8BIT = 1
 
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
@@ -79,6 +86,23 @@ def lib():
         L.bsfp8_grouped_gemm_dgrad.restype = ctypes.c_int
         L.bsfp8_grouped_gemm_dgrad.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i32, ctypes.c_int, _vp,
                                                ctypes.c_int, _vp, _vp]
+        _f, _d = ctypes.c_float, ctypes.c_double
+        L.bsfp8_residual_norm.restype = ctypes.c_int
+        L.bsfp8_residual_norm.argtypes = [_i64, _i64, _vp, ctypes.c_int, _vp, _vp, _vp, _vp, ctypes.c_int, _f, _f, _f,
+                                          _f, _vp, _vp, _vp, _vp, _vp]
+        L.bsfp8_residual_norm_grad_workspace_bytes.restype = _sz
+        L.bsfp8_residual_norm_grad_workspace_bytes.argtypes = [_i64, _i64]
+        L.bsfp8_residual_norm_grad.restype = ctypes.c_int
+        L.bsfp8_residual_norm_grad.argtypes = [_i64, _i64, ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                               ctypes.c_int, _f, _f, _f, _vp, _vp, _vp, _vp, _vp, ctypes.c_int, _vp,
+                                               _vp]
+        L.bsfp8_adamw_plan_bytes.restype = _sz
+        L.bsfp8_adamw_plan_bytes.argtypes = [_vp, _i32, ctypes.POINTER(_i64)]
+        L.bsfp8_adamw_plan.restype = ctypes.c_int
+        L.bsfp8_adamw_plan.argtypes = [_vp, _i32, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _sz]
+        L.bsfp8_adamw_step.restype = ctypes.c_int
+        L.bsfp8_adamw_step.argtypes = [_vp, _i32, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _d, _d, _d, _d, _d,
+                                       _i64, _vp, _vp, _vp, _vp, _vp]
         L.bsfp8_strerror.restype = ctypes.c_char_p
         L.bsfp8_strerror.argtypes = [ctypes.c_int]
         _lib = L
@@ -107,6 +131,8 @@ _BF16 = (torch.bfloat16, torch.int16)  # bf16 data, or its bits viewed as int16
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
 _F32_BITS = (torch.float32, torch.int32)
+_STREAM = (torch.float32, torch.bfloat16)  # element types of a residual stream, parameters, gradients
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
 
 
 def _dev(t, what, dtypes):
@@ -317,3 +343,217 @@ def grouped_gemm_dgrad(dy_q, n, w_q, k, split_sizes, capacity_rows, out, out_dty
     rc = lib().bsfp8_grouped_gemm_dgrad(*args)
     _check(rc, "grouped_gemm_dgrad")
     return out
+
+
+# ------------------------------------------------------------------------------------------
+# norms around a block
+# ------------------------------------------------------------------------------------------
+
+def _dtype_code(t):
+    return F32 if t.dtype == torch.float32 else BF16
+
+
+def _like(t, shape, what, dtype=None):
+    """A tensor argument of exactly this shape (and element type, where given)."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
+
+
+def _check_norm_block(rows, cols, y, post_weight, pre_weight, gate, gate_kind):
+    _like(y, (rows, cols), "y")
+    _like(post_weight, (cols,), "post_weight")
+    _like(pre_weight, (cols,), "pre_weight")
+    if gate_kind == GATE_CHANNEL:
+        _like(gate, (cols,), "gate")
+    elif gate_kind == GATE_TOKEN:
+        _like(gate, (rows,), "gate")
+
+
+def residual_norm(x, y=None, post_weight=None, pre_weight=None, gate=None, gate_kind=GATE_NONE, x_scale=1.0,
+                  y_scale=1.0, eps=1e-6, weight_offset=0.0, r=None, n=None, rstd_y=None, rstd_r=None, stream=None):
+    """bsfp8_residual_norm on the residual stream x [rows, cols] (fp32 or bf16) and the block's
+    output y [rows, cols] (bf16):
+
+        r = x_scale * x + y_scale * gate * (y * rstd_y * (post_weight + weight_offset))
+        n = r * rstd_r * (pre_weight + weight_offset)
+
+    post_weight, pre_weight: fp32 [cols]; None leaves out that norm (without pre_weight there is no
+    n).  gate: fp32 [cols] (GATE_CHANNEL) or [rows] (GATE_TOKEN).  Returns a dict of r (x's type), n
+    (bf16), rstd_y and rstd_r (fp32 [rows], for the gradient), in the tensors given or in new ones;
+    r may be x."""
+    if x.dim() != 2:
+        raise ValueError("residual_norm: x is [rows, cols]")
+    rows, cols = x.shape
+    px = _dev(x, "x", _STREAM)
+    py, pw, qw = _dev(y, "y", _BF16), _dev(post_weight, "post_weight", _F32), _dev(pre_weight, "pre_weight", _F32)
+    pg = _dev(gate, "gate", _F32)
+    _check_norm_block(rows, cols, y, post_weight, pre_weight, gate, gate_kind)
+    out = {"r": torch.empty_like(x) if r is None else r}
+    if pre_weight is not None:
+        out["n"] = torch.empty((rows, cols), dtype=torch.bfloat16, device=x.device) if n is None else n
+        out["rstd_r"] = torch.empty(rows, dtype=torch.float32, device=x.device) if rstd_r is None else rstd_r
+    if post_weight is not None:
+        out["rstd_y"] = torch.empty(rows, dtype=torch.float32, device=x.device) if rstd_y is None else rstd_y
+    if r is not None:
+        _like(r, (rows, cols), "r", x.dtype)
+    _like(n, (rows, cols), "n")
+    _like(rstd_y, (rows,), "rstd_y")
+    _like(rstd_r, (rows,), "rstd_r")
+    rc = lib().bsfp8_residual_norm(
+        rows, cols, px, _dtype_code(x), py, pw, qw, pg, gate_kind, x_scale, y_scale, eps, weight_offset,
+        _dev(out["r"], "r", _STREAM), _dev(out.get("n", n), "n", _BF16), _dev(out.get("rstd_y", rstd_y), "rstd_y", _F32),
+        _dev(out.get("rstd_r", rstd_r), "rstd_r", _F32), _stream(stream))
+    _check(rc, "residual_norm")
+    return out
+
+
+def residual_norm_grad_workspace_bytes(rows, cols):
+    return int(lib().bsfp8_residual_norm_grad_workspace_bytes(rows, cols))
+
+
+def residual_norm_grad(dn, dr, r=None, rstd_r=None, pre_weight=None, y=None, rstd_y=None, post_weight=None, gate=None,
+                       gate_kind=GATE_NONE, x_scale=1.0, y_scale=1.0, weight_offset=0.0, dx=None, dy=None,
+                       dpre_weight=None, dpost_weight=None, dgate=None, accumulate=False, workspace=None, stream=None):
+    """bsfp8_residual_norm_grad: the gradient of residual_norm from dn [rows, cols] (bf16, the gradient
+    at n, or None) and dr [rows, cols] (the stream's type, the gradient at r, or None), with r, rstd_r,
+    rstd_y as the forward returned them.  Returns a dict of dx (the stream's type), dy (bf16) and, for
+    the weights and the gate that are there, dpre_weight, dpost_weight, dgate (fp32), in the tensors
+    given or in new ones.  accumulate: the weights' and a channel gate's gradients are added to the
+    tensors given."""
+    ref = dr if dr is not None else r
+    if ref is None:
+        raise ValueError("residual_norm_grad: neither dr nor (dn and r)")
+    if ref.dim() != 2:
+        raise ValueError("residual_norm_grad: r and dr are [rows, cols]")
+    rows, cols = ref.shape
+    dev = ref.device
+    pdn, pdr, pr = _dev(dn, "dn", _BF16), _dev(dr, "dr", _STREAM), _dev(r, "r", _STREAM)
+    args = (pr, _dev(rstd_r, "rstd_r", _F32), _dev(pre_weight, "pre_weight", _F32), _dev(y, "y", _BF16),
+            _dev(rstd_y, "rstd_y", _F32), _dev(post_weight, "post_weight", _F32), _dev(gate, "gate", _F32))
+    _like(dn, (rows, cols), "dn")
+    _like(dr, (rows, cols), "dr", ref.dtype)
+    _like(r, (rows, cols), "r", ref.dtype)
+    _like(rstd_r, (rows,), "rstd_r")
+    _like(rstd_y, (rows,), "rstd_y")
+    _check_norm_block(rows, cols, y, post_weight, pre_weight, gate, gate_kind)
+    if accumulate and any(w is not None and d is None for w, d in (
+            (pre_weight, dpre_weight), (post_weight, dpost_weight),
+            (gate if gate_kind == GATE_CHANNEL else None, dgate))):
+        raise ValueError("residual_norm_grad: accumulate needs the gradients to add to")
+    f32 = dict(dtype=torch.float32, device=dev)
+    out = {"dx": torch.empty((rows, cols), dtype=ref.dtype, device=dev) if dx is None else dx}
+    if y is not None:
+        out["dy"] = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev) if dy is None else dy
+    if pre_weight is not None:
+        out["dpre_weight"] = torch.empty(cols, **f32) if dpre_weight is None else dpre_weight
+    if post_weight is not None:
+        out["dpost_weight"] = torch.empty(cols, **f32) if dpost_weight is None else dpost_weight
+    if gate is not None:
+        out["dgate"] = torch.empty(gate.shape, **f32) if dgate is None else dgate
+    _like(out["dx"], (rows, cols), "dx", ref.dtype)
+    _like(out.get("dy", dy), (rows, cols), "dy")
+    _like(out.get("dpre_weight", dpre_weight), (cols,), "dpre_weight")
+    _like(out.get("dpost_weight", dpost_weight), (cols,), "dpost_weight")
+    if gate is not None:
+        _like(out["dgate"], gate.shape, "dgate")
+    need = residual_norm_grad_workspace_bytes(rows, cols)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _need(workspace, need, "workspace")
+    rc = lib().bsfp8_residual_norm_grad(
+        rows, cols, _dtype_code(ref), pdn, pdr, *args, gate_kind, x_scale, y_scale, weight_offset,
+        _dev(out["dx"], "dx", _STREAM), _dev(out.get("dy", dy), "dy", _BF16),
+        _dev(out.get("dpre_weight", dpre_weight), "dpre_weight", _F32),
+        _dev(out.get("dpost_weight", dpost_weight), "dpost_weight", _F32), _dev(out.get("dgate", dgate), "dgate", _F32),
+        1 if accumulate else 0, _dev(workspace, "workspace", (workspace.dtype,)), _stream(stream))
+    _check(rc, "residual_norm_grad")
+    return out
+
+
+# ------------------------------------------------------------------------------------------
+# AdamW
+# ------------------------------------------------------------------------------------------
+
+class _AdamTensor(ctypes.Structure):
+    _fields_ = [("param", _vp), ("grad", _vp), ("exp_avg", _vp), ("exp_avg_sq", _vp), ("exp_avg_scale", _vp),
+                ("exp_avg_sq_scale", _vp), ("copy", _vp), ("numel", _i64), ("lr_scale", ctypes.c_float),
+                ("decay_scale", ctypes.c_float)]
+
+
+class AdamWPlan:
+    """The tensors of an AdamW step, their addresses laid out on the device once (adamw_plan).  It holds
+    the tensors; they stay where they are as long as it is used."""
+
+    def __init__(self, table, num_tensors, num_chunks, param_dtype, grad_dtype, state, tensors):
+        self.table, self.num_tensors, self.num_chunks = table, num_tensors, num_chunks
+        self.param_dtype, self.grad_dtype, self.state, self.tensors = param_dtype, grad_dtype, state, tensors
+
+
+def adamw_plan(params, grads, exp_avgs, exp_avg_sqs, exp_avg_scales=None, exp_avg_sq_scales=None, copies=None,
+               lr_scales=None, decay_scales=None):
+    """Plan of an AdamW step over lists of tensors: params and grads (fp32 or bf16, one type each),
+    states exp_avgs and exp_avg_sqs as fp32, or as e4m3 codes (uint8 or float8_e4m3fn) with the fp32
+    scales [ceil(numel / 128)] in exp_avg_scales and exp_avg_sq_scales (the second state is sqrt(v);
+    zeroed codes and scales are a valid start).  copies: bf16 tensors (or None) that receive the new
+    params.  lr_scales, decay_scales: factors on lr and weight_decay per tensor (default 1)."""
+    n = len(params)
+    if n == 0:
+        raise ValueError("adamw_plan: no tensors")
+    q8 = exp_avg_scales is not None
+    if q8 != (exp_avg_sq_scales is not None):
+        raise ValueError("adamw_plan: exp_avg_scales and exp_avg_sq_scales come together")
+    none = [None] * n
+    lists = dict(grads=grads, exp_avgs=exp_avgs, exp_avg_sqs=exp_avg_sqs, exp_avg_scales=exp_avg_scales or none,
+                 exp_avg_sq_scales=exp_avg_sq_scales or none, copies=copies or none, lr_scales=lr_scales or [1.0] * n,
+                 decay_scales=decay_scales or [1.0] * n)
+    for name, v in lists.items():
+        if len(v) != n:
+            raise ValueError(f"adamw_plan: {len(v)} {name} for {n} params")
+    ptypes, gtypes = (params[0].dtype,), (grads[0].dtype,)
+    for name, t in (("params", ptypes), ("grads", gtypes)):
+        if t[0] not in _STREAM:
+            raise TypeError(f"{name}[0]: dtype {t[0]}, expected torch.float32 or torch.bfloat16")
+    stypes = _E4M3 if q8 else _F32
+    device = params[0].device
+    table, numels = (_AdamTensor * n)(), (_i64 * n)()
+    for i, (p, g, m, v, ms, vs, c, ls, ds) in enumerate(zip(params, *lists.values())):
+        size = p.numel()
+        for what, t, types, count in (("params", p, ptypes, size), ("grads", g, gtypes, size),
+                                      ("exp_avgs", m, stypes, size), ("exp_avg_sqs", v, stypes, size),
+                                      ("exp_avg_scales", ms, _F32, (size + 127) // 128),
+                                      ("exp_avg_sq_scales", vs, _F32, (size + 127) // 128),
+                                      ("copies", c, (torch.bfloat16,), size)):
+            if t is None:
+                continue
+            _dev(t, f"{what}[{i}]", types)
+            if t.numel() != count:
+                raise ValueError(f"{what}[{i}]: {t.numel()} elements, expected {count}")
+            if t.device != device:
+                raise ValueError(f"{what}[{i}]: on {t.device}, params[0] on {device}")
+        numels[i] = size
+        table[i] = _AdamTensor(p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), _ptr(ms), _ptr(vs), _ptr(c),
+                               size, ls, ds)
+    chunks = _i64()
+    nbytes = lib().bsfp8_adamw_plan_bytes(numels, n, ctypes.byref(chunks))
+    host = torch.empty(max(1, nbytes), dtype=torch.uint8)
+    pd, gd, st = _dtype_code(params[0]), _dtype_code(grads[0]), STATE_8BIT if q8 else STATE_F32
+    _check(lib().bsfp8_adamw_plan(table, n, pd, gd, st, host.data_ptr(), nbytes), "adamw_plan")
+    kept = (list(params),) + tuple(lists.values())[:6]
+    return AdamWPlan(host.to(device), n, chunks.value, pd, gd, st, kept)
+
+
+def adamw_step(plan, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, step=1, lr_dev=None, step_dev=None,
+               grad_scale=None, noop_flag=None, stream=None):
+    """bsfp8_adamw_step: one AdamW step over the plan's tensors, in place.  step counts from 1.  Device
+    scalars: lr_dev (fp32) and step_dev (int32) replace lr and step (for a captured graph), grad_scale
+    (fp32) multiplies the gradients, a nonzero noop_flag (fp32) leaves everything as it is."""
+    rc = lib().bsfp8_adamw_step(plan.table.data_ptr(), plan.num_tensors, plan.num_chunks, plan.param_dtype,
+                                plan.grad_dtype, plan.state, lr, beta1, beta2, eps, weight_decay, step,
+                                _dev(lr_dev, "lr_dev", _F32), _dev(step_dev, "step_dev", _I32),
+                                _dev(grad_scale, "grad_scale", _F32), _dev(noop_flag, "noop_flag", _F32),
+                                _stream(stream))
+    _check(rc, "adamw_step")

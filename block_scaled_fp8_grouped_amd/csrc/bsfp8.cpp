@@ -7,7 +7,11 @@
 #include <stdint.h>
 
 #include "../../include/bsfp8.h"
+#include <string.h>
+
+#include "adamw_plan.hpp"
 #include "group_layout.hpp"
+#include "norm_layout.hpp"
 
 namespace bsfp8 {
 int launch_grouped_quantize(const void* in, int64_t R, int64_t C, const int32_t* splits, int E, int recipe,
@@ -25,6 +29,17 @@ int launch_grouped_gemm_fprop(const uint8_t* x_q, const uint8_t* x_s, int64_t R,
 int launch_grouped_gemm_dgrad(const uint8_t* dy_q, const uint8_t* dy_s, int64_t R, int64_t n, const uint8_t* w_q,
                               const void* w_s, int64_t k, const int32_t* splits, int E, int recipe, void* out,
                               int out_dtype, uint32_t* status, hipStream_t stream);
+int launch_residual_norm(int64_t R, int64_t C, const void* x, int x_f32, const void* y, const float* post_w,
+                         const float* pre_w, const float* gate, int gate_kind, float x_scale, float y_scale, float eps,
+                         float offset, void* r, void* n, float* rstd_y, float* rstd_r, hipStream_t stream);
+int launch_residual_norm_grad(int64_t R, int64_t C, int x_f32, const void* dn, const void* dr, const void* r,
+                              const float* rstd_r, const float* pre_w, const void* y, const float* rstd_y,
+                              const float* post_w, const float* gate, int gate_kind, float x_scale, float y_scale,
+                              float offset, void* dx, void* dy, float* dpre_w, float* dpost_w, float* dgate,
+                              int accumulate, float* workspace, hipStream_t stream);
+int launch_adamw(const void* plan, int32_t num_tensors, int64_t chunks, int p_f32, int g_f32, int q8, double lr,
+                 double beta1, double beta2, double eps, double decay, int64_t step, const float* lr_dev,
+                 const int32_t* step_dev, const float* grad_scale, const float* noop_flag, hipStream_t stream);
 }  // namespace bsfp8
 
 namespace {
@@ -51,6 +66,21 @@ constexpr int64_t kMaxKExtent = (int64_t(1) << 24) - 128;
 // lanes past the last column with offsets from 2^31 up: 128 * 4 * (output row length) must stay
 // below 2^31.
 constexpr int64_t kMaxOutCols = int64_t(1) << 21;
+bool aligned_to(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
+bool valid_dtype(int d) { return d == BSFP8_F32 || d == BSFP8_BF16; }
+bool finite_nonnegative(double v) { return isfinite(v) && v >= 0.0; }
+// rows and columns of the residual norms: every element offset fits in int64
+bool valid_norm_shape(int64_t rows, int64_t cols) {
+  return rows >= 0 && rows <= (int64_t(1) << 40) && cols >= 1 && cols <= bsfp8::kNormMaxCols;
+}
+// the block's output, its norm and its gate, as both directions take them
+int check_norm_block(const void* y, const float* post_w, const float* gate, int gate_kind) {
+  if (gate_kind < BSFP8_GATE_NONE || gate_kind > BSFP8_GATE_TOKEN) return BSFP8_ERR_ARGUMENT;
+  if (gate_kind != BSFP8_GATE_NONE && gate == nullptr) return BSFP8_ERR_NULL_POINTER;
+  if (gate_kind == BSFP8_GATE_NONE && gate != nullptr) return BSFP8_ERR_ARGUMENT;
+  if (y == nullptr && (post_w != nullptr || gate != nullptr)) return BSFP8_ERR_ARGUMENT;
+  return BSFP8_OK;
+}
 
 }  // namespace
 
@@ -198,6 +228,144 @@ int bsfp8_grouped_gemm_dgrad(const uint8_t* dy_row_q, const uint8_t* dy_row_s, i
     return BSFP8_ERR_ALIGNMENT;
   return bsfp8::launch_grouped_gemm_dgrad(dy_row_q, dy_row_s, capacity_rows, n, w_col_q, w_col_s, k, split_sizes,
                                           num_groups, recipe, out, out_dtype, status, (hipStream_t)stream);
+}
+
+int bsfp8_residual_norm(int64_t rows, int64_t cols, const void* x, int stream_dtype, const void* y,
+                        const float* post_weight, const float* pre_weight, const float* gate, int gate_kind,
+                        float x_scale, float y_scale, float eps, float weight_offset, void* r, void* n, float* rstd_y,
+                        float* rstd_r, void* stream) {
+  if (!valid_norm_shape(rows, cols)) return BSFP8_ERR_SHAPE;
+  if (!valid_dtype(stream_dtype) || !isfinite(x_scale) || !isfinite(y_scale) || !isfinite(weight_offset) ||
+      !finite_nonnegative(eps))
+    return BSFP8_ERR_ARGUMENT;
+  if (rows == 0) return BSFP8_OK;
+  const int rc = check_norm_block(y, post_weight, gate, gate_kind);
+  if (rc != BSFP8_OK) return rc;
+  if (x == nullptr || (pre_weight != nullptr && n == nullptr) || (pre_weight == nullptr && r == nullptr))
+    return BSFP8_ERR_NULL_POINTER;
+  if (pre_weight == nullptr && (n != nullptr || rstd_r != nullptr)) return BSFP8_ERR_ARGUMENT;
+  if (post_weight == nullptr && rstd_y != nullptr) return BSFP8_ERR_ARGUMENT;
+  if (!aligned16(x) || !aligned16(y) || !aligned16(post_weight) || !aligned16(pre_weight) || !aligned16(gate) ||
+      !aligned16(r) || !aligned16(n) || !aligned4(rstd_y) || !aligned4(rstd_r))
+    return BSFP8_ERR_ALIGNMENT;
+  return bsfp8::launch_residual_norm(rows, cols, x, stream_dtype == BSFP8_F32, y, post_weight, pre_weight, gate,
+                                     gate_kind, x_scale, y_scale, eps, weight_offset, r, n, rstd_y, rstd_r,
+                                     (hipStream_t)stream);
+}
+
+size_t bsfp8_residual_norm_grad_workspace_bytes(int64_t rows, int64_t cols) {
+  if (!valid_norm_shape(rows, cols)) return 0;
+  return (size_t)bsfp8::norm_grad_slots(rows, cols) * 3 * (size_t)cols * sizeof(float);
+}
+
+int bsfp8_residual_norm_grad(int64_t rows, int64_t cols, int stream_dtype, const void* dn, const void* dr,
+                             const void* r, const float* rstd_r, const float* pre_weight, const void* y,
+                             const float* rstd_y, const float* post_weight, const float* gate, int gate_kind,
+                             float x_scale, float y_scale, float weight_offset, void* dx, void* dy,
+                             float* dpre_weight, float* dpost_weight, float* dgate, int accumulate, void* workspace,
+                             void* stream) {
+  if (!valid_norm_shape(rows, cols)) return BSFP8_ERR_SHAPE;
+  if (!valid_dtype(stream_dtype) || !isfinite(x_scale) || !isfinite(y_scale) || !isfinite(weight_offset) ||
+      (accumulate != 0 && accumulate != 1))
+    return BSFP8_ERR_ARGUMENT;
+  const bool sums = dpre_weight != nullptr || dpost_weight != nullptr ||
+                    (gate_kind == BSFP8_GATE_CHANNEL && dgate != nullptr);
+  if (rows > 0) {
+    const int rc = check_norm_block(y, post_weight, gate, gate_kind);
+    if (rc != BSFP8_OK) return rc;
+    if (dn == nullptr && dr == nullptr) return BSFP8_ERR_NULL_POINTER;
+    if (dn != nullptr && (r == nullptr || rstd_r == nullptr || pre_weight == nullptr)) return BSFP8_ERR_NULL_POINTER;
+    if (post_weight != nullptr && rstd_y == nullptr) return BSFP8_ERR_NULL_POINTER;
+    if (sums && workspace == nullptr) return BSFP8_ERR_NULL_POINTER;
+  } else if (gate_kind < BSFP8_GATE_NONE || gate_kind > BSFP8_GATE_TOKEN) {
+    return BSFP8_ERR_ARGUMENT;
+  }
+  // a gradient of what the call has none of
+  if (rows > 0 && ((dn == nullptr && (dpre_weight != nullptr || r != nullptr || rstd_r != nullptr ||
+                                      pre_weight != nullptr)) ||
+                   (y == nullptr && dy != nullptr) || (post_weight == nullptr && dpost_weight != nullptr)))
+    return BSFP8_ERR_ARGUMENT;
+  if (gate_kind == BSFP8_GATE_NONE && dgate != nullptr) return BSFP8_ERR_ARGUMENT;
+  if (!aligned16(dn) || !aligned16(dr) || !aligned16(r) || !aligned16(pre_weight) || !aligned16(y) ||
+      !aligned16(post_weight) || !aligned16(gate) || !aligned16(dx) || !aligned16(dy) || !aligned16(dpre_weight) ||
+      !aligned16(dpost_weight) || !aligned16(dgate) || !aligned16(workspace) || !aligned4(rstd_r) || !aligned4(rstd_y))
+    return BSFP8_ERR_ALIGNMENT;
+  return bsfp8::launch_residual_norm_grad(rows, cols, stream_dtype == BSFP8_F32, dn, dr, r, rstd_r, pre_weight, y,
+                                          rstd_y, post_weight, gate, gate_kind, x_scale, y_scale, weight_offset, dx,
+                                          dy, dpre_weight, dpost_weight, dgate, accumulate, (float*)workspace,
+                                          (hipStream_t)stream);
+}
+
+size_t bsfp8_adamw_plan_bytes(const int64_t* numels, int32_t num_tensors, int64_t* num_chunks) {
+  int64_t chunks = 0;
+  bool ok = numels != nullptr && num_tensors > 0;
+  for (int32_t i = 0; ok && i < num_tensors; ++i) {
+    ok = numels[i] >= 0 && numels[i] <= (int64_t(1) << 40);
+    if (ok) chunks += bsfp8::adam_chunks_of(numels[i]);
+    ok = ok && chunks <= 0x7fffffff;
+  }
+  if (!ok) chunks = 0;
+  if (num_chunks != nullptr) *num_chunks = chunks;
+  return ok ? (size_t)(bsfp8::adam_table_bytes(num_tensors) + chunks * (int64_t)sizeof(bsfp8::AdamChunk)) : 0;
+}
+
+int bsfp8_adamw_plan(const bsfp8_adamw_tensor* tensors, int32_t num_tensors, int param_dtype, int grad_dtype,
+                     int state, void* host_plan, size_t host_plan_bytes) {
+  if (tensors == nullptr || host_plan == nullptr) return BSFP8_ERR_NULL_POINTER;
+  if (!valid_dtype(param_dtype) || !valid_dtype(grad_dtype) || (state != BSFP8_STATE_F32 && state != BSFP8_STATE_8BIT))
+    return BSFP8_ERR_ARGUMENT;
+  if (num_tensors <= 0) return BSFP8_ERR_SHAPE;
+  const bool q8 = state == BSFP8_STATE_8BIT;
+  const int pb = param_dtype == BSFP8_F32 ? 4 : 2, gb = grad_dtype == BSFP8_F32 ? 4 : 2, sb = q8 ? 1 : 4;
+  int64_t chunks = 0;
+  for (int32_t i = 0; i < num_tensors; ++i) {
+    const bsfp8_adamw_tensor& t = tensors[i];
+    if (t.numel < 0 || t.numel > (int64_t(1) << 40)) return BSFP8_ERR_SHAPE;
+    chunks += bsfp8::adam_chunks_of(t.numel);
+    if (chunks > 0x7fffffff) return BSFP8_ERR_SHAPE;
+    if (!isfinite(t.lr_scale) || !isfinite(t.decay_scale)) return BSFP8_ERR_ARGUMENT;
+    if (t.numel == 0) continue;
+    if (t.param == nullptr || t.grad == nullptr || t.exp_avg == nullptr || t.exp_avg_sq == nullptr ||
+        (q8 && (t.exp_avg_scale == nullptr || t.exp_avg_sq_scale == nullptr)))
+      return BSFP8_ERR_NULL_POINTER;
+    if (!aligned_to(t.param, pb) || !aligned_to(t.grad, gb) || !aligned_to(t.exp_avg, sb) ||
+        !aligned_to(t.exp_avg_sq, sb) || !aligned_to(t.copy, 2) ||
+        (q8 && (!aligned4(t.exp_avg_scale) || !aligned4(t.exp_avg_sq_scale))))
+      return BSFP8_ERR_ALIGNMENT;
+  }
+  const int64_t table = bsfp8::adam_table_bytes(num_tensors);
+  if (host_plan_bytes < (size_t)(table + chunks * (int64_t)sizeof(bsfp8::AdamChunk))) return BSFP8_ERR_SHAPE;
+  memset(host_plan, 0, (size_t)table);
+  memcpy(host_plan, tensors, (size_t)num_tensors * sizeof(bsfp8_adamw_tensor));
+  uint8_t* at = (uint8_t*)host_plan + table;
+  for (int32_t i = 0; i < num_tensors; ++i) {
+    const int64_t n = bsfp8::adam_chunks_of(tensors[i].numel);
+    for (int64_t j = 0; j < n; ++j, at += sizeof(bsfp8::AdamChunk)) {
+      const bsfp8::AdamChunk c{i, (int32_t)j};
+      memcpy(at, &c, sizeof(c));
+    }
+  }
+  return BSFP8_OK;
+}
+
+int bsfp8_adamw_step(const void* device_plan, int32_t num_tensors, int64_t num_chunks, int param_dtype,
+                     int grad_dtype, int state, double lr, double beta1, double beta2, double eps,
+                     double weight_decay, int64_t step, const float* lr_dev, const int32_t* step_dev,
+                     const float* grad_scale, const float* noop_flag, void* stream) {
+  if (!valid_dtype(param_dtype) || !valid_dtype(grad_dtype) || (state != BSFP8_STATE_F32 && state != BSFP8_STATE_8BIT))
+    return BSFP8_ERR_ARGUMENT;
+  if (!finite_nonnegative(lr) || !finite_nonnegative(eps) || !finite_nonnegative(weight_decay) ||
+      !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || step < 1)
+    return BSFP8_ERR_ARGUMENT;
+  if (num_tensors <= 0 || num_chunks < 0 || num_chunks > 0x7fffffff) return BSFP8_ERR_SHAPE;
+  if (num_chunks == 0) return BSFP8_OK;  // only empty tensors
+  if (device_plan == nullptr) return BSFP8_ERR_NULL_POINTER;
+  if (!aligned16(device_plan) || !aligned4(lr_dev) || !aligned4(step_dev) || !aligned4(grad_scale) ||
+      !aligned4(noop_flag))
+    return BSFP8_ERR_ALIGNMENT;
+  return bsfp8::launch_adamw(device_plan, num_tensors, num_chunks, param_dtype == BSFP8_F32, grad_dtype == BSFP8_F32,
+                             state == BSFP8_STATE_8BIT, lr, beta1, beta2, eps, weight_decay, step, lr_dev, step_dev,
+                             grad_scale, noop_flag, (hipStream_t)stream);
 }
 
 const char* bsfp8_strerror(int code) {

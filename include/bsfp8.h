@@ -277,6 +277,125 @@ int bsfp8_grouped_gemm_dgrad(const uint8_t* dy_row_q, const uint8_t* dy_row_s, i
                              const int32_t* split_sizes, int32_t num_groups, int recipe, void* out,
                              int out_dtype, uint32_t* status, void* stream);
 
+/* ----------------------------------------------------------------------------------------- */
+/* Norms before and after a block, fused with the block's gate and the residual sum.          */
+/* ----------------------------------------------------------------------------------------- */
+
+/* Element types of the residual stream, of parameters and of gradients. */
+#define BSFP8_F32 0
+#define BSFP8_BF16 1
+
+/* Gates of a block's output. */
+#define BSFP8_GATE_NONE 0
+#define BSFP8_GATE_CHANNEL 1 /* gate[cols] */
+#define BSFP8_GATE_TOKEN 2   /* gate[rows] */
+
+/*
+ * For each of `rows` rows of `cols` channels, in fp32:
+ *     z = y * rstd_y * (post_weight + weight_offset),   rstd_y = 1 / sqrt(mean(y^2) + eps)
+ *     r = x_scale * x + y_scale * gate * z
+ *     n = r * rstd_r * (pre_weight + weight_offset),    rstd_r = 1 / sqrt(mean(r^2) + eps)
+ * x            [rows][cols] of stream_dtype (BSFP8_F32 or BSFP8_BF16): the residual stream
+ * y            [rows][cols] bf16, the block's output, or NULL (r = x_scale * x)
+ * post_weight  fp32 [cols], the norm after the block, or NULL (z = y)
+ * pre_weight   fp32 [cols], the norm before the next block, or NULL (no n)
+ * gate         fp32, as gate_kind says (NULL for BSFP8_GATE_NONE)
+ * r            [rows][cols] of stream_dtype; may be x itself, and may be NULL where pre_weight is given
+ * n            [rows][cols] bf16 (required with pre_weight, NULL without)
+ * rstd_y, rstd_r  fp32 [rows], kept for the gradient, or NULL
+ * r and n are each rounded once from the fp32 values (n from r before its rounding).  Any rows and
+ * any cols in [1, 32768]; data pointers aligned to 16 bytes, each array contiguous.  Without y,
+ * post_weight and gate must be NULL.
+ * rows == 0 returns BSFP8_OK without touching any pointer.
+ */
+int bsfp8_residual_norm(int64_t rows, int64_t cols, const void* x, int stream_dtype, const void* y,
+                        const float* post_weight, const float* pre_weight, const float* gate,
+                        int gate_kind, float x_scale, float y_scale, float eps, float weight_offset,
+                        void* r, void* n, float* rstd_y, float* rstd_r, void* stream);
+
+/*
+ * Its gradient.  With rh = r * rstd_r, yh = y * rstd_y (yh = y without post_weight):
+ *     g1 = dn * (pre_weight + weight_offset)
+ *     d  = dr + rstd_r * (g1 - rh * mean(g1 * rh))       dx = x_scale * d
+ *     t  = y_scale * d, dz = gate * t
+ *     g2 = dz * (post_weight + weight_offset)            dy = rstd_y * (g2 - yh * mean(g2 * yh))
+ *                                                        (dy = dz without post_weight)
+ *     dpre_weight = sum over rows of dn * rh             dpost_weight = sum over rows of dz * yh
+ *     dgate = sum of t * z over the rows (BSFP8_GATE_CHANNEL) or the channels (BSFP8_GATE_TOKEN)
+ * dn           [rows][cols] bf16, the gradient at n, or NULL (then r, rstd_r, pre_weight are NULL too)
+ * dr           [rows][cols] of stream_dtype, the gradient at r, or NULL; dn or dr is given
+ * r, rstd_r, rstd_y   as the forward left them (rstd_y with post_weight)
+ * dx           [rows][cols] of stream_dtype or NULL; may be dr itself
+ * dy           [rows][cols] bf16 or NULL; may be dn itself
+ * dpre_weight, dpost_weight, dgate   fp32 or NULL; accumulate == 1 adds to the weights' and the
+ *              channel gate's (one fp32 add each), a token gate's gradient is always stored
+ * workspace    bsfp8_residual_norm_grad_workspace_bytes() bytes of device memory, needed when
+ *              dpre_weight, dpost_weight or a channel gate's dgate is asked for
+ * Sums over rows are taken in a fixed order.  rows == 0: the stored sums become zero.
+ */
+size_t bsfp8_residual_norm_grad_workspace_bytes(int64_t rows, int64_t cols);
+int bsfp8_residual_norm_grad(int64_t rows, int64_t cols, int stream_dtype, const void* dn, const void* dr,
+                             const void* r, const float* rstd_r, const float* pre_weight, const void* y,
+                             const float* rstd_y, const float* post_weight, const float* gate,
+                             int gate_kind, float x_scale, float y_scale, float weight_offset, void* dx,
+                             void* dy, float* dpre_weight, float* dpost_weight, float* dgate,
+                             int accumulate, void* workspace, void* stream);
+
+/* ----------------------------------------------------------------------------------------- */
+/* AdamW over many tensors in one launch, states in fp32 or in 8 bits.                        */
+/* ----------------------------------------------------------------------------------------- */
+/*
+ * For each element, every operation rounded to fp32 in the order written (the scalars that depend
+ * on lr and step are formed in fp64 and rounded once):
+ *     g = grad * grad_scale
+ *     m = m * beta1 + g * (1 - beta1)
+ *     v = v * beta2 + g * g * (1 - beta2)
+ *     p = p * (1 - lr * weight_decay) - m / (sqrt(v) * (1 - beta2^step)^(-1/2) + eps)
+ *                                         * (lr / (1 - beta1^step))
+ * BSFP8_STATE_F32: m and v are fp32 arrays.
+ * BSFP8_STATE_8BIT: m and u = sqrt(v) are e4m3 arrays; every 128 consecutive elements of a tensor
+ *   (the last block may be shorter) share one fp32 scale sf = max(amax / 448, 1e-30), a code
+ *   standing for code * sf.  New states are stored as e4m3(m * (1 / sf)); p uses them unrounded.
+ *   Zeroed codes and scales are a valid start.
+ * Non-finite gradients enter the states; noop_flag is for skipping such a step.
+ */
+#define BSFP8_STATE_F32 0
+#define BSFP8_STATE_8BIT 1
+
+typedef struct bsfp8_adamw_tensor {
+  void* param;              /* fp32 or bf16, updated */
+  const void* grad;         /* fp32 or bf16 */
+  void* exp_avg;            /* m: fp32, or e4m3 codes */
+  void* exp_avg_sq;         /* v: fp32, or e4m3 codes of sqrt(v) */
+  float* exp_avg_scale;     /* 8-bit states: fp32 [ceil(numel / 128)]; else NULL */
+  float* exp_avg_sq_scale;  /* the same */
+  void* copy;               /* bf16 copy of the new param, or NULL */
+  int64_t numel;            /* >= 0 */
+  float lr_scale;           /* this tensor's factor on lr */
+  float decay_scale;        /* this tensor's factor on weight_decay */
+} bsfp8_adamw_tensor;
+
+/* Bytes of a plan for tensors of these sizes and the number of its chunks (a kernel argument);
+ * 0 (and *num_chunks 0) for invalid arguments.  Host only. */
+size_t bsfp8_adamw_plan_bytes(const int64_t* numels, int32_t num_tensors, int64_t* num_chunks);
+/* Writes the plan into HOST memory; the caller copies it to the device (16-byte aligned) once and
+ * keeps it while the tensors stay where they are.  Element pointers need only their element's
+ * alignment.  Checks every tensor: BSFP8_ERR_NULL_POINTER, _SHAPE, _ALIGNMENT. */
+int bsfp8_adamw_plan(const bsfp8_adamw_tensor* tensors, int32_t num_tensors, int param_dtype,
+                     int grad_dtype, int state, void* host_plan, size_t host_plan_bytes);
+/*
+ * One step over the plan's tensors (param_dtype, grad_dtype, state and the counts as it was made with).
+ * lr >= 0, 0 <= beta1, beta2 < 1, eps >= 0, weight_decay >= 0, step >= 1 (BSFP8_ERR_ARGUMENT).
+ * lr_dev, step_dev  NULL, or device scalars that replace lr and step, read when the kernel runs (a
+ *                   captured graph is replayed with new values)
+ * grad_scale        NULL (1), or a device fp32 scalar (clipping, loss scale)
+ * noop_flag         NULL, or a device fp32 scalar: nonzero leaves everything as it is
+ */
+int bsfp8_adamw_step(const void* device_plan, int32_t num_tensors, int64_t num_chunks, int param_dtype,
+                     int grad_dtype, int state, double lr, double beta1, double beta2, double eps,
+                     double weight_decay, int64_t step, const float* lr_dev, const int32_t* step_dev,
+                     const float* grad_scale, const float* noop_flag, void* stream);
+
 /* Static description of a return code. */
 const char* bsfp8_strerror(int code);
 
