@@ -86,6 +86,15 @@ def lib():
         L.bsfp8_grouped_gemm_dgrad.restype = ctypes.c_int
         L.bsfp8_grouped_gemm_dgrad.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i32, ctypes.c_int, _vp,
                                                ctypes.c_int, _vp, _vp]
+        L.bsfp8_grouped_gemm_swiglu.restype = ctypes.c_int
+        L.bsfp8_grouped_gemm_swiglu.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i32, ctypes.c_int, _vp,
+                                                _vp, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp]
+        L.bsfp8_grouped_gemm_swiglu_grad_workspace_bytes.restype = _sz
+        L.bsfp8_grouped_gemm_swiglu_grad_workspace_bytes.argtypes = [_i64, _i64, _i32]
+        L.bsfp8_grouped_gemm_swiglu_grad.restype = ctypes.c_int
+        L.bsfp8_grouped_gemm_swiglu_grad.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _i32,
+                                                     ctypes.c_int, _vp, ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp,
+                                                     _vp, _vp]
         _f, _d = ctypes.c_float, ctypes.c_double
         L.bsfp8_residual_norm.restype = ctypes.c_int
         L.bsfp8_residual_norm.argtypes = [_i64, _i64, _vp, ctypes.c_int, _vp, _vp, _vp, _vp, ctypes.c_int, _f, _f, _f,
@@ -343,6 +352,81 @@ def grouped_gemm_dgrad(dy_q, n, w_q, k, split_sizes, capacity_rows, out, out_dty
     rc = lib().bsfp8_grouped_gemm_dgrad(*args)
     _check(rc, "grouped_gemm_dgrad")
     return out
+
+
+# ------------------------------------------------------------------------------------------
+# gated feed-forward projection
+# ------------------------------------------------------------------------------------------
+
+def _which(out):
+    """The layouts that a dict of quantized outputs holds."""
+    out = out or {}
+    return (ROWWISE if out.get("row_q") is not None else 0) | (COLWISE if out.get("col_q") is not None else 0)
+
+
+def grouped_gemm_swiglu(x_q, hidden, w_q, ffn, split_sizes, capacity_rows, recipe=RECIPE_MX, probs=None, ab=None,
+                        y=None, y_dtype=OUT_BF16, out=None, status=None, stream=None):
+    """bsfp8_grouped_gemm_swiglu: y = probs * silu(a) * b with (a | b) = x W1_e^T in one kernel.  x_q is the
+    rowwise dict of x [R, hidden], w_q the rowwise dict of W1 [E * 2 ffn, hidden] (each expert's a rows,
+    then its b rows).  Any of: ab bf16 [R, 2 ffn] (kept for the gradient), y [R, ffn] (bf16 or fp32, as
+    y_dtype says), out (alloc_quantized for [R, ffn]) receives y quantized in the layouts it holds.
+    Returns a dict of those.  Rows past sum(split_sizes) are untouched."""
+    E = int(split_sizes.numel())
+    which, q = _which(out), out or {}
+    args = (_quant(x_q, "row_q", "x_q"), _quant(x_q, "row_s", "x_q"), capacity_rows, hidden,
+            _quant(w_q, "row_q", "w_q"), _quant(w_q, "row_s", "w_q"), ffn, _dev(probs, "probs", _F32),
+            _dev(split_sizes, "split_sizes", _I32), E, recipe, _dev(ab, "ab", _BF16),
+            _dev(y, "y", _F32_BITS if y_dtype == OUT_F32 else _BF16), y_dtype, which, _quant(q, "row_q", "out"),
+            _quant(q, "row_s", "out"), _quant(q, "col_q", "out"), _quant(q, "col_s", "out"),
+            _dev(status, "status", _I32), _stream(stream))
+    _need_quant(x_q, RECIPE_MX, capacity_rows, hidden, E, ROWWISE, "x_q")
+    _need_quant(w_q, RECIPE_MX, E * 2 * ffn, hidden, 1, ROWWISE, "w_q")
+    _need_quant(q, RECIPE_MX, capacity_rows, ffn, E, which, "out")
+    _need(probs, capacity_rows * 4, "probs")
+    _need(ab, capacity_rows * 2 * ffn * 2, "ab")
+    _need(y, capacity_rows * ffn * (4 if y_dtype == OUT_F32 else 2), "y")
+    rc = lib().bsfp8_grouped_gemm_swiglu(*args)
+    _check(rc, "grouped_gemm_swiglu")
+    return {k: v for k, v in dict(ab=ab, y=y, **q).items() if v is not None}
+
+
+def grouped_gemm_swiglu_grad_workspace_bytes(capacity_rows, ffn, num_groups):
+    return int(lib().bsfp8_grouped_gemm_swiglu_grad_workspace_bytes(capacity_rows, ffn, num_groups))
+
+
+def grouped_gemm_swiglu_grad(dy_q, hidden, w_q, ffn, ab, split_sizes, capacity_rows, recipe=RECIPE_MX, probs=None,
+                             dab=None, out=None, dprobs=None, workspace=None, status=None, stream=None):
+    """bsfp8_grouped_gemm_swiglu_grad: from the gradient at the second projection's output, dy_q (the
+    rowwise dict of dy [R, hidden]), that projection's weight w_q (the colwise dict of W2 viewed as
+    [E * hidden, ffn] with split sizes [hidden] * E) and the forward's ab, the gradient (da | db), as
+    bf16 dab [R, 2 ffn] and / or quantized into out (alloc_quantized for [R, 2 ffn]), and that of the
+    probabilities, dprobs fp32 [R].  Returns a dict of those.  workspace: a device tensor of
+    grouped_gemm_swiglu_grad_workspace_bytes, for dprobs (None: a new one)."""
+    E = int(split_sizes.numel())
+    which, q = _which(out), out or {}
+    need = grouped_gemm_swiglu_grad_workspace_bytes(capacity_rows, ffn, E) if dprobs is not None else 0
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=split_sizes.device)
+    args = (_quant(dy_q, "row_q", "dy_q"), _quant(dy_q, "row_s", "dy_q"), capacity_rows, hidden,
+            _quant(w_q, "col_q", "w_q"), _quant(w_q, "col_s", "w_q"), ffn, _dev(ab, "ab", _BF16),
+            _dev(probs, "probs", _F32), _dev(split_sizes, "split_sizes", _I32), E, recipe, _dev(dab, "dab", _BF16),
+            which, _quant(q, "row_q", "out"), _quant(q, "row_s", "out"), _quant(q, "col_q", "out"),
+            _quant(q, "col_s", "out"), _dev(dprobs, "dprobs", _F32),
+            None if workspace is None else _dev(workspace, "workspace", (workspace.dtype,)),
+            _dev(status, "status", _I32), _stream(stream))
+    _need_quant(dy_q, RECIPE_MX, capacity_rows, hidden, E, ROWWISE, "dy_q")
+    hp = 128 * ((hidden + 127) // 128)
+    _need(w_q.get("col_q"), ffn * E * hp, "w_q['col_q']")
+    _need(w_q.get("col_s"), ffn * E * hp // 32, "w_q['col_s']")
+    _need_quant(q, RECIPE_MX, capacity_rows, 2 * ffn, E, which, "out")
+    _need(ab, capacity_rows * 2 * ffn * 2, "ab")
+    _need(dab, capacity_rows * 2 * ffn * 2, "dab")
+    _need(probs, capacity_rows * 4, "probs")
+    _need(dprobs, capacity_rows * 4, "dprobs")
+    _need(workspace, need, "workspace")
+    rc = lib().bsfp8_grouped_gemm_swiglu_grad(*args)
+    _check(rc, "grouped_gemm_swiglu_grad")
+    return {k: v for k, v in dict(dab=dab, dprobs=dprobs, **q).items() if v is not None}
 
 
 # ------------------------------------------------------------------------------------------

@@ -12,11 +12,12 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB_PATH = os.path.join(HERE, "libbsfp8.so")
-SOURCES = ["bsfp8.cpp", "quantize.hip", "gemm.hip", "norm.hip", "adamw.hip"]
+SOURCES = ["bsfp8.cpp", "quantize.hip", "gemm.hip", "norm.hip", "adamw.hip", "glu_gemm.hip"]
 # the MFMA-only throughput probe, a library of its own (measurement, not the path)
 PEAK_LIB_PATH = os.path.join(HERE, "libbsfp8_peak.so")
 PEAK_SOURCES = ["mfma_peak.hip"]
-HEADERS = ["common.hpp", "group_layout.hpp", "tile_addr.hpp", "tile_sched.hpp", "norm_layout.hpp", "adamw_plan.hpp"]
+HEADERS = ["common.hpp", "group_layout.hpp", "tile_addr.hpp", "tile_sched.hpp", "norm_layout.hpp", "adamw_plan.hpp",
+           "glu_epilogue.hpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

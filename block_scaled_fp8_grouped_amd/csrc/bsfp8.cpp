@@ -29,6 +29,16 @@ int launch_grouped_gemm_fprop(const uint8_t* x_q, const uint8_t* x_s, int64_t R,
 int launch_grouped_gemm_dgrad(const uint8_t* dy_q, const uint8_t* dy_s, int64_t R, int64_t n, const uint8_t* w_q,
                               const void* w_s, int64_t k, const int32_t* splits, int E, int recipe, void* out,
                               int out_dtype, uint32_t* status, hipStream_t stream);
+int launch_grouped_gemm_swiglu(const uint8_t* x_q, const uint8_t* x_s, int64_t R, int64_t hidden, const uint8_t* w_q,
+                               const uint8_t* w_s, int64_t F, const float* probs, const int32_t* splits, int E,
+                               void* ab, void* y, int y_f32, uint8_t* row_q, uint8_t* row_s, uint8_t* col_q,
+                               uint8_t* col_s, uint32_t* status, hipStream_t stream);
+int launch_grouped_gemm_swiglu_grad(const uint8_t* dy_q, const uint8_t* dy_s, int64_t R, int64_t hidden,
+                                    const uint8_t* w_q, const uint8_t* w_s, int64_t F, const void* ab,
+                                    const float* probs, const int32_t* splits, int E, void* dab, uint8_t* row_q,
+                                    uint8_t* row_s, uint8_t* col_q, uint8_t* col_s, float* dprobs, float* workspace,
+                                    uint32_t* status, hipStream_t stream);
+size_t glu_grad_workspace_bytes(int64_t R, int64_t F, int E);
 int launch_residual_norm(int64_t R, int64_t C, const void* x, int x_f32, const void* y, const float* post_w,
                          const float* pre_w, const float* gate, int gate_kind, float x_scale, float y_scale, float eps,
                          float offset, void* r, void* n, float* rstd_y, float* rstd_r, hipStream_t stream);
@@ -79,6 +89,26 @@ int check_norm_block(const void* y, const float* post_w, const float* gate, int 
   if (gate_kind != BSFP8_GATE_NONE && gate == nullptr) return BSFP8_ERR_NULL_POINTER;
   if (gate_kind == BSFP8_GATE_NONE && gate != nullptr) return BSFP8_ERR_ARGUMENT;
   if (y == nullptr && (post_w != nullptr || gate != nullptr)) return BSFP8_ERR_ARGUMENT;
+  return BSFP8_OK;
+}
+
+// quantized outputs of a gated projection: the pointers of the layouts asked for
+int check_glu_quantized(int which, const void* row_q, const void* row_s, const void* col_q, const void* col_s) {
+  if ((which & BSFP8_ROWWISE) && (row_q == nullptr || row_s == nullptr)) return BSFP8_ERR_NULL_POINTER;
+  if ((which & BSFP8_COLWISE) && (col_q == nullptr || col_s == nullptr)) return BSFP8_ERR_NULL_POINTER;
+  if ((which & BSFP8_ROWWISE) && (!aligned16(row_q) || !aligned16(row_s))) return BSFP8_ERR_ALIGNMENT;
+  if ((which & BSFP8_COLWISE) && (!aligned16(col_q) || !aligned16(col_s))) return BSFP8_ERR_ALIGNMENT;
+  return BSFP8_OK;
+}
+// what both directions of a gated projection need of their sizes
+int check_glu_shape(int64_t capacity_rows, int64_t hidden, int64_t ffn, int32_t num_groups, int recipe, int which) {
+  if (!valid_recipe(recipe & ~BSFP8_GEMM_FP8_MFMA)) return BSFP8_ERR_RECIPE;
+  if (recipe != BSFP8_RECIPE_MX_1X32_E8M0) return BSFP8_ERR_LAYOUT;
+  if (!valid_groups(num_groups)) return BSFP8_ERR_NUM_GROUPS;
+  if (!valid_dim(hidden) || !valid_dim(ffn) || capacity_rows < 0 || capacity_rows > (int64_t(1) << 31) ||
+      hidden + 127 > kMaxKExtent || 2 * ffn > kMaxOutCols)
+    return BSFP8_ERR_SHAPE;
+  if ((which & ~(BSFP8_ROWWISE | BSFP8_COLWISE)) != 0) return BSFP8_ERR_ARGUMENT;
   return BSFP8_OK;
 }
 
@@ -228,6 +258,64 @@ int bsfp8_grouped_gemm_dgrad(const uint8_t* dy_row_q, const uint8_t* dy_row_s, i
     return BSFP8_ERR_ALIGNMENT;
   return bsfp8::launch_grouped_gemm_dgrad(dy_row_q, dy_row_s, capacity_rows, n, w_col_q, w_col_s, k, split_sizes,
                                           num_groups, recipe, out, out_dtype, status, (hipStream_t)stream);
+}
+
+int bsfp8_grouped_gemm_swiglu(const uint8_t* x_row_q, const uint8_t* x_row_s, int64_t capacity_rows, int64_t hidden,
+                              const uint8_t* w_q, const uint8_t* w_s, int64_t ffn, const float* probs,
+                              const int32_t* split_sizes, int32_t num_groups, int recipe, void* ab, void* y,
+                              int y_dtype, int which, uint8_t* row_q, uint8_t* row_s, uint8_t* col_q, uint8_t* col_s,
+                              uint32_t* status, void* stream) {
+  int rc = check_glu_shape(capacity_rows, hidden, ffn, num_groups, recipe, which);
+  if (rc != BSFP8_OK) return rc;
+  if (y_dtype != BSFP8_OUT_F32 && y_dtype != BSFP8_OUT_BF16) return BSFP8_ERR_ARGUMENT;
+  if (capacity_rows == 0) return BSFP8_OK;
+  if (ab == nullptr && y == nullptr && which == 0) return BSFP8_ERR_ARGUMENT;
+  if (x_row_q == nullptr || x_row_s == nullptr || w_q == nullptr || w_s == nullptr || split_sizes == nullptr)
+    return BSFP8_ERR_NULL_POINTER;
+  if (!aligned16(x_row_q) || !aligned16(x_row_s) || !aligned16(w_q) || !aligned16(w_s) || !aligned4(probs) ||
+      !aligned4(split_sizes) || !aligned16(ab) || !aligned16(y) || !aligned4(status))
+    return BSFP8_ERR_ALIGNMENT;
+  rc = check_glu_quantized(which, row_q, row_s, col_q, col_s);
+  if (rc != BSFP8_OK) return rc;
+  const bool row = (which & BSFP8_ROWWISE) != 0, col = (which & BSFP8_COLWISE) != 0;
+  return bsfp8::launch_grouped_gemm_swiglu(x_row_q, x_row_s, capacity_rows, hidden, w_q, w_s, ffn, probs, split_sizes,
+                                           num_groups, ab, y, y_dtype == BSFP8_OUT_F32, row ? row_q : nullptr,
+                                           row ? row_s : nullptr, col ? col_q : nullptr, col ? col_s : nullptr,
+                                           status, (hipStream_t)stream);
+}
+
+size_t bsfp8_grouped_gemm_swiglu_grad_workspace_bytes(int64_t capacity_rows, int64_t ffn, int32_t num_groups) {
+  if (check_glu_shape(capacity_rows, 32, ffn, num_groups, BSFP8_RECIPE_MX_1X32_E8M0, 0) != BSFP8_OK) return 0;
+  return bsfp8::glu_grad_workspace_bytes(capacity_rows, ffn, num_groups);
+}
+
+int bsfp8_grouped_gemm_swiglu_grad(const uint8_t* dy_row_q, const uint8_t* dy_row_s, int64_t capacity_rows,
+                                   int64_t hidden, const uint8_t* w_col_q, const uint8_t* w_col_s, int64_t ffn,
+                                   const void* ab, const float* probs, const int32_t* split_sizes,
+                                   int32_t num_groups, int recipe, void* dab, int which, uint8_t* row_q,
+                                   uint8_t* row_s, uint8_t* col_q, uint8_t* col_s, float* dprobs, void* workspace,
+                                   uint32_t* status, void* stream) {
+  int rc = check_glu_shape(capacity_rows, hidden, ffn, num_groups, recipe, which);
+  if (rc != BSFP8_OK) return rc;
+  if (capacity_rows == 0) return BSFP8_OK;
+  if (dab == nullptr && which == 0 && dprobs == nullptr) return BSFP8_ERR_ARGUMENT;
+  if (dy_row_q == nullptr || dy_row_s == nullptr || w_col_q == nullptr || w_col_s == nullptr || ab == nullptr ||
+      split_sizes == nullptr)
+    return BSFP8_ERR_NULL_POINTER;
+  if (dprobs != nullptr && workspace == nullptr &&
+      bsfp8::glu_grad_workspace_bytes(capacity_rows, ffn, num_groups) > 0)
+    return BSFP8_ERR_NULL_POINTER;
+  if (!aligned16(dy_row_q) || !aligned16(dy_row_s) || !aligned16(w_col_q) || !aligned16(w_col_s) || !aligned16(ab) ||
+      !aligned4(probs) || !aligned4(split_sizes) || !aligned16(dab) || !aligned4(dprobs) || !aligned16(workspace) ||
+      !aligned4(status))
+    return BSFP8_ERR_ALIGNMENT;
+  rc = check_glu_quantized(which, row_q, row_s, col_q, col_s);
+  if (rc != BSFP8_OK) return rc;
+  const bool row = (which & BSFP8_ROWWISE) != 0, col = (which & BSFP8_COLWISE) != 0;
+  return bsfp8::launch_grouped_gemm_swiglu_grad(
+      dy_row_q, dy_row_s, capacity_rows, hidden, w_col_q, w_col_s, ffn, ab, probs, split_sizes, num_groups, dab,
+      row ? row_q : nullptr, row ? row_s : nullptr, col ? col_q : nullptr, col ? col_s : nullptr, dprobs,
+      (float*)workspace, status, (hipStream_t)stream);
 }
 
 int bsfp8_residual_norm(int64_t rows, int64_t cols, const void* x, int stream_dtype, const void* y,

@@ -278,6 +278,59 @@ int bsfp8_grouped_gemm_dgrad(const uint8_t* dy_row_q, const uint8_t* dy_row_s, i
                              int out_dtype, uint32_t* status, void* stream);
 
 /* ----------------------------------------------------------------------------------------- */
+/* The gated feed-forward projection in one kernel: both projections, the activation, the      */
+/* routing probability and the quantize of the result; and its gradient.  recipe:             */
+/* BSFP8_RECIPE_MX_1X32_E8M0.                                                                 */
+/* ----------------------------------------------------------------------------------------- */
+/*
+ * For the live rows t of expert e, products accumulated in fp32 (operands widened exactly):
+ *     a = x[t] W1_e[0 .. ffn)^T,  b = x[t] W1_e[ffn .. 2 ffn)^T,  y = probs[t] * silu(a) * b
+ * with silu(a) = a / (1 + exp(-a)) in fp32, from the unrounded a and b.
+ * x_row_q, x_row_s  rowwise output of bsfp8_grouped_quantize for x [capacity_rows][hidden]
+ * w_q, w_s          rowwise output for W1 [num_groups * 2 ffn][hidden] (split_sizes NULL): expert e's
+ *                   a rows, then its b rows
+ * probs             fp32 [capacity_rows], or NULL (1)
+ * ab                bf16 [capacity_rows][2 ffn], (a | b) kept for the gradient, or NULL
+ * y                 [capacity_rows][ffn] of y_dtype (BSFP8_OUT_F32 or BSFP8_OUT_BF16), or NULL
+ * which, row_q, row_s, col_q, col_s   y quantized from its fp32 values, laid out as
+ *                   bsfp8_grouped_quantize does for [capacity_rows][ffn]; which == 0: none
+ * At least one of ab, y and the quantized layouts is asked for.  Rows at or past sum(k_e) are not
+ * written.  hidden and ffn are multiples of 32, hidden below 2^24 - 128, ffn at most 2^20.
+ * capacity_rows == 0 returns BSFP8_OK without touching any pointer.
+ */
+int bsfp8_grouped_gemm_swiglu(const uint8_t* x_row_q, const uint8_t* x_row_s, int64_t capacity_rows,
+                              int64_t hidden, const uint8_t* w_q, const uint8_t* w_s, int64_t ffn,
+                              const float* probs, const int32_t* split_sizes, int32_t num_groups,
+                              int recipe, void* ab, void* y, int y_dtype, int which, uint8_t* row_q,
+                              uint8_t* row_s, uint8_t* col_q, uint8_t* col_s, uint32_t* status,
+                              void* stream);
+
+/*
+ * Its gradient, through the second projection: with dh = dy[t] W2_e (fp32), sg = 1 / (1 + exp(-a)),
+ *     da = dh * probs * b * sg * (1 + a * (1 - sg))      db = dh * probs * a * sg
+ *     dprobs[t] = sum over the ffn channels of dh * a * sg * b
+ * dy_row_q, dy_row_s  rowwise output of bsfp8_grouped_quantize for dy [capacity_rows][hidden]
+ * w_col_q, w_col_s    W2 viewed as [num_groups * hidden][ffn], colwise with split sizes hidden, ...,
+ *                     as bsfp8_grouped_gemm_dgrad takes it
+ * ab                  as the forward kept it
+ * dab                 bf16 [capacity_rows][2 ffn], (da | db), or NULL
+ * which, row_q, ...   (da | db) quantized from its fp32 values, for [capacity_rows][2 ffn]
+ * dprobs              fp32 [capacity_rows] or NULL; the parts of the tile columns are summed in order
+ * workspace           bsfp8_grouped_gemm_swiglu_grad_workspace_bytes() bytes of device memory, needed
+ *                     with dprobs (0 bytes: may be NULL)
+ * At least one of dab, the quantized layouts and dprobs is asked for.
+ */
+size_t bsfp8_grouped_gemm_swiglu_grad_workspace_bytes(int64_t capacity_rows, int64_t ffn,
+                                                      int32_t num_groups);
+int bsfp8_grouped_gemm_swiglu_grad(const uint8_t* dy_row_q, const uint8_t* dy_row_s,
+                                   int64_t capacity_rows, int64_t hidden, const uint8_t* w_col_q,
+                                   const uint8_t* w_col_s, int64_t ffn, const void* ab,
+                                   const float* probs, const int32_t* split_sizes, int32_t num_groups,
+                                   int recipe, void* dab, int which, uint8_t* row_q, uint8_t* row_s,
+                                   uint8_t* col_q, uint8_t* col_s, float* dprobs, void* workspace,
+                                   uint32_t* status, void* stream);
+
+/* ----------------------------------------------------------------------------------------- */
 /* Norms before and after a block, fused with the block's gate and the residual sum.          */
 /* ----------------------------------------------------------------------------------------- */
 
