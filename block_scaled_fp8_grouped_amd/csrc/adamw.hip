@@ -6,7 +6,7 @@
 // kAdamChunk elements, so tensors of one element and of billions share a launch and a workgroup
 // finds its work with two loads.
 //
-// 8-bit states: m and u = sqrt(v) as e4m3, one fp32 scale (largest magnitude / 448) per 128
+// 8-bit states: m and u = sqrt(v) as e4m3, one fp32 scale (largest magnitude times 1/448) per 128
 // consecutive elements of a tensor.  u instead of v: v spans the square of the gradients' range,
 // u's codes keep 2^17 of it with 4 significant bits each, and u is what the update divides by.  A
 // scale in fp32 rather than a power of two: the block's largest state is then always the code 448
@@ -94,7 +94,7 @@ __device__ __forceinline__ float block_scale(const float* v) {
   for (int i = 0; i < 4; ++i) m = fmaxf(m, fabsf(v[i]));
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
-  return fmaxf(m / 448.0f, 1e-30f);
+  return fmaxf(m * (1.0f / 448.0f), 1e-30f);
 }
 
 template <class PT, class GT, bool Q8>

@@ -65,11 +65,11 @@ __device__ __forceinline__ v8bf glu_widen8(int d0, int d1, float scale) {
   return v8bf{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
-constexpr int kGluBM = 256, kGluBN = 256;
-
-template <bool GRAD>
+template <bool GRAD, int TILE>
 struct GluShape {
-  static constexpr int BM = kGluBM, BN = kGluBN, BK = 128, WM = 128, WN = 64, NW = 8, NT = 512;
+  static_assert(TILE == 256 || TILE == 128, "tile");
+  static constexpr int BM = TILE, BN = TILE, BK = 128, WM = TILE / 2, WN = 64;
+  static constexpr int WAVES_N = BN / WN, NW = 2 * WAVES_N, NT = 64 * NW;
   static constexpr int FM = WM / 32, FN = WN / 32;
   static constexpr int COLS = GRAD ? BN : BN / 2;  // output columns (of one half) per tile
   static constexpr int B_OFF = BM * BK, SA_OFF = (BM + BN) * BK, SB_OFF = SA_OFF + 16 * BM;
@@ -79,17 +79,19 @@ struct GluShape {
   // half-waves) by half of the 64 banks
   static constexpr int PITCH = GRAD ? 72 : 40;
   static constexpr int EP = 32 * PITCH * 4;
-  static constexpr int SMEM = 2 * STAGE > NW * EP + 4 * BM * 4 ? 2 * STAGE : NW * EP + 4 * BM * 4;
-  static_assert(SMEM + BM * 4 + (int)sizeof(GroupScanSmem<NT>) <= 160 * 1024, "LDS budget");
+  static_assert(NW * EP + WAVES_N * BM * 4 <= 2 * STAGE, "the epilogue fits in the stages");
+  static_assert(NT == 2 * TILE, "launch bounds");
+  static_assert(B_INS == 4, "a wave fetches 32 rows of the weight");
+  static_assert((2 * STAGE + BM * 4 + (int)sizeof(GroupScanSmem<NT>)) * (256 / TILE) <= 160 * 1024, "LDS budget");
 };
 
-template <bool GRAD, bool KTAIL>
-__global__ __launch_bounds__(512) void glu_gemm_kernel(GluArgs args) {
-  using S = GluShape<GRAD>;
-  constexpr int BM = S::BM, BN = S::BN, BK = S::BK, NT = S::NT, FM = S::FM, FN = S::FN;
+template <bool GRAD, bool KTAIL, int TILE>
+__global__ __launch_bounds__(2 * TILE) void glu_gemm_kernel(GluArgs args) {
+  using S = GluShape<GRAD, TILE>;
+  constexpr int BM = S::BM, BN = S::BN, BK = S::BK, NT = S::NT, NW = S::NW, FM = S::FM, FN = S::FN;
   __shared__ GroupScanSmem<NT> gsm;
   __shared__ float probs[BM];
-  __shared__ __attribute__((aligned(16))) uint8_t smem[S::SMEM];
+  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * S::STAGE];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -129,17 +131,19 @@ __global__ __launch_bounds__(512) void glu_gemm_kernel(GluArgs args) {
 #pragma unroll
   for (int u = 0; u < S::B_INS; ++u)
     b_off[u] = tile_dma_voffset(wave * S::B_INS + u, lane, (uint32_t)args.b_ld, 0) - b_shift * (uint32_t)args.b_ld;
-  // scales: threads of waves 2 b, 2 b + 1 take block b's A bytes (two rows each; a group's rows begin
-  // anywhere), waves 4 + b its B bytes (4 LDS rows per lane, which lie in one run of 32 columns)
-  const int sa_blk = wave >> 1, sa_row = 2 * ((wave & 1) * 64 + lane);
+  // scales: the waves share the 4 blocks' A bytes, two rows per lane (a group's rows begin anywhere);
+  // the last BN / 64 waves take the B bytes, 4 LDS rows per lane, which lie in one run of 32 columns
+  const int sa_blk = wave / (NW / 4), sa_row = 2 * ((wave % (NW / 4)) * 64 + lane);
   const uint8_t* a_sc = args.a_s + gi.off + row0;
+  constexpr int kFirstB = NW - BN / 64;
+  const int sb_word = (wave - kFirstB) * 64 + lane, sb_blk = sb_word / (BN / 4), sb_at = sb_word % (BN / 4);
   int sb_row;  // this lane's first B scale: column of its projection, pulled back to a live one
   int64_t sb_half = 0;
   if constexpr (GRAD) {
-    sb_row = scale_dma_row(0, lane, b_last);
+    sb_row = scale_dma_row(0, sb_at, b_last);
   } else {
-    sb_row = scale_dma_row(0, (lane >> 4) * 8 + (lane & 7), b_last);
-    sb_half = ((lane >> 3) & 1) * F;
+    sb_row = scale_dma_row(0, (sb_at >> 4) * 8 + (sb_at & 7), b_last);
+    sb_half = ((sb_at >> 3) & 1) * F;
   }
   const uint8_t* b_sc = args.b_s + gi.e * args.bs_estride + sb_half + col0 + sb_row;
   uint8_t sa[2];
@@ -158,8 +162,8 @@ __global__ __launch_bounds__(512) void glu_gemm_kernel(GluArgs args) {
       } else {
         sa[0] = sa[1] = 0x7f;  // past K: unit scales over zero data
       }
-      if (wave >= 4) {
-        const int64_t bb = (int64_t)kk * 4 + (wave - 4);
+      if (wave >= kFirstB) {
+        const int64_t bb = (int64_t)kk * 4 + sb_blk;
         sb = !KTAIL || bb * 32 < K ? *(const uint32_t*)(b_sc + bb * args.bs_bstride) : 0x7f7f7f7fu;
       }
     }
@@ -178,8 +182,8 @@ __global__ __launch_bounds__(512) void glu_gemm_kernel(GluArgs args) {
     float* fa = (float*)(base + S::SA_OFF) + sa_blk * BM + sa_row;
     fa[0] = glu_e8m0(sa[0]);
     fa[1] = glu_e8m0(sa[1]);
-    if (wave >= 4)
-      *(v4f*)((float*)(base + S::SB_OFF) + (wave - 4) * BN + 4 * lane) =
+    if (wave >= kFirstB)
+      *(v4f*)((float*)(base + S::SB_OFF) + 4 * sb_word) =
           v4f{glu_e8m0(sb & 0xffu), glu_e8m0((sb >> 8) & 0xffu), glu_e8m0((sb >> 16) & 0xffu), glu_e8m0(sb >> 24)};
   };
   auto wait_dma = [&]() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); };
@@ -381,7 +385,225 @@ __global__ __launch_bounds__(512) void glu_gemm_kernel(GluArgs args) {
     if (args.dpart != nullptr) {
       __syncthreads();
       const float* s = (const float*)(smem + S::NW * S::EP);
-      if (tid <= a_last) args.dpart[(int64_t)tn * args.R + gi.off + row0 + tid] = ((s[tid] + s[BM + tid]) + s[2 * BM + tid]) + s[3 * BM + tid];
+      if (tid <= a_last) {
+        float d = s[tid];
+#pragma unroll
+        for (int w = 1; w < S::WAVES_N; ++w) d += s[w * BM + tid];
+        args.dpart[(int64_t)tn * args.R + gi.off + row0 + tid] = d;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// Few rows per expert (serving)
+// ------------------------------------------------------------------------------------------
+//
+// Bound by HBM: every live expert's weight is read once for a handful of rows, so what counts is the
+// bytes in flight.  Tile: 32 tokens x 64 weight rows (forward: 32 of each projection).  The 4 waves of
+// a workgroup share the K extent, wave w taking the steps w, w + 4, ..., and their sums are added in
+// order at the end: no barrier and no LDS until then, each wave keeps two steps of weights (16 KB) in
+// flight in registers.  16 x 16 x 32 MFMAs; lane (row, q) of a fragment loads the whole scale block q of
+// its row (two 16-byte loads), so it needs one scale byte per step.  The order of K within an MFMA is
+// that of the lanes, the same for both operands.
+constexpr int kRowsBM = 32, kRowsBN = 64, kRowsNW = 4, kRowsPitch = 68;
+
+template <bool GRAD>
+__global__ __launch_bounds__(256) void glu_rows_kernel(GluArgs args) {
+  constexpr int BM = kRowsBM, BN = kRowsBN, NW = kRowsNW, NT = 64 * NW, P = kRowsPitch;
+  constexpr int COLS = GRAD ? BN : BN / 2;
+  __shared__ GroupScanSmem<NT> gsm;
+  __shared__ __attribute__((aligned(16))) float part[NW][BM][P];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int q = lane >> 4, l16 = lane & 15;
+  const int64_t L = xcd_logical(blockIdx.x);
+  if (L >= args.tiles) return;
+  int64_t mt;
+  int tn;
+  fprop_tile(L, args.tiles_n, &mt, &tn);
+  GroupInfo gi;
+  const uint32_t flags = group_scan<NT>(args.splits, args.E, args.R, BM, mt, 0, gsm, gi);
+  report_status(args.status, flags);
+  if (gi.e < 0) return;
+  const int64_t row0 = (mt - gi.tile) * BM, col0 = (int64_t)tn * COLS;
+  const int64_t F = args.F, K = args.K;
+  const int a_last = (int)(gi.k - row0 < BM ? gi.k - row0 : BM) - 1;
+  const int b_last = (int)(F - col0 < COLS ? F - col0 : COLS) - 1;
+
+  // fragments: tokens 16 i + l16; weight rows 16 j + l16 of the tile's 64 (forward: j < 2 of a, j >= 2 of b)
+  const __amdgpu_buffer_rsrc_t a_rs = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(args.a_q + (gi.off + row0) * K), (short)0, (int)((a_last + 1) * K), 0x00020000);
+  const uint8_t* b_base = args.b_q + gi.e * args.b_estride + col0 * args.b_ld;
+  const uint32_t b_bytes = (uint32_t)((GRAD ? b_last + 1 : 32) * args.b_ld);
+  __amdgpu_buffer_rsrc_t b_rs[2];
+  b_rs[0] = __builtin_amdgcn_make_buffer_rsrc((void*)b_base, (short)0, (int)b_bytes, 0x00020000);
+  b_rs[1] = GRAD ? b_rs[0]
+                 : __builtin_amdgcn_make_buffer_rsrc((void*)(b_base + F * args.b_ld), (short)0, (int)b_bytes, 0x00020000);
+  uint32_t a_off[2], b_off[4];
+  const uint8_t *a_sc[2], *b_sc[4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = 16 * i + l16;
+    a_off[i] = (uint32_t)r * (uint32_t)K + 32 * q;
+    a_sc[i] = args.a_s + gi.off + row0 + (r < a_last ? r : a_last);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = 16 * (GRAD ? j : j & 1) + l16;
+    b_off[j] = (uint32_t)r * (uint32_t)args.b_ld + 32 * q;
+    b_sc[j] = args.b_s + gi.e * args.bs_estride + (GRAD ? 0 : (j >> 1) * F) + col0 + (r < b_last ? r : b_last);
+  }
+  const int nblk = (int)(K / 32), nk = (nblk + 3) / 4;
+
+  struct Frag {
+    v4i a[2][2], b[4][2];
+    uint8_t as[2], bs[4];
+  };
+  auto load = [&](Frag& f, int kk) {
+    const int kb = 4 * kk + q, kc = kb < nblk ? kb : nblk - 1;
+    // a block past K reads as zeros (an offset past every resource's range) under a live scale
+    const uint32_t k0 = kb < nblk ? (uint32_t)kk * 128u : 0x80000000u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f.b[j][0] = __builtin_amdgcn_raw_buffer_load_b128(b_rs[GRAD ? 0 : j >> 1], (int)(b_off[j] + k0), 0, 0);
+      f.b[j][1] = __builtin_amdgcn_raw_buffer_load_b128(b_rs[GRAD ? 0 : j >> 1], (int)(b_off[j] + k0 + 16), 0, 0);
+      f.bs[j] = b_sc[j][kc * args.bs_bstride];
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f.a[i][0] = __builtin_amdgcn_raw_buffer_load_b128(a_rs, (int)(a_off[i] + k0), 0, 0);
+      f.a[i][1] = __builtin_amdgcn_raw_buffer_load_b128(a_rs, (int)(a_off[i] + k0 + 16), 0, 0);
+      f.as[i] = a_sc[i][kc * args.R];
+    }
+  };
+  v4f acc[2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0, 0, 0, 0};
+  auto multiply = [&](const Frag& f) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      v8bf aw[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        aw[i] = glu_widen8(f.a[i][t >> 1][2 * (t & 1)], f.a[i][t >> 1][2 * (t & 1) + 1], glu_e8m0(f.as[i]));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const v8bf bw = glu_widen8(f.b[j][t >> 1][2 * (t & 1)], f.b[j][t >> 1][2 * (t & 1) + 1], glu_e8m0(f.bs[j]));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(aw[i], bw, acc[i][j], 0, 0, 0);
+      }
+    }
+  };
+  // three buffers: two steps' loads are in flight while one is multiplied (steps past the end load zeros)
+  Frag f0, f1, f2;
+  const int steps = (nk - wave + NW - 1) / NW;  // of this wave; may be 0
+  load(f0, wave);
+  load(f1, wave + NW);
+  for (int s = 0; s < steps; s += 3) {
+    load(f2, wave + NW * (s + 2));
+    multiply(f0);
+    load(f0, wave + NW * (s + 3));
+    multiply(f1);
+    load(f1, wave + NW * (s + 4));
+    multiply(f2);
+  }
+
+  // register r of fragment (i, j): token 16 i + 4 q + r, weight row 16 j + l16
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) part[wave][16 * i + 4 * q + r][16 * j + l16] = acc[i][j][r];
+  __syncthreads();
+  const int row = tid >> 3, ch = 8 * (tid & 7);  // 8 of the tile's 64 sums per thread
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = part[0][row][ch + k];
+#pragma unroll
+  for (int w = 1; w < NW; ++w)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] += part[w][row][ch + k];
+  const int64_t at = gi.off + row0 + row;
+  const bool live_row = row <= a_last;
+  const float p = !live_row ? 0.0f : args.probs != nullptr ? args.probs[at] : 1.0f;
+  if constexpr (!GRAD) {
+    // lanes 0 .. 3 of a row hold a, 4 .. 7 b
+    if (args.ab != nullptr && live_row) {
+      v8s w;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = (short)f32_to_bf16(v[k]);
+      *(v8s*)(args.ab + at * 2 * F + (ch < 32 ? 0 : F - 32) + col0 + ch) = w;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float b = __shfl_xor(v[k], 4, 64);
+      v[k] = live_row ? swiglu(v[k], b, p) : 0.0f;  // in the lanes that hold a
+    }
+    put_row8(args.out, args.R, F, at, col0 + ch, live_row && ch < 32, v);
+    if (args.out.col_q != nullptr) {
+      __syncthreads();  // every thread has read its sums
+      if (ch < 32)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) part[0][row][ch + k] = v[k];
+      __syncthreads();
+      if (wave == 0) {
+        float c[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) c[k] = part[0][k][lane & 31];
+        put_col32(args.out, F, gi, row0, col0 + lane, lane < 32, c);
+      }
+    }
+  } else {
+    v8s av = {0, 0, 0, 0, 0, 0, 0, 0}, bv = av;
+    const bool live = live_row && ch <= b_last;
+    if (live) {
+      const uint16_t* ab = args.ab + at * 2 * F + col0 + ch;
+      av = *(const v8s*)ab;
+      bv = *(const v8s*)(ab + F);
+    }
+    float da[8], db[8], dp = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) swiglu_grad(to_f32(av[k]), to_f32(bv[k]), p, live ? v[k] : 0.0f, da[k], db[k], dp);
+    put_row8(args.out, args.R, 2 * F, at, col0 + ch, live, da);
+    put_row8(args.out, args.R, 2 * F, at, F + col0 + ch, live, db);
+    dp += __shfl_xor(dp, 1, 64);
+    dp += __shfl_xor(dp, 2, 64);
+    dp += __shfl_xor(dp, 4, 64);
+    if (args.dpart != nullptr && (lane & 7) == 0 && live_row) args.dpart[(int64_t)tn * args.R + at] = dp;
+    if (args.out.col_q != nullptr) {
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        part[0][row][ch + k] = da[k];
+        part[1][row][ch + k] = db[k];
+      }
+      __syncthreads();
+      if (wave < 2) {
+        float c[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) c[k] = part[wave][k][lane];
+        put_col32(args.out, 2 * F, gi, row0, wave * F + col0 + lane, lane <= b_last, c);
+      }
+    }
+  }
+  // the group's last tile also writes the pad lanes of the 32-row blocks that have no tile
+  if (args.out.col_q != nullptr && row0 + BM >= gi.k) {
+    constexpr int HALVES = GRAD ? 2 : 1;
+    const int64_t N = HALVES * F;
+    const int64_t first = row0 + BM, blocks = (gi.kp - first) / 32;  // at most 3
+    for (int64_t x = tid; x < blocks * HALVES * COLS; x += NT) {
+      const int c = (int)(x % COLS), half = (int)(x / COLS % HALVES);
+      const int64_t t = first + 32 * (x / (COLS * HALVES)), col = half * F + col0 + c;
+      if (c > b_last) continue;
+      uint8_t* dst = args.out.col_q + col_elem(N, gi.p, gi.kp, col, t);
+      *(v4i*)dst = v4i{0, 0, 0, 0};
+      *(v4i*)(dst + 16) = v4i{0, 0, 0, 0};
+      args.out.col_s[col_e8m0(N, gi.p, t / 32, col)] = 0;
     }
   }
 }
@@ -404,26 +626,57 @@ __global__ __launch_bounds__(256) void glu_dprobs_kernel(const float* __restrict
 // Launchers
 // ------------------------------------------------------------------------------------------
 
-static int64_t glu_tiles_n(bool grad, int64_t F) {
-  const int64_t c = grad ? GluShape<true>::COLS : GluShape<false>::COLS;
+// Tile of a launch.  Up to 32 rows per expert on average take the few-rows kernel (kRowsTile); the others
+// 256 x 256 tiles unless that leaves much of the chip idle.  Groups end half a tile early on average, hence
+// R / 256 + E / 2 rows of tiles.
+constexpr int kRowsTile = 32;
+constexpr int64_t kSmallGluTiles = 512;
+
+static int glu_tile(bool grad, int64_t R, int64_t F, int E) {
+  if (R <= (int64_t)kRowsTile * E) return kRowsTile;
+  const int64_t cols = grad ? 256 : 128;
+  return (R / 256 + (E + 1) / 2) * ((F + cols - 1) / cols) < kSmallGluTiles ? 128 : 256;
+}
+
+// Columns of one half per tile, and the tiles of a row of them.
+static int64_t glu_tiles_n(bool grad, int tile, int64_t F) {
+  const int64_t w = tile == kRowsTile ? kRowsBN : tile, c = grad ? w : w / 2;
   return (F + c - 1) / c;
 }
 
-size_t glu_grad_workspace_bytes(int64_t R, int64_t F, int) {
-  const int64_t n = glu_tiles_n(true, F);
+size_t glu_grad_workspace_bytes(int64_t R, int64_t F, int E) {
+  const int64_t n = glu_tiles_n(true, glu_tile(true, R, F, E), F);
   return n > 1 ? (size_t)(n * R * 4) : 0;
+}
+
+// The grid of a launch: rows of tiles that any valid sizes can need (at most one per row), in whole runs.
+static int glu_grid(GluArgs& a, bool grad, int tile, dim3* grid) {
+  a.tiles_n = (int)glu_tiles_n(grad, tile, a.F);
+  const int64_t gm = fprop_run_mtiles(a.tiles_n);
+  int64_t mt = (a.R + (int64_t)(tile - 1) * a.E) / tile;
+  if (mt > a.R) mt = a.R;
+  a.tiles = (mt + gm - 1) / gm * gm * a.tiles_n;
+  if (xcd_launch_size(a.tiles) > 0x7fffffff) return BSFP8_ERR_SHAPE;
+  *grid = dim3((unsigned)xcd_launch_size(a.tiles));
+  return BSFP8_OK;
 }
 
 template <bool GRAD>
 static int launch_glu(GluArgs& a, hipStream_t stream) {
-  a.tiles_n = (int)glu_tiles_n(GRAD, a.F);
-  const int64_t gm = fprop_run_mtiles(a.tiles_n);
-  const int64_t mt = (a.R + (int64_t)(kGluBM - 1) * a.E) / kGluBM;
-  a.tiles = (mt + gm - 1) / gm * gm * a.tiles_n;
-  if (xcd_launch_size(a.tiles) > 0x7fffffff) return BSFP8_ERR_SHAPE;
-  const dim3 grid((unsigned)xcd_launch_size(a.tiles)), block(512);
-  if (a.K % 128 != 0) hipLaunchKernelGGL((glu_gemm_kernel<GRAD, true>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((glu_gemm_kernel<GRAD, false>), grid, block, 0, stream, a);
+  const int tile = glu_tile(GRAD, a.R, a.F, a.E);
+  const bool tail = a.K % 128 != 0;
+  dim3 grid;
+  const int rc = glu_grid(a, GRAD, tile, &grid);
+  if (rc != BSFP8_OK) return rc;
+  if (tile == kRowsTile) {
+    hipLaunchKernelGGL((glu_rows_kernel<GRAD>), grid, dim3(64 * kRowsNW), 0, stream, a);
+  } else if (tile == 128) {
+    if (tail) hipLaunchKernelGGL((glu_gemm_kernel<GRAD, true, 128>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((glu_gemm_kernel<GRAD, false, 128>), grid, dim3(256), 0, stream, a);
+  } else {
+    if (tail) hipLaunchKernelGGL((glu_gemm_kernel<GRAD, true, 256>), grid, dim3(512), 0, stream, a);
+    else hipLaunchKernelGGL((glu_gemm_kernel<GRAD, false, 256>), grid, dim3(512), 0, stream, a);
+  }
   return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
 }
 
@@ -476,12 +729,12 @@ int launch_grouped_gemm_swiglu_grad(const uint8_t* dy_q, const uint8_t* dy_s, in
   a.ab = (uint16_t*)const_cast<void*>(ab);
   a.out = GluOut{dab, 0, row_q, row_s, col_q, col_s};
   a.status = status;
-  const bool parts = dprobs != nullptr && glu_tiles_n(true, F) > 1;
+  const bool parts = dprobs != nullptr && glu_tiles_n(true, glu_tile(true, R, F, E), F) > 1;
   a.dpart = parts ? workspace : dprobs;
   const int rc = launch_glu<true>(a, stream);
   if (rc != BSFP8_OK || !parts) return rc;
   hipLaunchKernelGGL(glu_dprobs_kernel, dim3((unsigned)((R + 255) / 256)), dim3(256), 0, stream, workspace,
-                     (int)glu_tiles_n(true, F), R, splits, E, dprobs);
+                     a.tiles_n, R, splits, E, dprobs);
   return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
 }
 

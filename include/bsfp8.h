@@ -407,7 +407,7 @@ int bsfp8_residual_norm_grad(int64_t rows, int64_t cols, int stream_dtype, const
  *                                         * (lr / (1 - beta1^step))
  * BSFP8_STATE_F32: m and v are fp32 arrays.
  * BSFP8_STATE_8BIT: m and u = sqrt(v) are e4m3 arrays; every 128 consecutive elements of a tensor
- *   (the last block may be shorter) share one fp32 scale sf = max(amax / 448, 1e-30), a code
+ *   (the last block may be shorter) share one fp32 scale sf = max(amax * (1/448), 1e-30), a code
  *   standing for code * sf.  New states are stored as e4m3(m * (1 / sf)); p uses them unrounded.
  *   Zeroed codes and scales are a valid start.
  * Non-finite gradients enter the states; noop_flag is for skipping such a step.
