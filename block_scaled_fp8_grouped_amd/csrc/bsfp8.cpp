@@ -100,13 +100,15 @@ int check_glu_quantized(int which, const void* row_q, const void* row_s, const v
   if ((which & BSFP8_COLWISE) && (!aligned16(col_q) || !aligned16(col_s))) return BSFP8_ERR_ALIGNMENT;
   return BSFP8_OK;
 }
+// the gated projections' loads mark offsets past a 256-row tile by 2^31
+constexpr int64_t kMaxGluHidden = int64_t(1) << 22;
 // what both directions of a gated projection need of their sizes
 int check_glu_shape(int64_t capacity_rows, int64_t hidden, int64_t ffn, int32_t num_groups, int recipe, int which) {
   if (!valid_recipe(recipe & ~BSFP8_GEMM_FP8_MFMA)) return BSFP8_ERR_RECIPE;
   if (recipe != BSFP8_RECIPE_MX_1X32_E8M0) return BSFP8_ERR_LAYOUT;
   if (!valid_groups(num_groups)) return BSFP8_ERR_NUM_GROUPS;
   if (!valid_dim(hidden) || !valid_dim(ffn) || capacity_rows < 0 || capacity_rows > (int64_t(1) << 31) ||
-      hidden + 127 > kMaxKExtent || 2 * ffn > kMaxOutCols)
+      hidden > kMaxGluHidden || 2 * ffn > kMaxOutCols)
     return BSFP8_ERR_SHAPE;
   if ((which & ~(BSFP8_ROWWISE | BSFP8_COLWISE)) != 0) return BSFP8_ERR_ARGUMENT;
   return BSFP8_OK;

@@ -24,6 +24,8 @@
 // One workgroup per tile, fixed order, no atomics: the same bits every time.  Rows past a group's
 // live rows read as zeros and are not stored; the colwise pad lanes get the zeros that those rows
 // compute.
+#include <type_traits>
+
 #include "glu_epilogue.hpp"
 #include "tile_addr.hpp"
 #include "tile_sched.hpp"
@@ -49,12 +51,31 @@ struct GluArgs {
   uint32_t* status;
 };
 
-__device__ __forceinline__ void glu_dma16(__amdgpu_buffer_rsrc_t rs, uint8_t* lds, uint32_t voff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)lds, 16, voff, 0, 0, 0);
+// The LDS DMAs are issued in assembly and waited for by count (glu_wait): issued through the builtins, the
+// compiler cannot tell a DMA into one stage from the reads of another and waits for all of them.
+// 16 bytes per lane to LDS address lds + 16 * lane; a lane whose offset lies past the resource's range
+// stores zeros.  M0 holds the wave-uniform LDS address (one wait state before its use).
+__device__ __forceinline__ void glu_dma16(v4i rsrc, uint32_t lds, uint32_t voff) {
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(voff), "s"(rsrc), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ void glu_dma16(const void* g, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(g), "{m0}"(lds) : "memory");
+}
+// Words of a raw buffer resource over `bytes` bytes at `base` (wave-uniform).
+__device__ __forceinline__ v4i glu_rsrc(const void* base, uint32_t bytes) {
+  const uint64_t a = (uint64_t)(uintptr_t)base;
+  return v4i{__builtin_amdgcn_readfirstlane((int)(uint32_t)a), __builtin_amdgcn_readfirstlane((int)((a >> 32) & 0xffff)),
+             __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+}
+// All of this wave's DMAs but the newest N have landed and its LDS reads have returned; then the barrier.
+template <int N>
+__device__ __forceinline__ void glu_wait_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
 }
 
-// fp32 value 2^(byte - 127) of an E8M0 byte (byte 0: the subnormal 2^-127).
-__device__ __forceinline__ float glu_e8m0(uint32_t byte) { return __uint_as_float(max(byte << 23, 0x00400000u)); }
+// An E8M0 byte as the scale operand of the widening conversions, which use its exponent field alone (0 stands
+// for 2^-127 there too: checked on the GPU for every byte and code).
+__device__ __forceinline__ float glu_e8m0(uint32_t byte) { return __uint_as_float(byte << 23); }
 
 // Eight e4m3 codes -> eight bf16 values times `scale` (exact).
 __device__ __forceinline__ v8bf glu_widen8(int d0, int d1, float scale) {
@@ -65,33 +86,51 @@ __device__ __forceinline__ v8bf glu_widen8(int d0, int d1, float scale) {
   return v8bf{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
-template <bool GRAD, int TILE>
+// Chunk c (16 bytes) of an LDS row of BK bytes sits at c ^ glu_swz(r): the 16 lanes that a 16-byte LDS read
+// serves at once (0-3, 12-15, 20-27 and the rest of each 32) see every bank once.
+template <int BK>
+__device__ __forceinline__ int glu_swz(int row) {
+  return BK == 128 ? swz(row) : (row >> 2) & 3;
+}
+// Source offset of DMA lane `lane` of the 1 KB of LDS rows that begin at `row0`: row-major rows of ld bytes.
+template <int BK>
+__device__ __forceinline__ uint32_t glu_dma_offset(int row0, int lane, uint32_t ld) {
+  constexpr int C = BK / 16;
+  const int row = row0 + lane / C;
+  return (uint32_t)row * ld + 16u * (uint32_t)((lane % C) ^ glu_swz<BK>(row));
+}
+
+// Tiles of BM x BN, K steps of BK bytes, waves of BM / 2 x 64, NS stages of LDS.
+template <bool GRAD, int BM_, int BN_, int BK_, int NS_>
 struct GluShape {
-  static_assert(TILE == 256 || TILE == 128, "tile");
-  static constexpr int BM = TILE, BN = TILE, BK = 128, WM = TILE / 2, WN = 64;
+  static constexpr int BM = BM_, BN = BN_, BK = BK_, NS = NS_, WM = BM / 2, WN = 64, BLKS = BK / 32;
   static constexpr int WAVES_N = BN / WN, NW = 2 * WAVES_N, NT = 64 * NW;
   static constexpr int FM = WM / 32, FN = WN / 32;
   static constexpr int COLS = GRAD ? BN : BN / 2;  // output columns (of one half) per tile
-  static constexpr int B_OFF = BM * BK, SA_OFF = (BM + BN) * BK, SB_OFF = SA_OFF + 16 * BM;
-  static constexpr int STAGE = SB_OFF + 16 * BN;
-  static constexpr int A_INS = BM / 8 / NW, B_INS = BN / 8 / NW;
+  // a stage: A rows, B rows, then the E8M0 bytes as the scale DMAs leave them: AL lanes of 16 bytes per block
+  // of A (from the 16-byte boundary before its first row), then BL per block of B
+  static constexpr int AL = BM / 16 + 1, BL = BN / 16;
+  static constexpr int SC_INS = (BLKS * (AL + BL) + 63) / 64;  // scale DMAs per step; wave w < SC_INS issues one
+  static constexpr int B_OFF = BM * BK, SC_OFF = (BM + BN) * BK, STAGE = SC_OFF + SC_INS * 1024;
+  static constexpr int SB_OFF = SC_OFF + BLKS * AL * 16;
+  static constexpr int A_INS = BM * BK / 1024 / NW, B_INS = BN * BK / 1024 / NW;
   // epilogue: each wave's 32 rows of fp32, the row pitch shifting the rows 4 apart (one register's two
   // half-waves) by half of the 64 banks
   static constexpr int PITCH = GRAD ? 72 : 40;
   static constexpr int EP = 32 * PITCH * 4;
-  static_assert(NW * EP + WAVES_N * BM * 4 <= 2 * STAGE, "the epilogue fits in the stages");
-  static_assert(NT == 2 * TILE, "launch bounds");
-  static_assert(B_INS == 4, "a wave fetches 32 rows of the weight");
-  static_assert((2 * STAGE + BM * 4 + (int)sizeof(GroupScanSmem<NT>)) * (256 / TILE) <= 160 * 1024, "LDS budget");
+  static_assert(NT == 2 * BN && NT >= BM, "launch bounds, the probabilities' loads");
+  static_assert(B_INS * 1024 / BK == 32, "a wave fetches 32 rows of the weight");
+  static_assert(SC_INS <= NW, "scale loads");
+  static_assert(NW * EP + (WAVES_N + 1) * BM * 4 <= NS * STAGE && (int)sizeof(GroupScanSmem<NT>) <= NS * STAGE, "LDS reuse");
+  static_assert(NS * STAGE <= 160 * 1024, "LDS budget");
 };
 
-template <bool GRAD, bool KTAIL, int TILE>
-__global__ __launch_bounds__(2 * TILE) void glu_gemm_kernel(GluArgs args) {
-  using S = GluShape<GRAD, TILE>;
-  constexpr int BM = S::BM, BN = S::BN, BK = S::BK, NT = S::NT, NW = S::NW, FM = S::FM, FN = S::FN;
-  __shared__ GroupScanSmem<NT> gsm;
-  __shared__ float probs[BM];
-  __shared__ __attribute__((aligned(16))) uint8_t smem[2 * S::STAGE];
+template <bool GRAD, int BM, int BN, int BK, int NS>
+__global__ __launch_bounds__(2 * BN, BM == 128 ? 3 : 2) void glu_gemm_kernel(GluArgs args) {
+  using S = GluShape<GRAD, BM, BN, BK, NS>;
+  constexpr int NT = S::NT, FM = S::FM, FN = S::FN, BLKS = S::BLKS;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[NS * S::STAGE];
+  GroupScanSmem<NT>& gsm = *(GroupScanSmem<NT>*)smem;  // done before the first DMA (a barrier below)
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -112,8 +151,9 @@ __global__ __launch_bounds__(2 * TILE) void glu_gemm_kernel(GluArgs args) {
   const int64_t F = args.F, K = args.K;
   const int a_last = (int)(gi.k - row0 < BM ? gi.k - row0 : BM) - 1;      // last live tile row
   const int b_last = (int)(F - col0 < S::COLS ? F - col0 : S::COLS) - 1;  // last live column of a half
-  if (tid < BM)
-    probs[tid] = tid > a_last ? 0.0f : args.probs != nullptr ? args.probs[gi.off + row0 + tid] : 1.0f;
+  // this thread's row of the probabilities, to LDS behind the main loop
+  float my_prob = 0.0f;
+  if (tid < BM && tid <= a_last) my_prob = args.probs != nullptr ? args.probs[gi.off + row0 + tid] : 1.0f;
 
   // ---------------- loads of one K step ----------------
   // B: LDS rows 32 w .. of wave w; forward: rows 32 (w / 2) .. of projection w % 2
@@ -121,51 +161,52 @@ __global__ __launch_bounds__(2 * TILE) void glu_gemm_kernel(GluArgs args) {
   const uint32_t b_shift = GRAD ? 0 : (uint32_t)(wave * 32 - (wave >> 1) * 32);  // LDS row minus source row
   const uint8_t* a_base = args.a_q + (gi.off + row0) * K;
   const uint8_t* b_base = args.b_q + gi.e * args.b_estride + (half + col0) * args.b_ld;
-  const __amdgpu_buffer_rsrc_t a_rs =
-      __builtin_amdgcn_make_buffer_rsrc((void*)a_base, (short)0, (int)tile_range(gi.k - row0, K), 0x00020000);
-  const __amdgpu_buffer_rsrc_t b_rs =
-      __builtin_amdgcn_make_buffer_rsrc((void*)b_base, (short)0, (int)tile_range(F - col0, args.b_ld), 0x00020000);
+  // (the live rows of the tile only: below 2^30 bytes, so an offset from 2^31 up is past them)
+  const v4i a_rs = glu_rsrc(a_base, (uint32_t)(a_last + 1) * (uint32_t)K);
+  const v4i b_rs = glu_rsrc(b_base, (uint32_t)(b_last + 1) * (uint32_t)args.b_ld);
+  const uint32_t smem_lds =
+      __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)smem);
   uint32_t a_off[S::A_INS], b_off[S::B_INS];
 #pragma unroll
-  for (int u = 0; u < S::A_INS; ++u) a_off[u] = tile_dma_voffset(wave * S::A_INS + u, lane, (uint32_t)K, 0);
+  for (int u = 0; u < S::A_INS; ++u) a_off[u] = glu_dma_offset<BK>((wave * S::A_INS + u) * (1024 / BK), lane, (uint32_t)K);
 #pragma unroll
   for (int u = 0; u < S::B_INS; ++u)
-    b_off[u] = tile_dma_voffset(wave * S::B_INS + u, lane, (uint32_t)args.b_ld, 0) - b_shift * (uint32_t)args.b_ld;
-  // scales: the waves share the 4 blocks' A bytes, two rows per lane (a group's rows begin anywhere);
-  // the last BN / 64 waves take the B bytes, 4 LDS rows per lane, which lie in one run of 32 columns
-  const int sa_blk = wave / (NW / 4), sa_row = 2 * ((wave % (NW / 4)) * 64 + lane);
+    b_off[u] = glu_dma_offset<BK>((wave * S::B_INS + u) * (1024 / BK), lane, (uint32_t)args.b_ld) -
+               b_shift * (uint32_t)args.b_ld;
+  // Scales, 16 bytes per lane.  A: a group's rows begin anywhere, so the lanes read the aligned 16 bytes that
+  // hold them (the first at or after the buffer's own aligned start, the last the one that holds the last
+  // live row's).  B: 16 LDS rows, which lie in one run of 32 columns.  Lanes with nothing to load repeat a
+  // live address.
+  constexpr int AL = S::AL, BL = S::BL;
+  const int sc_lane = wave * 64 + lane;
+  const bool sc_is_a = sc_lane < BLKS * AL;
+  const int sc_at = sc_is_a ? sc_lane : (sc_lane - BLKS * AL) % (BLKS * BL);
+  const int sc_blk = sc_is_a ? sc_at / AL : sc_at / BL, sc_chunk = sc_is_a ? sc_at % AL : sc_at % BL;
   const uint8_t* a_sc = args.a_s + gi.off + row0;
-  constexpr int kFirstB = NW - BN / 64;
-  const int sb_word = (wave - kFirstB) * 64 + lane, sb_blk = sb_word / (BN / 4), sb_at = sb_word % (BN / 4);
-  int sb_row;  // this lane's first B scale: column of its projection, pulled back to a live one
-  int64_t sb_half = 0;
-  if constexpr (GRAD) {
-    sb_row = scale_dma_row(0, sb_at, b_last);
-  } else {
-    sb_row = scale_dma_row(0, (sb_at >> 4) * 8 + (sb_at & 7), b_last);
-    sb_half = ((sb_at >> 3) & 1) * F;
+  const uint8_t* b_sc;
+  {
+    const int r = GRAD ? 16 * sc_chunk : (sc_chunk >> 2) * 32 + 16 * (sc_chunk & 1);
+    b_sc = args.b_s + gi.e * args.bs_estride + (GRAD ? 0 : ((sc_chunk >> 1) & 1) * F) + col0 +
+           (r <= b_last ? r : b_last & ~15);
   }
-  const uint8_t* b_sc = args.b_s + gi.e * args.bs_estride + sb_half + col0 + sb_row;
-  uint8_t sa[2];
-  uint32_t sb = 0;
-  const int nk = (int)((K + BK - 1) / BK);
-  // parts [p0, p1): 0 the scales, then A_INS + B_INS DMAs
-  auto issue = [&](int kk, uint8_t* base, int p0, int p1) {
-    const uint32_t k0 = (uint32_t)kk * BK;
-    if (p0 == 0) {
-      const int64_t kb = (int64_t)kk * 4 + sa_blk;
-      if (!KTAIL || kb * 32 < K) {
-        const __amdgpu_buffer_rsrc_t rs =
-            __builtin_amdgcn_make_buffer_rsrc((void*)(a_sc + kb * args.R), (short)0, a_last + 1, 0x00020000);
-        sa[0] = __builtin_amdgcn_raw_buffer_load_b8(rs, sa_row, 0, 0);
-        sa[1] = __builtin_amdgcn_raw_buffer_load_b8(rs, sa_row + 1, 0, 0);
+  const int nblk = (int)(K / 32), nk = (int)((K + BK - 1) / BK);
+  // parts [p0, p1): 0 the scales, then A_INS + B_INS DMAs.  A step past the last stores zeros (offsets past
+  // every resource's range, as the host bounds 256 rows by 2^31 bytes), so that the counts stay the same.
+  constexpr int NP = S::A_INS + S::B_INS + 1;
+  auto issue = [&](int kk, int p0, int p1) {
+    const uint32_t k0 = kk < nk ? (uint32_t)kk * BK : 0x80000000u;
+    const uint32_t base = smem_lds + (uint32_t)(kk % NS) * S::STAGE;
+    if (p0 == 0 && wave < S::SC_INS) {
+      const int kb = BLKS * kk + sc_blk, kc = kb < nblk ? kb : nblk - 1;
+      const uint8_t* src;
+      if (sc_is_a) {
+        const uintptr_t first = (uintptr_t)(a_sc + (int64_t)kc * args.R), last = (first + a_last) & ~(uintptr_t)15;
+        const uintptr_t at = (first & ~(uintptr_t)15) + 16 * sc_chunk;
+        src = (const uint8_t*)(at < last ? at : last);
       } else {
-        sa[0] = sa[1] = 0x7f;  // past K: unit scales over zero data
+        src = b_sc + (int64_t)kc * args.bs_bstride;
       }
-      if (wave >= kFirstB) {
-        const int64_t bb = (int64_t)kk * 4 + sb_blk;
-        sb = !KTAIL || bb * 32 < K ? *(const uint32_t*)(b_sc + bb * args.bs_bstride) : 0x7f7f7f7fu;
-      }
+      glu_dma16(src, base + S::SC_OFF + wave * 1024);
     }
 #pragma unroll
     for (int u = 0; u < S::A_INS; ++u) {
@@ -178,15 +219,12 @@ __global__ __launch_bounds__(2 * TILE) void glu_gemm_kernel(GluArgs args) {
       glu_dma16(b_rs, base + S::B_OFF + (wave * S::B_INS + u) * 1024, b_off[u] + k0);
     }
   };
-  auto settle = [&](uint8_t* base) {  // this step's scales to the stage, as fp32
-    float* fa = (float*)(base + S::SA_OFF) + sa_blk * BM + sa_row;
-    fa[0] = glu_e8m0(sa[0]);
-    fa[1] = glu_e8m0(sa[1]);
-    if (wave >= kFirstB)
-      *(v4f*)((float*)(base + S::SB_OFF) + 4 * sb_word) =
-          v4f{glu_e8m0(sb & 0xffu), glu_e8m0((sb >> 8) & 0xffu), glu_e8m0((sb >> 16) & 0xffu), glu_e8m0(sb >> 24)};
+  // waits until all but the newest `steps` steps' loads have landed, in every wave
+  auto wait = [&](auto steps) {
+    constexpr int N = decltype(steps)::value;
+    if (wave < S::SC_INS) glu_wait_barrier<N * NP>();
+    else glu_wait_barrier<N*(NP - 1)>();
   };
-  auto wait_dma = [&]() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); };
 
   v16f acc[FM][FN];
 #pragma unroll
@@ -196,79 +234,82 @@ __global__ __launch_bounds__(2 * TILE) void glu_gemm_kernel(GluArgs args) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-  auto step = [&](bool tail, int kk, const uint8_t* __restrict__ cur, uint8_t* __restrict__ nxt) {
-    const int64_t k0 = (int64_t)kk * BK;
-    auto chunk = [&](const uint8_t* p, int c) {
-      const v4i v = *(const v4i*)p;
-      return !KTAIL || !tail || k0 + 16 * c < K ? v : v4i{0, 0, 0, 0};
-    };
+  // The fragments of one scale block (32 bytes of K) of a step and their scales; two such sets alternate, so
+  // that one block's LDS reads go out beside the MFMAs of the block before.
+  struct Block {
+    v4i a[FM], b[FN];
+    float as[FM], bs[FN];
+  };
+  auto read = [&](Block& q, int kk, int blk) {
+    const uint8_t* cur = smem + (kk % NS) * S::STAGE;
+    // where the block's A scales begin in the stage
+    const int sh = S::SC_OFF + blk * AL * 16 + (int)((uintptr_t)(a_sc + (int64_t)(BLKS * kk + blk) * args.R) & 15);
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      v8i af[FM], bf[FN];
-      float as[FM][2], bs[FN][2];
+    for (int i = 0; i < FM; ++i) {
+      const int row = wm * S::WM + i * 32 + l32;
+      q.a[i] = *(const v4i*)(cur + row * BK + (((2 * blk + h) ^ glu_swz<BK>(row)) << 4));
+      q.as[i] = glu_e8m0(cur[sh + row]);
+    }
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const int row = wm * S::WM + i * 32 + l32;
-        const v4i lo = chunk(cur + row * BK + (((4 * s + h) ^ swz(row)) << 4), 4 * s + h);
-        const v4i hi = chunk(cur + row * BK + (((4 * s + 2 + h) ^ swz(row)) << 4), 4 * s + 2 + h);
-        af[i] = v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        as[i][0] = ((const float*)(cur + S::SA_OFF))[(2 * s) * BM + row];
-        as[i][1] = ((const float*)(cur + S::SA_OFF))[(2 * s + 1) * BM + row];
-      }
-#pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const int row = wn * S::WN + j * 32 + l32;
-        const v4i lo = chunk(cur + S::B_OFF + row * BK + (((4 * s + h) ^ swz(row)) << 4), 4 * s + h);
-        const v4i hi = chunk(cur + S::B_OFF + row * BK + (((4 * s + 2 + h) ^ swz(row)) << 4), 4 * s + 2 + h);
-        bf[j] = v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        bs[j][0] = ((const float*)(cur + S::SB_OFF))[(2 * s) * BN + row];
-        bs[j][1] = ((const float*)(cur + S::SB_OFF))[(2 * s + 1) * BN + row];
-      }
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        v8bf aw[FM], bw[FN];
-#pragma unroll
-        for (int i = 0; i < FM; ++i) aw[i] = glu_widen8(af[i][2 * t], af[i][2 * t + 1], as[i][t >> 1]);
-#pragma unroll
-        for (int j = 0; j < FN; ++j) bw[j] = glu_widen8(bf[j][2 * t], bf[j][2 * t + 1], bs[j][t >> 1]);
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-          for (int j = 0; j < FN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(aw[i], bw[j], acc[i][j], 0, 0, 0);
-        // the next step's loads go out behind this half's reads, spread over its MFMA groups
-        if (s == 0 && kk + 1 < nk) {
-          constexpr int NP = S::A_INS + S::B_INS + 1;
-          issue(kk + 1, nxt, t * NP / 4, (t + 1) * NP / 4);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
+    for (int j = 0; j < FN; ++j) {
+      const int row = wn * S::WN + j * 32 + l32;
+      q.b[j] = *(const v4i*)(cur + S::B_OFF + row * BK + (((2 * blk + h) ^ glu_swz<BK>(row)) << 4));
+      q.bs[j] = glu_e8m0(cur[S::SB_OFF + blk * BN + row]);
     }
   };
-
-  issue(0, smem, 0, 1 << 20);
-  wait_dma();
-  settle(smem);
-  __syncthreads();
-  const int nfull = KTAIL ? nk - 1 : nk;
-  for (int kk = 0; kk < nfull; ++kk) {
-    uint8_t* cur = smem + (kk & 1) * S::STAGE;
-    uint8_t* nxt = smem + ((kk & 1) ^ 1) * S::STAGE;
-    step(false, kk, cur, nxt);
-    if (kk + 1 < nk) {
-      wait_dma();
-      settle(nxt);
+  auto multiply = [&](const Block& q, auto between) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      v8bf aw[FM], bw[FN];
+#pragma unroll
+      for (int i = 0; i < FM; ++i) aw[i] = glu_widen8(q.a[i][2 * t], q.a[i][2 * t + 1], q.as[i]);
+#pragma unroll
+      for (int j = 0; j < FN; ++j) bw[j] = glu_widen8(q.b[j][2 * t], q.b[j][2 * t + 1], q.bs[j]);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(aw[i], bw[j], acc[i][j], 0, 0, 0);
+      between(t);
     }
-    __syncthreads();
-  }
-  if constexpr (KTAIL) {  // the step that runs past K (its loads were issued by the one before)
-    step(true, nfull, smem + (nfull & 1) * S::STAGE, smem + ((nfull & 1) ^ 1) * S::STAGE);
-    __syncthreads();
-  }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto nothing = [](int) {};
+  Block q[2];
+  // One K step; q[0] holds its first block.  Before its last block's MFMAs all its reads have returned and the
+  // next step's loads have landed: behind that barrier its stage is free, the loads of the step NS ahead go
+  // into it, and the next step's first block is read, both beside those MFMAs.  Blocks past K (a last step that
+  // K does not fill) are not multiplied.
+  auto step = [&](int kk) {
+#pragma unroll
+    for (int blk = 0; blk + 1 < BLKS; ++blk) {
+      read(q[(blk + 1) & 1], kk, blk + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      if (blk == 0 || BLKS * kk + blk < nblk) multiply(q[blk & 1], nothing);
+    }
+    wait(std::integral_constant<int, NS - 2>());
+    read(q[0], kk + 1, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    if (BLKS * kk + BLKS - 1 < nblk)
+      multiply(q[(BLKS - 1) & 1], [&](int t) { issue(kk + NS, t * NP / 2, (t + 1) * NP / 2); });
+    else
+      issue(kk + NS, 0, NP);
+  };
+
+  __syncthreads();  // the group scan's LDS is free
+#pragma unroll
+  for (int kk = 0; kk < NS; ++kk) issue(kk, 0, NP);
+  wait(std::integral_constant<int, NS - 1>());
+  read(q[0], 0, 0);
+  for (int kk = 0; kk < nk; ++kk) step(kk);
+  glu_wait_barrier<0>();  // the zeros past the last step have landed: LDS is free
 
   // ---------------- epilogue ----------------
   // register r of fragment (i, j): row 32 i + 8 (r / 4) + 4 h + r % 4, column 32 j + l32 of the block
   float* tile = (float*)(smem + wave * S::EP);
+  float* probs = (float*)(smem + S::NW * S::EP);
+  if (tid < BM) probs[tid] = my_prob;
+  __syncthreads();
   constexpr int PITCH = S::PITCH;
   if constexpr (!GRAD) {
     const int cw = wn * 32;  // the wave's first column within the tile
@@ -291,7 +332,8 @@ __global__ __launch_bounds__(2 * TILE) void glu_gemm_kernel(GluArgs args) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int r = 4 * q + k;
-          v[r] = swiglu(acc[i][0][r], acc[i][1][r], p[k]);
+          // (a dead row's scales may be anything)
+          v[r] = rb + 8 * q + 4 * h + k <= a_last ? swiglu(acc[i][0][r], acc[i][1][r], p[k]) : 0.0f;
           if (args.ab != nullptr) {
             const uint32_t at = ((uint32_t)(i * 32 + 8 * q + 4 * h + k) * (uint32_t)N2 + (uint32_t)l32) * 2;
             __builtin_amdgcn_raw_buffer_store_b16((short)f32_to_bf16(acc[i][0][r]), ab_rs, (int)at, 0, 0);
@@ -321,7 +363,7 @@ __global__ __launch_bounds__(2 * TILE) void glu_gemm_kernel(GluArgs args) {
     }
   } else {
     const int cw = wn * 64;
-    float* dp_sum = (float*)(smem + S::NW * S::EP) + wn * BM;  // this wave's column part of dprobs, per row
+    float* dp_sum = probs + (1 + wn) * BM;  // this wave's column part of dprobs, per row
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       const int rb = wm * S::WM + i * 32;
@@ -348,11 +390,12 @@ __global__ __launch_bounds__(2 * TILE) void glu_gemm_kernel(GluArgs args) {
       for (int pass = 0; pass < 4; ++pass) {
         const int r = pass * 8 + (lane >> 3);
         const float p = probs[rb + r];
+        const bool live = cols && rb + r <= a_last;
         float da[8], dp = 0.0f;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          swiglu_grad(to_f32(av[pass][k]), to_f32(bv[pass][k]), p, tile[r * PITCH + ch + k], da[k], db[pass][k], dp);
-        const bool live = cols && rb + r <= a_last;
+          swiglu_grad(to_f32(av[pass][k]), to_f32(bv[pass][k]), p, live ? tile[r * PITCH + ch + k] : 0.0f, da[k],
+                      db[pass][k], dp);
         const int64_t row = gi.off + row0 + rb + r, col = col0 + cw + ch;
         put_row8(args.out, args.R, 2 * F, row, col, live, da);
         put_row8(args.out, args.R, 2 * F, row, F + col, live, db[pass]);
@@ -384,7 +427,7 @@ __global__ __launch_bounds__(2 * TILE) void glu_gemm_kernel(GluArgs args) {
     }
     if (args.dpart != nullptr) {
       __syncthreads();
-      const float* s = (const float*)(smem + S::NW * S::EP);
+      const float* s = probs + BM;
       if (tid <= a_last) {
         float d = s[tid];
 #pragma unroll
@@ -409,7 +452,7 @@ __global__ __launch_bounds__(2 * TILE) void glu_gemm_kernel(GluArgs args) {
 constexpr int kRowsBM = 32, kRowsBN = 64, kRowsNW = 4, kRowsPitch = 68;
 
 template <bool GRAD>
-__global__ __launch_bounds__(256) void glu_rows_kernel(GluArgs args) {
+__global__ __launch_bounds__(256, 2) void glu_rows_kernel(GluArgs args) {
   constexpr int BM = kRowsBM, BN = kRowsBN, NW = kRowsNW, NT = 64 * NW, P = kRowsPitch;
   constexpr int COLS = GRAD ? BN : BN / 2;
   __shared__ GroupScanSmem<NT> gsm;
@@ -626,21 +669,26 @@ __global__ __launch_bounds__(256) void glu_dprobs_kernel(const float* __restrict
 // Launchers
 // ------------------------------------------------------------------------------------------
 
-// Tile of a launch.  Up to 32 rows per expert on average take the few-rows kernel (kRowsTile); the others
-// 256 x 256 tiles unless that leaves much of the chip idle.  Groups end half a tile early on average, hence
-// R / 256 + E / 2 rows of tiles.
-constexpr int kRowsTile = 32;
-constexpr int64_t kSmallGluTiles = 512;
+// Tile of a launch.  Up to 32 rows per expert on average take the few-rows kernel; the others the largest
+// tile that still gives every CU its share.  Groups end half a tile early on average, hence R / BM + E / 2
+// rows of tiles.
+struct GluTile {
+  int bm, bn;
+};
 
-static int glu_tile(bool grad, int64_t R, int64_t F, int E) {
-  if (R <= (int64_t)kRowsTile * E) return kRowsTile;
-  const int64_t cols = grad ? 256 : 128;
-  return (R / 256 + (E + 1) / 2) * ((F + cols - 1) / cols) < kSmallGluTiles ? 128 : 256;
+static GluTile glu_tile(bool grad, int64_t R, int64_t F, int E) {
+  if (R <= (int64_t)kRowsBM * E) return {kRowsBM, kRowsBN};
+  auto tiles = [&](int bm, int bn) {
+    const int64_t cols = grad ? bn : bn / 2;
+    return (R / bm + (E + 1) / 2) * ((F + cols - 1) / cols);
+  };
+  if (tiles(256, 256) >= 512) return {256, 256};
+  return {128, 128};
 }
 
 // Columns of one half per tile, and the tiles of a row of them.
-static int64_t glu_tiles_n(bool grad, int tile, int64_t F) {
-  const int64_t w = tile == kRowsTile ? kRowsBN : tile, c = grad ? w : w / 2;
+static int64_t glu_tiles_n(bool grad, GluTile t, int64_t F) {
+  const int64_t c = grad ? t.bn : t.bn / 2;
   return (F + c - 1) / c;
 }
 
@@ -650,10 +698,10 @@ size_t glu_grad_workspace_bytes(int64_t R, int64_t F, int E) {
 }
 
 // The grid of a launch: rows of tiles that any valid sizes can need (at most one per row), in whole runs.
-static int glu_grid(GluArgs& a, bool grad, int tile, dim3* grid) {
-  a.tiles_n = (int)glu_tiles_n(grad, tile, a.F);
+static int glu_grid(GluArgs& a, bool grad, GluTile t, dim3* grid) {
+  a.tiles_n = (int)glu_tiles_n(grad, t, a.F);
   const int64_t gm = fprop_run_mtiles(a.tiles_n);
-  int64_t mt = (a.R + (int64_t)(tile - 1) * a.E) / tile;
+  int64_t mt = (a.R + (int64_t)(t.bm - 1) * a.E) / t.bm;
   if (mt > a.R) mt = a.R;
   a.tiles = (mt + gm - 1) / gm * gm * a.tiles_n;
   if (xcd_launch_size(a.tiles) > 0x7fffffff) return BSFP8_ERR_SHAPE;
@@ -661,22 +709,20 @@ static int glu_grid(GluArgs& a, bool grad, int tile, dim3* grid) {
   return BSFP8_OK;
 }
 
+template <bool GRAD, int BM, int BN, int BK, int NS>
+static void launch_glu_tile(const GluArgs& a, dim3 grid, hipStream_t stream) {
+  hipLaunchKernelGGL((glu_gemm_kernel<GRAD, BM, BN, BK, NS>), grid, dim3(2 * BN), 0, stream, a);
+}
+
 template <bool GRAD>
 static int launch_glu(GluArgs& a, hipStream_t stream) {
-  const int tile = glu_tile(GRAD, a.R, a.F, a.E);
-  const bool tail = a.K % 128 != 0;
+  const GluTile t = glu_tile(GRAD, a.R, a.F, a.E);
   dim3 grid;
-  const int rc = glu_grid(a, GRAD, tile, &grid);
+  const int rc = glu_grid(a, GRAD, t, &grid);
   if (rc != BSFP8_OK) return rc;
-  if (tile == kRowsTile) {
-    hipLaunchKernelGGL((glu_rows_kernel<GRAD>), grid, dim3(64 * kRowsNW), 0, stream, a);
-  } else if (tile == 128) {
-    if (tail) hipLaunchKernelGGL((glu_gemm_kernel<GRAD, true, 128>), grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((glu_gemm_kernel<GRAD, false, 128>), grid, dim3(256), 0, stream, a);
-  } else {
-    if (tail) hipLaunchKernelGGL((glu_gemm_kernel<GRAD, true, 256>), grid, dim3(512), 0, stream, a);
-    else hipLaunchKernelGGL((glu_gemm_kernel<GRAD, false, 256>), grid, dim3(512), 0, stream, a);
-  }
+  if (t.bm == kRowsBM) hipLaunchKernelGGL((glu_rows_kernel<GRAD>), grid, dim3(64 * kRowsNW), 0, stream, a);
+  else if (t.bn == 256) launch_glu_tile<GRAD, 256, 256, 128, 2>(a, grid, stream);
+  else launch_glu_tile<GRAD, 128, 128, 64, 3>(a, grid, stream);
   return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
 }
 

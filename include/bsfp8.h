@@ -295,7 +295,7 @@ int bsfp8_grouped_gemm_dgrad(const uint8_t* dy_row_q, const uint8_t* dy_row_s, i
  * which, row_q, row_s, col_q, col_s   y quantized from its fp32 values, laid out as
  *                   bsfp8_grouped_quantize does for [capacity_rows][ffn]; which == 0: none
  * At least one of ab, y and the quantized layouts is asked for.  Rows at or past sum(k_e) are not
- * written.  hidden and ffn are multiples of 32, hidden below 2^24 - 128, ffn at most 2^20.
+ * written.  hidden and ffn are multiples of 32, hidden at most 2^22, ffn at most 2^20.
  * capacity_rows == 0 returns BSFP8_OK without touching any pointer.
  */
 int bsfp8_grouped_gemm_swiglu(const uint8_t* x_row_q, const uint8_t* x_row_s, int64_t capacity_rows,
