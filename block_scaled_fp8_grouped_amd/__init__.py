@@ -154,7 +154,7 @@ def _dev(t, what, dtypes):
         return _ptr(t)
     if t.dtype not in dtypes:
         raise TypeError(f"{what}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{what}: a {t.device.type} tensor; the library takes device memory")
     if not t.is_contiguous():
         raise ValueError(f"{what}: not contiguous")
@@ -193,8 +193,16 @@ def _col_s_types(recipe):
     return _F32 if (recipe & ~GEMM_FP8_MFMA) == RECIPE_PC else _U8
 
 
+# torch's current stream as a raw handle, without building a Stream object for every call (a quarter of a
+# small call's host time), where this torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None and _raw_device is not None and torch.cuda.is_initialized():
+            return _raw_stream(_raw_device())
         return torch.cuda.current_stream().cuda_stream
     return getattr(stream, "cuda_stream", stream)
 
@@ -441,14 +449,15 @@ def _like(t, shape, what, dtype=None):
     """A tensor argument of exactly this shape (and element type, where given)."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
 
 
-def _check_norm_block(rows, cols, y, post_weight, pre_weight, gate, gate_kind):
-    _like(y, (rows, cols), "y")
+def _check_norm_block(shape, y, post_weight, pre_weight, gate, gate_kind):
+    rows, cols = shape
+    _like(y, shape, "y")
     _like(post_weight, (cols,), "post_weight")
     _like(pre_weight, (cols,), "pre_weight")
     if gate_kind == GATE_CHANNEL:
@@ -471,26 +480,33 @@ def residual_norm(x, y=None, post_weight=None, pre_weight=None, gate=None, gate_
     r may be x."""
     if x.dim() != 2:
         raise ValueError("residual_norm: x is [rows, cols]")
-    rows, cols = x.shape
-    px = _dev(x, "x", _STREAM)
-    py, pw, qw = _dev(y, "y", _BF16), _dev(post_weight, "post_weight", _F32), _dev(pre_weight, "pre_weight", _F32)
-    pg = _dev(gate, "gate", _F32)
-    _check_norm_block(rows, cols, y, post_weight, pre_weight, gate, gate_kind)
-    out = {"r": torch.empty_like(x) if r is None else r}
+    shape = rows, cols = x.shape
+    args = (_dev(x, "x", _STREAM), F32 if x.dtype is torch.float32 else BF16, _dev(y, "y", _BF16),
+            _dev(post_weight, "post_weight", _F32), _dev(pre_weight, "pre_weight", _F32), _dev(gate, "gate", _F32))
+    _check_norm_block(shape, y, post_weight, pre_weight, gate, gate_kind)
+    dev = x.device
+    out = {}
+    if r is None:
+        r = torch.empty_like(x)
+    else:
+        _like(r, shape, "r", x.dtype)
+    out["r"] = r
     if pre_weight is not None:
-        out["n"] = torch.empty((rows, cols), dtype=torch.bfloat16, device=x.device) if n is None else n
-        out["rstd_r"] = torch.empty(rows, dtype=torch.float32, device=x.device) if rstd_r is None else rstd_r
+        if n is None:
+            n = torch.empty_like(x, dtype=torch.bfloat16)
+        if rstd_r is None:
+            rstd_r = torch.empty(rows, dtype=torch.float32, device=dev)
+        out["n"], out["rstd_r"] = n, rstd_r
     if post_weight is not None:
-        out["rstd_y"] = torch.empty(rows, dtype=torch.float32, device=x.device) if rstd_y is None else rstd_y
-    if r is not None:
-        _like(r, (rows, cols), "r", x.dtype)
-    _like(n, (rows, cols), "n")
+        if rstd_y is None:
+            rstd_y = torch.empty(rows, dtype=torch.float32, device=dev)
+        out["rstd_y"] = rstd_y
+    _like(n, shape, "n")
     _like(rstd_y, (rows,), "rstd_y")
     _like(rstd_r, (rows,), "rstd_r")
-    rc = lib().bsfp8_residual_norm(
-        rows, cols, px, _dtype_code(x), py, pw, qw, pg, gate_kind, x_scale, y_scale, eps, weight_offset,
-        _dev(out["r"], "r", _STREAM), _dev(out.get("n", n), "n", _BF16), _dev(out.get("rstd_y", rstd_y), "rstd_y", _F32),
-        _dev(out.get("rstd_r", rstd_r), "rstd_r", _F32), _stream(stream))
+    rc = lib().bsfp8_residual_norm(rows, cols, *args, gate_kind, x_scale, y_scale, eps, weight_offset,
+                                   _dev(r, "r", _STREAM), _dev(n, "n", _BF16), _dev(rstd_y, "rstd_y", _F32),
+                                   _dev(rstd_r, "rstd_r", _F32), _stream(stream))
     _check(rc, "residual_norm")
     return out
 
@@ -513,46 +529,48 @@ def residual_norm_grad(dn, dr, r=None, rstd_r=None, pre_weight=None, y=None, rst
         raise ValueError("residual_norm_grad: neither dr nor (dn and r)")
     if ref.dim() != 2:
         raise ValueError("residual_norm_grad: r and dr are [rows, cols]")
-    rows, cols = ref.shape
-    dev = ref.device
-    pdn, pdr, pr = _dev(dn, "dn", _BF16), _dev(dr, "dr", _STREAM), _dev(r, "r", _STREAM)
-    args = (pr, _dev(rstd_r, "rstd_r", _F32), _dev(pre_weight, "pre_weight", _F32), _dev(y, "y", _BF16),
-            _dev(rstd_y, "rstd_y", _F32), _dev(post_weight, "post_weight", _F32), _dev(gate, "gate", _F32))
-    _like(dn, (rows, cols), "dn")
-    _like(dr, (rows, cols), "dr", ref.dtype)
-    _like(r, (rows, cols), "r", ref.dtype)
+    shape = rows, cols = ref.shape
+    dev, dtype = ref.device, ref.dtype
+    args = (F32 if dtype is torch.float32 else BF16, _dev(dn, "dn", _BF16), _dev(dr, "dr", _STREAM),
+            _dev(r, "r", _STREAM), _dev(rstd_r, "rstd_r", _F32), _dev(pre_weight, "pre_weight", _F32),
+            _dev(y, "y", _BF16), _dev(rstd_y, "rstd_y", _F32), _dev(post_weight, "post_weight", _F32),
+            _dev(gate, "gate", _F32))
+    _like(dn, shape, "dn")
+    _like(dr, shape, "dr", dtype)
+    _like(r, shape, "r", dtype)
     _like(rstd_r, (rows,), "rstd_r")
     _like(rstd_y, (rows,), "rstd_y")
-    _check_norm_block(rows, cols, y, post_weight, pre_weight, gate, gate_kind)
+    _check_norm_block(shape, y, post_weight, pre_weight, gate, gate_kind)
     if accumulate and any(w is not None and d is None for w, d in (
             (pre_weight, dpre_weight), (post_weight, dpost_weight),
             (gate if gate_kind == GATE_CHANNEL else None, dgate))):
         raise ValueError("residual_norm_grad: accumulate needs the gradients to add to")
-    f32 = dict(dtype=torch.float32, device=dev)
-    out = {"dx": torch.empty((rows, cols), dtype=ref.dtype, device=dev) if dx is None else dx}
+    out = {}
+    if dx is None:
+        dx = torch.empty_like(ref)
+    else:
+        _like(dx, shape, "dx", dtype)
+    out["dx"] = dx
     if y is not None:
-        out["dy"] = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev) if dy is None else dy
+        out["dy"] = dy = torch.empty_like(y) if dy is None else dy
     if pre_weight is not None:
-        out["dpre_weight"] = torch.empty(cols, **f32) if dpre_weight is None else dpre_weight
+        out["dpre_weight"] = dpre_weight = torch.empty_like(pre_weight) if dpre_weight is None else dpre_weight
     if post_weight is not None:
-        out["dpost_weight"] = torch.empty(cols, **f32) if dpost_weight is None else dpost_weight
+        out["dpost_weight"] = dpost_weight = torch.empty_like(post_weight) if dpost_weight is None else dpost_weight
     if gate is not None:
-        out["dgate"] = torch.empty(gate.shape, **f32) if dgate is None else dgate
-    _like(out["dx"], (rows, cols), "dx", ref.dtype)
-    _like(out.get("dy", dy), (rows, cols), "dy")
-    _like(out.get("dpre_weight", dpre_weight), (cols,), "dpre_weight")
-    _like(out.get("dpost_weight", dpost_weight), (cols,), "dpost_weight")
-    if gate is not None:
-        _like(out["dgate"], gate.shape, "dgate")
+        out["dgate"] = dgate = torch.empty_like(gate) if dgate is None else dgate
+        _like(dgate, gate.shape, "dgate")
+    _like(dy, shape, "dy")
+    _like(dpre_weight, (cols,), "dpre_weight")
+    _like(dpost_weight, (cols,), "dpost_weight")
     need = residual_norm_grad_workspace_bytes(rows, cols)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _need(workspace, need, "workspace")
+    else:
+        _need(workspace, need, "workspace")
     rc = lib().bsfp8_residual_norm_grad(
-        rows, cols, _dtype_code(ref), pdn, pdr, *args, gate_kind, x_scale, y_scale, weight_offset,
-        _dev(out["dx"], "dx", _STREAM), _dev(out.get("dy", dy), "dy", _BF16),
-        _dev(out.get("dpre_weight", dpre_weight), "dpre_weight", _F32),
-        _dev(out.get("dpost_weight", dpost_weight), "dpost_weight", _F32), _dev(out.get("dgate", dgate), "dgate", _F32),
+        rows, cols, *args, gate_kind, x_scale, y_scale, weight_offset, _dev(dx, "dx", _STREAM), _dev(dy, "dy", _BF16),
+        _dev(dpre_weight, "dpre_weight", _F32), _dev(dpost_weight, "dpost_weight", _F32), _dev(dgate, "dgate", _F32),
         1 if accumulate else 0, _dev(workspace, "workspace", (workspace.dtype,)), _stream(stream))
     _check(rc, "residual_norm_grad")
     return out

@@ -345,7 +345,7 @@ int bsfp8_residual_norm(int64_t rows, int64_t cols, const void* x, int stream_dt
 
 size_t bsfp8_residual_norm_grad_workspace_bytes(int64_t rows, int64_t cols) {
   if (!valid_norm_shape(rows, cols)) return 0;
-  return (size_t)bsfp8::norm_grad_slots(rows, cols) * 3 * (size_t)cols * sizeof(float);
+  return (size_t)bsfp8::norm_grad_slots(rows, cols) * 2 * (size_t)cols * sizeof(float);
 }
 
 int bsfp8_residual_norm_grad(int64_t rows, int64_t cols, int stream_dtype, const void* dn, const void* dr,

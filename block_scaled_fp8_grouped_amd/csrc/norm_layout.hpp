@@ -6,39 +6,32 @@
 namespace bsfp8 {
 
 constexpr int64_t kNormMaxCols = 32768;  // 1024 threads x 4 chunks x 8 elements
+constexpr int64_t kNormCus = 256;
 
-// Threads per row and chunks of 8 elements per thread.
+// Up to 512 columns a row is one wave's, 4 rows to a workgroup; above, a workgroup's of as many waves as
+// the row needs at `vpt` chunks of 8 elements per thread.
 struct NormShape {
-  int nt, vpt;
+  bool wave;
+  int vpt, threads;
 };
 
 inline NormShape norm_shape(int64_t cols) {
-  const int64_t c = (cols + 7) / 8;  // chunks of a row
-  if (c <= 64) return {64, 1};
-  if (c <= 128) return {64, 2};
-  if (c <= 256) return {256, 1};
-  if (c <= 512) return {256, 2};
-  if (c <= 1024) return {1024, 1};
-  if (c <= 2048) return {1024, 2};
-  return {1024, 4};
+  if (cols <= 512) return {true, 1, 256};
+  const int vpt = cols <= 8192 ? 1 : cols <= 16384 ? 2 : 4;
+  return {false, vpt, 64 * (int)((cols + 512 * vpt - 1) / (512 * vpt))};
 }
 
-inline int64_t norm_rows_per_block(int64_t cols) {
-  const int nt = norm_shape(cols).nt;
-  return nt < 256 ? 256 / nt : 1;
+// Workgroups: as many as fill the chip with `waves` waves per CU, each walking every gridDim-th row.
+inline int64_t norm_fill(int64_t rows, int64_t cols, int64_t waves) {
+  const NormShape s = norm_shape(cols);
+  const int64_t rpb = s.wave ? 4 : 1, need = (rows + rpb - 1) / rpb, per = waves / (s.threads / 64);
+  const int64_t most = kNormCus * (per < 1 ? 1 : per);
+  return need < most ? need : most;
 }
 
-// Forward: enough workgroups for every CU to hold 8, each walking every gridDim-th row.
-inline int64_t norm_blocks(int64_t rows, int64_t cols) {
-  const int64_t rpb = norm_rows_per_block(cols), b = (rows + rpb - 1) / rpb;
-  return b < 2048 ? b : 2048;
-}
+inline int64_t norm_blocks(int64_t rows, int64_t cols) { return norm_fill(rows, cols, 32); }
 
 // Gradient: as many workgroups as partial rows.
-inline int64_t norm_grad_slots(int64_t rows, int64_t cols) {
-  const int64_t rpb = norm_rows_per_block(cols), b = (rows + rpb - 1) / rpb;
-  const int64_t most = norm_shape(cols).nt >= 1024 ? 512 : 1024;
-  return b < most ? b : most;
-}
+inline int64_t norm_grad_slots(int64_t rows, int64_t cols) { return norm_fill(rows, cols, 16); }
 
 }  // namespace bsfp8
