@@ -17,6 +17,8 @@
 // Rows of any length and any 2- or 4-byte alignment take the same path: a thread's 8 elements are
 // moved as one unaligned vector, the last chunk of a row whose length is not a multiple of 8 by
 // element.
+#include <type_traits>
+
 #include "common.hpp"
 #include "norm_layout.hpp"
 
@@ -46,20 +48,38 @@ __device__ __forceinline__ float to_f32(float f) { return f; }
 __device__ __forceinline__ void from_f32(float f, uint16_t& o) { o = f32_to_bf16(f); }
 __device__ __forceinline__ void from_f32(float f, float& o) { o = f; }
 
-// 8 elements as they lie in memory.
+// 8 elements as they lie in memory: n of them exist at p, the others read as 0; any alignment of the
+// element's size.
 template <class T>
-struct Raw8 {
-  T t[8];
-  // n of them exist at p, the others read as 0; any alignment of the element's size
-  __device__ __forceinline__ void load(const T* p, int n) {
+struct Raw8;
+template <>
+struct Raw8<float> {
+  float t[8];
+  __device__ __forceinline__ void load_all(const float* p) { __builtin_memcpy(t, p, sizeof(t)); }
+  __device__ __forceinline__ void load(const float* p, int n) {
     if (n >= 8) {
       __builtin_memcpy(t, p, sizeof(t));
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = i < n ? p[i] : (T)0;
+      for (int i = 0; i < 8; ++i) t[i] = i < n ? p[i] : 0.0f;
     }
   }
-  __device__ __forceinline__ float operator[](int i) const { return to_f32(t[i]); }
+  __device__ __forceinline__ float operator[](int i) const { return t[i]; }
+};
+template <>
+struct Raw8<uint16_t> {
+  uint32_t w[4];  // pairs, so that the compiler keeps them in four registers
+  __device__ __forceinline__ void load_all(const uint16_t* p) { __builtin_memcpy(w, p, sizeof(w)); }
+  __device__ __forceinline__ void load(const uint16_t* p, int n) {
+    if (n >= 8) {
+      __builtin_memcpy(w, p, sizeof(w));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = (2 * i < n ? (uint32_t)p[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+    }
+  }
+  __device__ __forceinline__ float operator[](int i) const { return i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]); }
 };
 template <class T>
 __device__ __forceinline__ void load8(const T* p, int n, float* v) {
@@ -82,37 +102,64 @@ __device__ __forceinline__ void store8(T* p, int n, const float* v) {
   }
 }
 
-// Sum over the threads of a row, the same bits in every thread: a wave (WAVE), or the workgroup's up to
-// 16 waves through LDS.  `sm` holds two alternating buffers, so one barrier per reduction is enough: a
-// buffer is written again two reductions later, after the barrier of the one between.
-template <bool WAVE>
+// Sum of a wave's 64 values, in lane 63: adds with data-parallel lane moves (a shuffle through LDS takes ten
+// times as long).
+__device__ __forceinline__ float wave_sum(float v) {
+  auto add = [&](auto ctrl, int rows) {
+    constexpr int C = decltype(ctrl)::value;
+    const int m = rows == 0xf ? __builtin_amdgcn_update_dpp(0, __float_as_int(v), C, 0xf, 0xf, false)
+                              : rows == 0xa ? __builtin_amdgcn_update_dpp(0, __float_as_int(v), C, 0xa, 0xf, false)
+                                            : __builtin_amdgcn_update_dpp(0, __float_as_int(v), C, 0xc, 0xf, false);
+    v += __int_as_float(m);
+  };
+  add(std::integral_constant<int, 0x111>(), 0xf);  // the lane 1, 2, 4, 8 below in its row of 16 (0 where none)
+  add(std::integral_constant<int, 0x112>(), 0xf);
+  add(std::integral_constant<int, 0x114>(), 0xf);
+  add(std::integral_constant<int, 0x118>(), 0xf);
+  add(std::integral_constant<int, 0x142>(), 0xa);  // lane 15 of the row below, into rows 1 and 3
+  add(std::integral_constant<int, 0x143>(), 0xc);  // lane 31, into rows 2 and 3
+  return v;
+}
+
+// Sums of K values over the threads of a row, the same bits in every thread: a wave (WAVE), or the
+// workgroup's up to 16 waves through LDS.  `sm` holds two alternating buffers, so one barrier per reduction is
+// enough: a buffer is written again two reductions later, after the barrier of the one between.
+template <bool WAVE, int K>
 struct RowSum {
-  float (*sm)[16];
+  float (*sm)[K][16];
   int turn = 0;
-  __device__ __forceinline__ explicit RowSum(float (*buffers)[16]) : sm(buffers) {
+  __device__ __forceinline__ explicit RowSum(float (*buffers)[K][16]) : sm(buffers) {
     if constexpr (!WAVE) {
-      if (threadIdx.x < 32) sm[threadIdx.x >> 4][threadIdx.x & 15] = 0.0f;  // the waves that are not there
+      if (threadIdx.x < 32 * K) sm[0][0][threadIdx.x] = 0.0f;  // the waves that are not there
       __syncthreads();
     }
   }
-  __device__ __forceinline__ float operator()(float v) {
+  __device__ __forceinline__ void operator()(float (&v)[K]) {
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
-    if constexpr (!WAVE) {
-      if ((threadIdx.x & 63) == 0) sm[turn][threadIdx.x >> 6] = v;
+    for (int k = 0; k < K; ++k) v[k] = wave_sum(v[k]);
+    if constexpr (WAVE) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v[k]), 63));
+    } else {
+      if ((threadIdx.x & 63) == 63)
+#pragma unroll
+        for (int k = 0; k < K; ++k) sm[turn][k][threadIdx.x >> 6] = v[k];
       __syncthreads();
-      v4f s = *(const v4f*)&sm[turn][0];
 #pragma unroll
-      for (int i = 1; i < 4; ++i) s += *(const v4f*)&sm[turn][4 * i];
-      v = (s[0] + s[1]) + (s[2] + s[3]);
+      for (int k = 0; k < K; ++k) {
+        v4f s = *(const v4f*)&sm[turn][k][0];
+#pragma unroll
+        for (int i = 1; i < 4; ++i) s += *(const v4f*)&sm[turn][k][4 * i];
+        v[k] = (s[0] + s[1]) + (s[2] + s[3]);
+      }
       turn ^= 1;
     }
-    return v;
   }
 };
 
+// (the hardware's reciprocal square root, within 1 ulp of fp32)
 __device__ __forceinline__ float rstd_of(float sum, float inv_c, float eps) {
-  return 1.0f / sqrtf(sum * inv_c + eps);
+  return __builtin_amdgcn_rsqf(sum * inv_c + eps);
 }
 
 // The factors of 8 columns: pre_weight + offset, and (post_weight + offset) times a channel's gate.
@@ -140,11 +187,11 @@ __device__ __forceinline__ void load_factors(const NormArgs& a, int c, int n, fl
 // WAVE: a row per wave, 4 rows per workgroup of 256; else a row per workgroup.  VPT chunks of 8 elements
 // per thread; with one, the factors are held and the next row is fetched ahead.
 template <class XT, bool WAVE, int VPT>
-__global__ __launch_bounds__(WAVE ? 256 : 1024) void residual_norm_kernel(NormArgs a) {
+__global__ __launch_bounds__(WAVE ? 256 : 1024, VPT == 1 ? 7 : 4) void residual_norm_kernel(NormArgs a) {
   constexpr bool AHEAD = VPT == 1;
   const int NT = WAVE ? 64 : blockDim.x, RPB = WAVE ? 4 : 1;
-  __shared__ __attribute__((aligned(16))) float sm[2][16];
-  RowSum<WAVE> row_sum(sm);
+  __shared__ __attribute__((aligned(16))) float sm[2][1][16];
+  RowSum<WAVE, 1> row_sum(sm);
   const int t = WAVE ? threadIdx.x & 63 : threadIdx.x;
   const float inv_c = 1.0f / (float)a.C;
   const int C = (int)a.C;
@@ -181,12 +228,13 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void residual_norm_kernel(NormAr
     if (AHEAD && row + stride < a.R) fetch(row + stride);
     if (has_y) {
       if (a.post_w != nullptr) {
-        float q = 0.0f;
+        float q[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) q = __builtin_fmaf(y[i][e], y[i][e], q);
-        const float ry = rstd_of(row_sum(q), inv_c, a.eps);
+          for (int e = 0; e < 8; ++e) q[0] = __builtin_fmaf(y[i][e], y[i][e], q[0]);
+        row_sum(q);
+        const float ry = rstd_of(q[0], inv_c, a.eps);
         if (t == 0 && a.rstd_y != nullptr) a.rstd_y[row] = ry;
         s *= ry;
       }
@@ -208,12 +256,13 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void residual_norm_kernel(NormAr
       }
     }
     if (a.pre_w != nullptr) {
-      float q = 0.0f;
+      float q[1] = {0.0f};
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q = __builtin_fmaf(x[i][e], x[i][e], q);
-      const float rr = rstd_of(row_sum(q), inv_c, a.eps);
+        for (int e = 0; e < 8; ++e) q[0] = __builtin_fmaf(x[i][e], x[i][e], q[0]);
+      row_sum(q);
+      const float rr = rstd_of(q[0], inv_c, a.eps);
       if (t == 0 && a.rstd_r != nullptr) a.rstd_r[row] = rr;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
@@ -226,116 +275,169 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void residual_norm_kernel(NormAr
   }
 }
 
-template <class XT, bool WAVE, int VPT>
+// ROWS rows at a time: their loads are in flight together and their reductions share a barrier.  With two,
+// the last thread of a row whose length is not a multiple of 8 takes the row's last 8 elements instead of a
+// part of a chunk (loads by element cost more registers than 16 waves leave); the first `shift` of them are
+// its neighbour's: their factors are zero here, which keeps them out of the row's sums, and they are not
+// stored.
+template <class XT, bool WAVE, int VPT, int ROWS>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void residual_norm_grad_kernel(NormArgs a) {
-  constexpr bool AHEAD = VPT == 1;
-  const int NT = WAVE ? 64 : blockDim.x, RPB = WAVE ? 4 : 1;
-  __shared__ __attribute__((aligned(16))) float sm[2][16];
-  RowSum<WAVE> row_sum(sm);
+  constexpr bool HOLD = VPT == 1;
+  constexpr bool WHOLE = ROWS == 2;
+  const int NT = WAVE ? 64 : blockDim.x, RPB = WAVE ? 4 * ROWS : ROWS;
+  __shared__ __attribute__((aligned(16))) float sm[2][ROWS][16];
+  RowSum<WAVE, ROWS> row_sum(sm);
   const int t = WAVE ? threadIdx.x & 63 : threadIdx.x;
   const float inv_c = 1.0f / (float)a.C;
   const int C = (int)a.C;
   const bool has_n = a.dn != nullptr, has_y = a.y != nullptr;
   float wq[VPT][8], wp[VPT][8], sum_pre[VPT][8], sum_y[VPT][8];
-  if constexpr (AHEAD) load_factors(a, t * 8, C - t * 8, wq[0], wp[0]);
+  const bool mine = t * 8 < C;
+  const int shift = WHOLE && mine && t * 8 + 8 > C ? t * 8 + 8 - C : 0;
+  if constexpr (HOLD) {
+    load_factors(a, t * 8 - shift, C - t * 8 + shift, wq[0], wp[0]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < shift) wq[0][e] = wp[0][e] = 0.0f;
+  }
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum_pre[i][e] = sum_y[i][e] = 0.0f;
-  Raw8<uint16_t> nraw[VPT], yraw[VPT];
-  Raw8<XT> rraw[VPT], draw[VPT];
-  float rr_next = 0.0f, ry_next = 1.0f, gate_next = 1.0f;
-  auto fetch = [&](int64_t row) {
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (t + i * NT) * 8;
-      const int64_t at = row * a.C + c;
-      if (has_n) {
-        nraw[i].load(a.dn + at, C - c);
-        rraw[i].load((const XT*)a.r + at, C - c);
-      }
-      if (a.dr != nullptr) draw[i].load((const XT*)a.dr + at, C - c);
-      if (has_y) yraw[i].load(a.y + at, C - c);
-    }
-    if (has_n) rr_next = a.rstd_r[row];
-    if (a.post_w != nullptr) ry_next = a.rstd_y[row];
-    if (a.gate_kind == BSFP8_GATE_TOKEN) gate_next = a.gate[row];
-  };
   const int64_t stride = (int64_t)gridDim.x * RPB;
-  int64_t row = (int64_t)blockIdx.x * RPB + (WAVE ? threadIdx.x >> 6 : 0);
-  if (AHEAD && row < a.R) fetch(row);
-  for (; row < a.R; row += stride) {
-    const int64_t base = row * a.C;
-    if constexpr (!AHEAD) fetch(row);
-    const float rr = rr_next, ry = ry_next, gate = gate_next;
-    float g[VPT][8], rh[VPT][8], d[VPT][8];
-    // (y and dr stay as they came until they are needed, in half the registers or fewer)
-    Raw8<uint16_t> ycur[VPT];
-    Raw8<XT> dcur[VPT];
-    float q = 0.0f;
+  const int wave_row = WAVE ? __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) * ROWS : 0;
+  // elements of this thread's chunk i that exist
+  auto count = [&](int i, bool live) { return live ? C - (t + i * NT) * 8 : 0; };
+  auto put8 = [&](auto* p, int n, const float* v) {
+    if constexpr (WHOLE) {
+      if (n > 0) {
+        if (shift == 0) {
+          store8(p, 8, v);
+        } else {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      if constexpr (!AHEAD) load_factors(a, (t + i * NT) * 8, C - (t + i * NT) * 8, wq[i], wp[i]);
-      ycur[i] = yraw[i];
-      dcur[i] = draw[i];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (has_n) {
-          const float n = nraw[i][e];
-          rh[i][e] = rraw[i][e] * rr;
-          sum_pre[i][e] = __builtin_fmaf(n, rh[i][e], sum_pre[i][e]);
-          g[i][e] = n * wq[i][e];
-          q = __builtin_fmaf(g[i][e], rh[i][e], q);
+          for (int e = 1; e < 8; ++e)
+            if (e >= shift) from_f32(v[e], p[e]);
         }
       }
+    } else {
+      store8(p, n, v);
     }
-    if (AHEAD && row + stride < a.R) fetch(row + stride);
-    // through the norm before the next block: d = dr + rr (g1 - rh mean(g1 rh))
-    const float m1 = has_n ? row_sum(q) * inv_c : 0.0f;
+  };
+  for (int64_t row = (int64_t)blockIdx.x * RPB + wave_row; row < a.R; row += stride) {
+    Raw8<uint16_t> n[ROWS][VPT], y[ROWS][VPT];
+    Raw8<XT> r[ROWS][VPT], d0[ROWS][VPT];
+    float rr[ROWS], ry[ROWS], gate[ROWS], q[ROWS], d[ROWS][VPT][8];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        d[i][e] = a.dr != nullptr ? dcur[i][e] : 0.0f;
-        if (has_n) d[i][e] = __builtin_fmaf(rr, __builtin_fmaf(-rh[i][e], m1, g[i][e]), d[i][e]);
-      }
-    if (a.dx != nullptr) {
+    for (int j = 0; j < ROWS; ++j) {
+      const bool live = row + j < a.R;  // a row that is not there has no columns: zeros, nothing stored
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int c = (t + i * NT) * 8;
-        float o[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = a.x_scale * d[i][e];
-        store8((XT*)a.dx + base + c, C - c, o);
+        const uint32_t c = (t + i * NT) * 8 - shift;
+        const int64_t base = (row + j) * a.C;
+        const int m = count(i, live);
+        if constexpr (WHOLE) {
+          n[j][i] = y[j][i] = {};
+          r[j][i] = d0[j][i] = {};
+          if (m > 0) {
+            if (has_n) {
+              n[j][i].load_all(a.dn + base + c);
+              r[j][i].load_all((const XT*)a.r + base + c);
+            }
+            if (a.dr != nullptr) d0[j][i].load_all((const XT*)a.dr + base + c);
+            if (has_y) y[j][i].load_all(a.y + base + c);
+          }
+        } else {
+          if (has_n) {
+            n[j][i].load(a.dn + base + c, m);
+            r[j][i].load((const XT*)a.r + base + c, m);
+          }
+          if (a.dr != nullptr) d0[j][i].load((const XT*)a.dr + base + c, m);
+          if (has_y) y[j][i].load(a.y + base + c, m);
+        }
       }
+      rr[j] = has_n && live ? a.rstd_r[row + j] : 0.0f;
+      ry[j] = a.post_w == nullptr ? 1.0f : live ? a.rstd_y[row + j] : 0.0f;
+      gate[j] = a.gate_kind != BSFP8_GATE_TOKEN ? 1.0f : live ? a.gate[row + j] : 0.0f;
+      q[j] = 0.0f;
+    }
+    if constexpr (!HOLD) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) load_factors(a, (t + i * NT) * 8, C - (t + i * NT) * 8, wq[i], wp[i]);
+    }
+    // through the norm before the next block: d = dr + rr (g1 - rh mean(g1 rh))
+    if (has_n) {
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j)
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float rh = r[j][i][e] * rr[j], nr = n[j][i][e] * rh;
+            sum_pre[i][e] += nr;
+            q[j] = __builtin_fmaf(nr, wq[i][e], q[j]);
+          }
+      __builtin_amdgcn_sched_barrier(0);  // (each phase's temporaries end with it: registers)
+      row_sum(q);
+    }
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
+      const float m = q[j] * inv_c * rr[j];
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          d[j][i][e] = a.dr != nullptr ? d0[j][i][e] : 0.0f;
+          if (has_n)
+            d[j][i][e] = __builtin_fmaf(rr[j], __builtin_fmaf(-r[j][i][e], m, n[j][i][e] * wq[i][e]), d[j][i][e]);
+        }
+        if (a.dx != nullptr) {
+          const uint32_t c = (t + i * NT) * 8 - shift;
+          float o[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = a.x_scale * d[j][i][e];
+          put8((XT*)a.dx + (row + j) * a.C + c, count(i, row + j < a.R), o);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
     if (!has_y) continue;
     // through the gate and the norm after the block: with t = y_scale d and u = t (post_weight + offset)
     // (channel gate), g2 = (token gate) u and the token gate's gradient is the sum of u yh
-    q = 0.0f;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
+    for (int j = 0; j < ROWS; ++j) {
+      q[j] = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float back = a.y_scale * d[i][e];
-        rh[i][e] = ycur[i][e] * ry;  // yh from here on
-        sum_y[i][e] = __builtin_fmaf(gate * back, rh[i][e], sum_y[i][e]);
-        d[i][e] = back * wp[i][e];
-        q = __builtin_fmaf(d[i][e], rh[i][e], q);
-      }
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float back = a.y_scale * d[j][i][e], by = back * (y[j][i][e] * ry[j]);
+          sum_y[i][e] = __builtin_fmaf(gate[j], by, sum_y[i][e]);
+          q[j] = __builtin_fmaf(by, wp[i][e], q[j]);
+          d[j][i][e] = back * wp[i][e];
+        }
+      __builtin_amdgcn_sched_barrier(0);
+    }
     const bool token = a.gate_kind == BSFP8_GATE_TOKEN && a.dgate != nullptr;
     if (a.post_w != nullptr || token) {
-      q = row_sum(q);
-      if (token && t == 0) a.dgate[row] = q;
+      row_sum(q);
+      if (token && t == 0) {
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j)
+          if (row + j < a.R) a.dgate[row + j] = q[j];
+      }
     }
     if (a.dy != nullptr) {
-      const float m = a.post_w != nullptr ? q * inv_c : 0.0f, k = ry * gate;
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int c = (t + i * NT) * 8;
+      for (int j = 0; j < ROWS; ++j) {
+        const float m = a.post_w != nullptr ? q[j] * inv_c * ry[j] : 0.0f, k = ry[j] * gate[j];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[i][e] = k * __builtin_fmaf(-rh[i][e], m, d[i][e]);
-        store8(a.dy + base + c, C - c, d[i]);
+        for (int i = 0; i < VPT; ++i) {
+          const uint32_t c = (t + i * NT) * 8 - shift;
+          float o[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = k * __builtin_fmaf(-y[j][i][e], m, d[j][i][e]);
+          put8(a.dy + (row + j) * a.C + c, count(i, row + j < a.R), o);
+        }
       }
     }
   }
@@ -352,8 +454,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void residual_norm_grad_kernel(N
           for (int i = 0; i < VPT; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              float* p = &tot[(t + i * 64) * 8 + e];
-              *p = w == 0 ? s[i][e] : *p + s[i][e];
+              float* p = &tot[(t + i * 64) * 8 - shift + e];
+              if (e >= shift) *p = w == 0 ? s[i][e] : *p + s[i][e];
             }
         }
         __syncthreads();
@@ -363,8 +465,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void residual_norm_grad_kernel(N
     } else {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int c = (t + i * NT) * 8;
-        store8(out + which * a.C + c, C - c, s[i]);
+        const int c = (t + i * NT) * 8 - shift;
+        put8(out + which * a.C + c, C - (t + i * NT) * 8, s[i]);
       }
     }
   };
@@ -416,10 +518,13 @@ __global__ __launch_bounds__(1024) void residual_norm_reduce_kernel(NormReduceAr
 
 template <class XT, bool GRAD, bool WAVE, int VPT>
 static int launch_norm(const NormArgs& a, int64_t blocks, int threads, hipStream_t stream) {
-  if constexpr (GRAD)
-    hipLaunchKernelGGL((residual_norm_grad_kernel<XT, WAVE, VPT>), dim3((unsigned)blocks), dim3(threads), 0, stream, a);
+  const dim3 grid((unsigned)blocks), block(threads);
+  if constexpr (!GRAD)
+    hipLaunchKernelGGL((residual_norm_kernel<XT, WAVE, VPT>), grid, block, 0, stream, a);
+  else if (VPT == 1 && norm_grad_rows(a.C) == 2)
+    hipLaunchKernelGGL((residual_norm_grad_kernel<XT, WAVE, VPT, VPT == 1 ? 2 : 1>), grid, block, 0, stream, a);
   else
-    hipLaunchKernelGGL((residual_norm_kernel<XT, WAVE, VPT>), dim3((unsigned)blocks), dim3(threads), 0, stream, a);
+    hipLaunchKernelGGL((residual_norm_grad_kernel<XT, WAVE, VPT, 1>), grid, block, 0, stream, a);
   return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
 }
 

@@ -21,17 +21,19 @@ inline NormShape norm_shape(int64_t cols) {
   return {false, vpt, 64 * (int)((cols + 512 * vpt - 1) / (512 * vpt))};
 }
 
-// Workgroups: as many as fill the chip with `waves` waves per CU, each walking every gridDim-th row.
-inline int64_t norm_fill(int64_t rows, int64_t cols, int64_t waves) {
+// Workgroups: as many as fill the chip with `waves` waves per CU, each walking every gridDim-th set of
+// `rows_at_once` rows (per wave or per workgroup).
+inline int64_t norm_fill(int64_t rows, int64_t cols, int64_t waves, int rows_at_once) {
   const NormShape s = norm_shape(cols);
-  const int64_t rpb = s.wave ? 4 : 1, need = (rows + rpb - 1) / rpb, per = waves / (s.threads / 64);
+  const int64_t rpb = (s.wave ? 4 : 1) * rows_at_once, need = (rows + rpb - 1) / rpb, per = waves / (s.threads / 64);
   const int64_t most = kNormCus * (per < 1 ? 1 : per);
   return need < most ? need : most;
 }
 
-inline int64_t norm_blocks(int64_t rows, int64_t cols) { return norm_fill(rows, cols, 32); }
+inline int64_t norm_blocks(int64_t rows, int64_t cols) { return norm_fill(rows, cols, 28, 1); }
 
-// Gradient: as many workgroups as partial rows.
-inline int64_t norm_grad_slots(int64_t rows, int64_t cols) { return norm_fill(rows, cols, 16); }
+// Rows that the gradient takes at once, and its workgroups, as many as partial rows.
+inline int norm_grad_rows(int64_t cols) { return cols >= 8 && cols <= 8192 ? 2 : 1; }
+inline int64_t norm_grad_slots(int64_t rows, int64_t cols) { return norm_fill(rows, cols, 16, norm_grad_rows(cols)); }
 
 }  // namespace bsfp8
