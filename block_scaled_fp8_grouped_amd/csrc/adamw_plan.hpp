@@ -8,8 +8,7 @@
 
 namespace bsfp8 {
 
-constexpr int kAdamThreads = 256;
-constexpr int64_t kAdamChunk = 2048;  // elements per workgroup: 8 per thread, whole 128-element blocks
+constexpr int64_t kAdamChunk = 2048;  // elements of a workgroup's turn: whole 128-element blocks
 
 typedef bsfp8_adamw_tensor AdamTensor;
 

@@ -41,6 +41,7 @@ struct NormArgs {
   uint16_t* dy;
   float *dgate, *partial;  // dgate: per token; partial: [slots][2][C] (the pre_weight sum, the y sum)
   int need;                // sums to keep: 1 the pre_weight sum, 2 the y sum
+  bool stream;             // row outputs past the caches
 };
 
 __device__ __forceinline__ float to_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
@@ -88,13 +89,24 @@ __device__ __forceinline__ void load8(const T* p, int n, float* v) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = r[i];
 }
+// 8 elements past the caches, any alignment of the element's size.
+__device__ __forceinline__ void stream8(float* p, const float* t) {
+  typedef float V __attribute__((ext_vector_type(4), aligned(4)));
+  __builtin_nontemporal_store(V{t[0], t[1], t[2], t[3]}, (V*)p);
+  __builtin_nontemporal_store(V{t[4], t[5], t[6], t[7]}, (V*)p + 1);
+}
+__device__ __forceinline__ void stream8(uint16_t* p, const uint16_t* t) {
+  typedef uint16_t V __attribute__((ext_vector_type(8), aligned(2)));
+  __builtin_nontemporal_store(V{t[0], t[1], t[2], t[3], t[4], t[5], t[6], t[7]}, (V*)p);
+}
 template <class T>
-__device__ __forceinline__ void store8(T* p, int n, const float* v) {
+__device__ __forceinline__ void store8(T* p, int n, const float* v, bool past_caches = false) {
   T t[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) from_f32(v[i], t[i]);
   if (n >= 8) {
-    __builtin_memcpy(p, t, sizeof(t));
+    if (past_caches) stream8(p, t);
+    else __builtin_memcpy(p, t, sizeof(t));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -252,7 +264,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024, VPT == 1 ? 7 : 4) void residual_
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int c = (t + i * NT) * 8;
-        store8((XT*)a.r + base + c, C - c, x[i]);
+        store8((XT*)a.r + base + c, C - c, x[i], a.stream);
       }
     }
     if (a.pre_w != nullptr) {
@@ -269,7 +281,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024, VPT == 1 ? 7 : 4) void residual_
         const int c = (t + i * NT) * 8;
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[i][e] = x[i][e] * rr * wq[i][e];
-        store8(a.n + base + c, C - c, x[i]);
+        store8(a.n + base + c, C - c, x[i], a.stream);
       }
     }
   }
@@ -308,11 +320,11 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void residual_norm_grad_kernel(N
   const int wave_row = WAVE ? __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) * ROWS : 0;
   // elements of this thread's chunk i that exist
   auto count = [&](int i, bool live) { return live ? C - (t + i * NT) * 8 : 0; };
-  auto put8 = [&](auto* p, int n, const float* v) {
+  auto put8 = [&](auto* p, int n, const float* v, bool stream) {
     if constexpr (WHOLE) {
       if (n > 0) {
         if (shift == 0) {
-          store8(p, 8, v);
+          store8(p, 8, v, stream);
         } else {
 #pragma unroll
           for (int e = 1; e < 8; ++e)
@@ -320,7 +332,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void residual_norm_grad_kernel(N
         }
       }
     } else {
-      store8(p, n, v);
+      store8(p, n, v, stream);
     }
   };
   for (int64_t row = (int64_t)blockIdx.x * RPB + wave_row; row < a.R; row += stride) {
@@ -395,7 +407,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void residual_norm_grad_kernel(N
           float o[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[e] = a.x_scale * d[j][i][e];
-          put8((XT*)a.dx + (row + j) * a.C + c, count(i, row + j < a.R), o);
+          put8((XT*)a.dx + (row + j) * a.C + c, count(i, row + j < a.R), o, a.stream);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -436,7 +448,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void residual_norm_grad_kernel(N
           float o[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[e] = k * __builtin_fmaf(-y[j][i][e], m, d[j][i][e]);
-          put8(a.dy + (row + j) * a.C + c, count(i, row + j < a.R), o);
+          put8(a.dy + (row + j) * a.C + c, count(i, row + j < a.R), o, a.stream);
         }
       }
     }
@@ -466,7 +478,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void residual_norm_grad_kernel(N
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int c = (t + i * NT) * 8 - shift;
-        put8(out + which * a.C + c, C - (t + i * NT) * 8, s[i]);
+        put8(out + which * a.C + c, C - (t + i * NT) * 8, s[i], false);
       }
     }
   };
@@ -528,8 +540,13 @@ static int launch_norm(const NormArgs& a, int64_t blocks, int threads, hipStream
   return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
 }
 
+// Row outputs of at least this many elements each go past the caches: two of them would fill the last-level
+// cache, and the next pass would not find their beginning there (32768 x 7168: gradient 540 -> 513 us).
+constexpr int64_t kNormStreamElements = int64_t(1) << 26;
+
 template <class XT, bool GRAD>
-static int dispatch_norm(const NormArgs& a, hipStream_t stream) {
+static int dispatch_norm(NormArgs& a, hipStream_t stream) {
+  a.stream = a.R * a.C >= kNormStreamElements;
   const NormShape s = norm_shape(a.C);
   const int64_t blocks = GRAD ? norm_grad_slots(a.R, a.C) : norm_blocks(a.R, a.C);
   if (s.wave) return launch_norm<XT, GRAD, true, 1>(a, blocks, s.threads, stream);
