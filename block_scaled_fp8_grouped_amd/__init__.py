@@ -450,9 +450,18 @@ def _like(t, shape, what, dtype=None):
     if t is None:
         return
     if t.shape != shape:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {None if shape is None else tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
+
+
+def _out(t, shape, what, dtypes):
+    """Pointer of an output tensor that the caller gave, of this shape and one of these types, or None."""
+    if t is None:
+        return None
+    p = _dev(t, what, dtypes)
+    _like(t, shape, what)
+    return p
 
 
 def _check_norm_block(shape, y, post_weight, pre_weight, gate, gate_kind):
@@ -481,33 +490,45 @@ def residual_norm(x, y=None, post_weight=None, pre_weight=None, gate=None, gate_
     if x.dim() != 2:
         raise ValueError("residual_norm: x is [rows, cols]")
     shape = rows, cols = x.shape
-    args = (_dev(x, "x", _STREAM), F32 if x.dtype is torch.float32 else BF16, _dev(y, "y", _BF16),
-            _dev(post_weight, "post_weight", _F32), _dev(pre_weight, "pre_weight", _F32), _dev(gate, "gate", _F32))
+    px = _dev(x, "x", _STREAM)
+    py, pw, qw = _dev(y, "y", _BF16), _dev(post_weight, "post_weight", _F32), _dev(pre_weight, "pre_weight", _F32)
+    pg = _dev(gate, "gate", _F32)
     _check_norm_block(shape, y, post_weight, pre_weight, gate, gate_kind)
-    dev = x.device
-    out = {}
+    # given tensors are checked, new ones are as they have to be
+    out, pn, prr, pry = {}, None, None, None
     if r is None:
-        r = torch.empty_like(x)
+        out["r"] = r = torch.empty_like(x)
+        pr = r.data_ptr()
     else:
-        _like(r, shape, "r", x.dtype)
-    out["r"] = r
+        out["r"], pr = r, _out(r, shape, "r", (x.dtype,))
     if pre_weight is not None:
         if n is None:
             n = torch.empty_like(x, dtype=torch.bfloat16)
+            pn = n.data_ptr()
+        else:
+            pn = _out(n, shape, "n", _BF16)
+        out["n"] = n
         if rstd_r is None:
-            rstd_r = torch.empty(rows, dtype=torch.float32, device=dev)
-        out["n"], out["rstd_r"] = n, rstd_r
+            rstd_r = x.new_empty(rows, dtype=torch.float32)
+            prr = rstd_r.data_ptr()
+        else:
+            prr = _out(rstd_r, (rows,), "rstd_r", _F32)
+        out["rstd_r"] = rstd_r
+    else:
+        pn, prr = _out(n, shape, "n", _BF16), _out(rstd_r, (rows,), "rstd_r", _F32)
     if post_weight is not None:
         if rstd_y is None:
-            rstd_y = torch.empty(rows, dtype=torch.float32, device=dev)
+            rstd_y = x.new_empty(rows, dtype=torch.float32)
+            pry = rstd_y.data_ptr()
+        else:
+            pry = _out(rstd_y, (rows,), "rstd_y", _F32)
         out["rstd_y"] = rstd_y
-    _like(n, shape, "n")
-    _like(rstd_y, (rows,), "rstd_y")
-    _like(rstd_r, (rows,), "rstd_r")
-    rc = lib().bsfp8_residual_norm(rows, cols, *args, gate_kind, x_scale, y_scale, eps, weight_offset,
-                                   _dev(r, "r", _STREAM), _dev(n, "n", _BF16), _dev(rstd_y, "rstd_y", _F32),
-                                   _dev(rstd_r, "rstd_r", _F32), _stream(stream))
-    _check(rc, "residual_norm")
+    else:
+        pry = _out(rstd_y, (rows,), "rstd_y", _F32)
+    rc = lib().bsfp8_residual_norm(rows, cols, px, F32 if x.dtype is torch.float32 else BF16, py, pw, qw, pg, gate_kind,
+                                   x_scale, y_scale, eps, weight_offset, pr, pn, pry, prr, _stream(stream))
+    if rc:
+        _check(rc, "residual_norm")
     return out
 
 
@@ -530,7 +551,7 @@ def residual_norm_grad(dn, dr, r=None, rstd_r=None, pre_weight=None, y=None, rst
     if ref.dim() != 2:
         raise ValueError("residual_norm_grad: r and dr are [rows, cols]")
     shape = rows, cols = ref.shape
-    dev, dtype = ref.device, ref.dtype
+    dtype = ref.dtype
     args = (F32 if dtype is torch.float32 else BF16, _dev(dn, "dn", _BF16), _dev(dr, "dr", _STREAM),
             _dev(r, "r", _STREAM), _dev(rstd_r, "rstd_r", _F32), _dev(pre_weight, "pre_weight", _F32),
             _dev(y, "y", _BF16), _dev(rstd_y, "rstd_y", _F32), _dev(post_weight, "post_weight", _F32),
@@ -546,33 +567,34 @@ def residual_norm_grad(dn, dr, r=None, rstd_r=None, pre_weight=None, y=None, rst
             (gate if gate_kind == GATE_CHANNEL else None, dgate))):
         raise ValueError("residual_norm_grad: accumulate needs the gradients to add to")
     out = {}
-    if dx is None:
-        dx = torch.empty_like(ref)
-    else:
-        _like(dx, shape, "dx", dtype)
-    out["dx"] = dx
-    if y is not None:
-        out["dy"] = dy = torch.empty_like(y) if dy is None else dy
-    if pre_weight is not None:
-        out["dpre_weight"] = dpre_weight = torch.empty_like(pre_weight) if dpre_weight is None else dpre_weight
-    if post_weight is not None:
-        out["dpost_weight"] = dpost_weight = torch.empty_like(post_weight) if dpost_weight is None else dpost_weight
-    if gate is not None:
-        out["dgate"] = dgate = torch.empty_like(gate) if dgate is None else dgate
-        _like(dgate, gate.shape, "dgate")
-    _like(dy, shape, "dy")
-    _like(dpre_weight, (cols,), "dpre_weight")
-    _like(dpost_weight, (cols,), "dpost_weight")
+
+    def put(name, given, like, out_shape, dtypes):
+        # the pointer of an output: the tensor given, or a new one where the call has what it is the gradient of
+        if given is None:
+            if like is None:
+                return None
+            given = torch.empty_like(like)
+            out[name] = given
+            return given.data_ptr()
+        if like is not None:
+            out[name] = given
+        return _out(given, out_shape, name, dtypes)
+
+    pdx = put("dx", dx, ref, shape, (dtype,))
+    pdy = put("dy", dy, y, shape, _BF16)
+    pre = put("dpre_weight", dpre_weight, pre_weight, (cols,), _F32)
+    post = put("dpost_weight", dpost_weight, post_weight, (cols,), _F32)
+    pgate = put("dgate", dgate, gate, None if gate is None else gate.shape, _F32)
     need = residual_norm_grad_workspace_bytes(rows, cols)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = ref.new_empty(need, dtype=torch.uint8)
     else:
         _need(workspace, need, "workspace")
     rc = lib().bsfp8_residual_norm_grad(
-        rows, cols, *args, gate_kind, x_scale, y_scale, weight_offset, _dev(dx, "dx", _STREAM), _dev(dy, "dy", _BF16),
-        _dev(dpre_weight, "dpre_weight", _F32), _dev(dpost_weight, "dpost_weight", _F32), _dev(dgate, "dgate", _F32),
+        rows, cols, *args, gate_kind, x_scale, y_scale, weight_offset, pdx, pdy, pre, post, pgate,
         1 if accumulate else 0, _dev(workspace, "workspace", (workspace.dtype,)), _stream(stream))
-    _check(rc, "residual_norm_grad")
+    if rc:
+        _check(rc, "residual_norm_grad")
     return out
 
 
