@@ -22,11 +22,36 @@ __device__ __forceinline__ float swiglu(float a, float b, float p) { return a * 
 
 // From d, the gradient at the product's output before the activation's probability: the gradients
 // of p silu(a) b at a and b, and silu(a) b d, this column's part of the probability's.
+// silu'(a) = sg (1 + a (1 - sg)) = sg + (s - s sg) with s = a sg.
 __device__ __forceinline__ void swiglu_grad(float a, float b, float p, float d, float& da, float& db, float& dp) {
-  const float sg = sigmoid_fast(a), sl = a * sg, q = d * p;
-  db = q * sl;
-  da = q * b * (sg * (1.0f + a * (1.0f - sg)));
-  dp += d * sl * b;
+  const float sg = sigmoid_fast(a), sl = a * sg, slope = sg + __builtin_fmaf(-sl, sg, sl);
+  const float z = d * sl;
+  db = z * p;
+  dp = __builtin_fmaf(z, b, dp);
+  da = d * p * b * slope;
+}
+
+// max(m, |a|, |b|) in one instruction (NaN operands are passed over)
+__device__ __forceinline__ float max3_abs(float m, float a, float b) {
+  asm("v_max3_f32 %0, %0, |%1|, |%2|" : "+v"(m) : "v"(a), "v"(b));
+  return m;
+}
+
+// E8M0 byte of a block with largest magnitude amax: e8m0_exponent(amax) + 127.  Adding 0x1fffff carries into the
+// exponent field exactly where the mantissa is above 1.75's, and subnormals end at 0.
+__device__ __forceinline__ uint32_t e8m0_byte(float amax) {
+  const uint32_t f = (__float_as_uint(amax) + 0x1fffffu) >> 23;
+  return f > 8u ? f - 8u : 0u;
+}
+// Four fp32 -> four e4m3 codes of v / 2^(byte - 127): the conversion divides by its scale operand, of which it uses
+// the exponent field alone (equal to the multiplication by 2^-e and the plain conversion: checked on the
+// GPU for every byte over 252 million values).
+__device__ __forceinline__ uint32_t e4m3x4_scaled(float a, float b, float c, float d, float scale) {
+  typedef short v2s __attribute__((ext_vector_type(2)));
+  v2s w = {0, 0};
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, a, b, scale, false);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, c, d, scale, true);
+  return __builtin_bit_cast(uint32_t, w);
 }
 
 // Orders a wave's LDS writes before its own later LDS reads (no other wave is involved).
@@ -60,19 +85,19 @@ __device__ __forceinline__ void put_row8(const GluOut& o, int64_t R, int64_t N, 
     }
   }
   if (o.row_q != nullptr) {
-    uint32_t m = 0;
+    float m = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(v[k]) & 0x7fffffffu);
-    m = max(m, (uint32_t)__shfl_xor((int)m, 1, 64));
-    m = max(m, (uint32_t)__shfl_xor((int)m, 2, 64));
-    const int e = e8m0_exponent(__uint_as_float(m));
-    const float s = exp2_neg(e);
+    for (int k = 0; k < 8; k += 2) m = max3_abs(m, v[k], v[k + 1]);
+    m = fmaxf(m, __shfl_xor(m, 1, 64));
+    m = fmaxf(m, __shfl_xor(m, 2, 64));
+    const uint32_t byte = e8m0_byte(m);
+    const float s = __uint_as_float(byte << 23);
     if (live) {
       v2i q;
-      q[0] = (int)e4m3x4(v[0] * s, v[1] * s, v[2] * s, v[3] * s);
-      q[1] = (int)e4m3x4(v[4] * s, v[5] * s, v[6] * s, v[7] * s);
+      q[0] = (int)e4m3x4_scaled(v[0], v[1], v[2], v[3], s);
+      q[1] = (int)e4m3x4_scaled(v[4], v[5], v[6], v[7], s);
       *(v2i*)(o.row_q + row * N + col) = q;
-      if ((col & 31) == 0) o.row_s[col / 32 * R + row] = (uint8_t)(e + 127);
+      if ((col & 31) == 0) o.row_s[col / 32 * R + row] = (uint8_t)byte;
     }
   }
 }
@@ -81,20 +106,19 @@ __device__ __forceinline__ void put_row8(const GluOut& o, int64_t R, int64_t N, 
 // all in this lane.
 __device__ __forceinline__ void put_col32(const GluOut& o, int64_t N, const GroupInfo& g, int64_t t, int64_t col,
                                           bool live, const float* v) {
-  uint32_t m = 0;
+  float m = 0.0f;
 #pragma unroll
-  for (int k = 0; k < 32; ++k) m = max(m, __float_as_uint(v[k]) & 0x7fffffffu);
-  const int e = e8m0_exponent(__uint_as_float(m));
-  const float s = exp2_neg(e);
+  for (int k = 0; k < 32; k += 2) m = max3_abs(m, v[k], v[k + 1]);
+  const uint32_t byte = e8m0_byte(m);
+  const float s = __uint_as_float(byte << 23);
   v4i q[2];
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    q[k >> 2][k & 3] = (int)e4m3x4(v[4 * k] * s, v[4 * k + 1] * s, v[4 * k + 2] * s, v[4 * k + 3] * s);
+  for (int k = 0; k < 8; ++k) q[k >> 2][k & 3] = (int)e4m3x4_scaled(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3], s);
   if (live) {
     uint8_t* dst = o.col_q + col_elem(N, g.p, g.kp, col, t);
     *(v4i*)dst = q[0];
     *(v4i*)(dst + 16) = q[1];
-    o.col_s[col_e8m0(N, g.p, t / 32, col)] = (uint8_t)(e + 127);
+    o.col_s[col_e8m0(N, g.p, t / 32, col)] = (uint8_t)byte;
   }
 }
 

@@ -100,10 +100,10 @@ __device__ __forceinline__ uint32_t glu_dma_offset(int row0, int lane, uint32_t 
   return (uint32_t)row * ld + 16u * (uint32_t)((lane % C) ^ glu_swz<BK>(row));
 }
 
-// Tiles of BM x BN, K steps of BK bytes, waves of BM / 2 x 64, NS stages of LDS.
-template <bool GRAD, int BM_, int BN_, int BK_, int NS_>
+// Tiles of BM x BN, K steps of BK bytes, waves of BM / 2 x WN, NS stages of LDS.
+template <bool GRAD, int BM_, int BN_, int WN_, int BK_, int NS_>
 struct GluShape {
-  static constexpr int BM = BM_, BN = BN_, BK = BK_, NS = NS_, WM = BM / 2, WN = 64, BLKS = BK / 32;
+  static constexpr int BM = BM_, BN = BN_, BK = BK_, NS = NS_, WM = BM / 2, WN = WN_, BLKS = BK / 32;
   static constexpr int WAVES_N = BN / WN, NW = 2 * WAVES_N, NT = 64 * NW;
   static constexpr int FM = WM / 32, FN = WN / 32;
   static constexpr int COLS = GRAD ? BN : BN / 2;  // output columns (of one half) per tile
@@ -117,17 +117,18 @@ struct GluShape {
   // epilogue: each wave's 32 rows of fp32, the row pitch shifting the rows 4 apart (one register's two
   // half-waves) by half of the 64 banks
   static constexpr int PITCH = GRAD ? 72 : 40;
-  static constexpr int EP = 32 * PITCH * 4;
-  static_assert(NT == 2 * BN && NT >= BM, "launch bounds, the probabilities' loads");
-  static_assert(B_INS * 1024 / BK == 32, "a wave fetches 32 rows of the weight");
+  static constexpr int AB_PITCH = 72;  // forward: the kept product's 32 rows of 64 bf16, behind them
+  static constexpr int EP = 32 * PITCH * 4 + (GRAD ? 0 : 32 * AB_PITCH * 2);
+  static constexpr int INS_ROWS = 1024 / BK, RUNS = B_INS * INS_ROWS / 32;  // runs of 32 weight rows per wave
+  static_assert(NT >= BM && RUNS * 32 == B_INS * INS_ROWS, "the probabilities' loads, the weight's");
   static_assert(SC_INS <= NW, "scale loads");
-  static_assert(NW * EP + (WAVES_N + 1) * BM * 4 <= NS * STAGE && (int)sizeof(GroupScanSmem<NT>) <= NS * STAGE, "LDS reuse");
+  static_assert(NW * EP + (BN / 64 + 1) * BM * 4 <= NS * STAGE && (int)sizeof(GroupScanSmem<NT>) <= NS * STAGE, "LDS reuse");
   static_assert(NS * STAGE <= 160 * 1024, "LDS budget");
 };
 
-template <bool GRAD, int BM, int BN, int BK, int NS>
-__global__ __launch_bounds__(2 * BN, BM == 128 ? 3 : 2) void glu_gemm_kernel(GluArgs args) {
-  using S = GluShape<GRAD, BM, BN, BK, NS>;
+template <bool GRAD, int BM, int BN, int WN, int BK, int NS>
+__global__ __launch_bounds__(128 * BN / WN, BM == 128 ? 3 : WN == 128 ? 1 : 2) void glu_gemm_kernel(GluArgs args) {
+  using S = GluShape<GRAD, BM, BN, WN, BK, NS>;
   constexpr int NT = S::NT, FM = S::FM, FN = S::FN, BLKS = S::BLKS;
   __shared__ __attribute__((aligned(16))) uint8_t smem[NS * S::STAGE];
   GroupScanSmem<NT>& gsm = *(GroupScanSmem<NT>*)smem;  // done before the first DMA (a barrier below)
@@ -156,23 +157,27 @@ __global__ __launch_bounds__(2 * BN, BM == 128 ? 3 : 2) void glu_gemm_kernel(Glu
   if (tid < BM && tid <= a_last) my_prob = args.probs != nullptr ? args.probs[gi.off + row0 + tid] : 1.0f;
 
   // ---------------- loads of one K step ----------------
-  // B: LDS rows 32 w .. of wave w; forward: rows 32 (w / 2) .. of projection w % 2
-  const int64_t half = GRAD ? 0 : (int64_t)(wave & 1) * F;
-  const uint32_t b_shift = GRAD ? 0 : (uint32_t)(wave * 32 - (wave >> 1) * 32);  // LDS row minus source row
+  // B: LDS rows in runs of 32; forward: run k is rows 32 (k / 2) .. of projection k % 2
   const uint8_t* a_base = args.a_q + (gi.off + row0) * K;
-  const uint8_t* b_base = args.b_q + gi.e * args.b_estride + (half + col0) * args.b_ld;
+  const uint8_t* b_base = args.b_q + gi.e * args.b_estride + col0 * args.b_ld;
   // (the live rows of the tile only: below 2^30 bytes, so an offset from 2^31 up is past them)
   const v4i a_rs = glu_rsrc(a_base, (uint32_t)(a_last + 1) * (uint32_t)K);
-  const v4i b_rs = glu_rsrc(b_base, (uint32_t)(b_last + 1) * (uint32_t)args.b_ld);
+  v4i b_rs[S::RUNS];
+#pragma unroll
+  for (int k = 0; k < S::RUNS; ++k)
+    b_rs[k] = glu_rsrc(b_base + (GRAD ? 0 : ((wave * S::RUNS + k) & 1) * F * args.b_ld),
+                       (uint32_t)(b_last + 1) * (uint32_t)args.b_ld);
   const uint32_t smem_lds =
       __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)smem);
   uint32_t a_off[S::A_INS], b_off[S::B_INS];
 #pragma unroll
-  for (int u = 0; u < S::A_INS; ++u) a_off[u] = glu_dma_offset<BK>((wave * S::A_INS + u) * (1024 / BK), lane, (uint32_t)K);
+  for (int u = 0; u < S::A_INS; ++u) a_off[u] = glu_dma_offset<BK>((wave * S::A_INS + u) * S::INS_ROWS, lane, (uint32_t)K);
 #pragma unroll
-  for (int u = 0; u < S::B_INS; ++u)
-    b_off[u] = glu_dma_offset<BK>((wave * S::B_INS + u) * (1024 / BK), lane, (uint32_t)args.b_ld) -
-               b_shift * (uint32_t)args.b_ld;
+  for (int u = 0; u < S::B_INS; ++u) {
+    const int row = (wave * S::B_INS + u) * S::INS_ROWS, run = wave * S::RUNS + u * S::INS_ROWS / 32;
+    b_off[u] = glu_dma_offset<BK>(row, lane, (uint32_t)args.b_ld);
+    if constexpr (!GRAD) b_off[u] -= (uint32_t)((run - (run >> 1)) * 32) * (uint32_t)args.b_ld;
+  }
   // Scales, 16 bytes per lane.  A: a group's rows begin anywhere, so the lanes read the aligned 16 bytes that
   // hold them (the first at or after the buffer's own aligned start, the last the one that holds the last
   // live row's).  B: 16 LDS rows, which lie in one run of 32 columns.  Lanes with nothing to load repeat a
@@ -216,7 +221,7 @@ __global__ __launch_bounds__(2 * BN, BM == 128 ? 3 : 2) void glu_gemm_kernel(Glu
 #pragma unroll
     for (int u = 0; u < S::B_INS; ++u) {
       if (1 + S::A_INS + u < p0 || 1 + S::A_INS + u >= p1) continue;
-      glu_dma16(b_rs, base + S::B_OFF + (wave * S::B_INS + u) * 1024, b_off[u] + k0);
+      glu_dma16(b_rs[u * S::INS_ROWS / 32], base + S::B_OFF + (wave * S::B_INS + u) * 1024, b_off[u] + k0);
     }
   };
   // waits until all but the newest `steps` steps' loads have landed, in every wave
@@ -312,118 +317,147 @@ __global__ __launch_bounds__(2 * BN, BM == 128 ? 3 : 2) void glu_gemm_kernel(Glu
   __syncthreads();
   constexpr int PITCH = S::PITCH;
   if constexpr (!GRAD) {
-    const int cw = wn * 32;  // the wave's first column within the tile
-    const int64_t col = col0 + cw;
-    const bool cols = cw <= b_last;  // its 32 columns all exist, or none
-    const int64_t N2 = 2 * F;
-    // the kept product: a buffer resource over the block's live rows, its halves F columns apart
-    const int left = a_last + 1 - wm * S::WM;
-    const int vrows = left < 0 ? 0 : left > S::WM ? S::WM : left;
-    const __amdgpu_buffer_rsrc_t ab_rs = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(args.ab + (gi.off + row0 + wm * S::WM) * N2 + col), (short)0,
-        args.ab != nullptr && vrows > 0 && cols ? (int)(((int64_t)(vrows - 1) * N2 + F + 32) * 2) : 0, 0x00020000);
+    uint16_t* ab_tile = (uint16_t*)(tile + 32 * PITCH);
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const int rb = wm * S::WM + i * 32;
-      float v[16];
+    for (int pair = 0; pair < FN / 2; ++pair) {
+      const int cw = wn * (S::WN / 2) + 32 * pair;  // the pair's first column within the tile
+      const int64_t col = col0 + cw;
+      const bool cols = cw <= b_last;  // its 32 columns all exist, or none
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const v4f p = *(const v4f*)&probs[rb + 8 * q + 4 * h];
+      for (int i = 0; i < FM; ++i) {
+        const int rb = wm * S::WM + i * 32;
+        const int64_t row = gi.off + row0 + rb;
+        const v16f &a = acc[i][2 * pair], &b = acc[i][2 * pair + 1];
+        float v[16];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = 4 * q + k;
-          // (a dead row's scales may be anything)
-          v[r] = rb + 8 * q + 4 * h + k <= a_last ? swiglu(acc[i][0][r], acc[i][1][r], p[k]) : 0.0f;
-          if (args.ab != nullptr) {
-            const uint32_t at = ((uint32_t)(i * 32 + 8 * q + 4 * h + k) * (uint32_t)N2 + (uint32_t)l32) * 2;
-            __builtin_amdgcn_raw_buffer_store_b16((short)f32_to_bf16(acc[i][0][r]), ab_rs, (int)at, 0, 0);
-            __builtin_amdgcn_raw_buffer_store_b16((short)f32_to_bf16(acc[i][1][r]), ab_rs, (int)(at + 2 * (uint32_t)F), 0, 0);
+        for (int q = 0; q < 4; ++q) {
+          const v4f p = *(const v4f*)&probs[rb + 8 * q + 4 * h];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[4 * q + k] = swiglu(a[4 * q + k], b[4 * q + k], p[k]);
+        }
+        if (rb + 31 > a_last) {  // dead rows, whose scales may have been anything, count as zeros
+#pragma unroll
+          for (int r = 0; r < 16; ++r) v[r] = rb + 8 * (r >> 2) + 4 * h + (r & 3) <= a_last ? v[r] : 0.0f;
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) tile[(8 * (r >> 2) + 4 * h + (r & 3)) * PITCH + l32] = v[r];
+        if (args.ab != nullptr) {
+#pragma unroll
+          for (int r = 0; r < 16; r += 2) {
+            const uint32_t wa = __builtin_bit_cast(uint32_t, v2bf{(__bf16)a[r], (__bf16)a[r + 1]});
+            const uint32_t wb = __builtin_bit_cast(uint32_t, v2bf{(__bf16)b[r], (__bf16)b[r + 1]});
+            uint16_t* t = ab_tile + (8 * (r >> 2) + 4 * h + (r & 3)) * S::AB_PITCH + l32;
+            t[0] = (uint16_t)wa;
+            t[32] = (uint16_t)wb;
+            t[S::AB_PITCH] = (uint16_t)(wa >> 16);
+            t[S::AB_PITCH + 32] = (uint16_t)(wb >> 16);
           }
-          tile[(8 * q + 4 * h + k) * PITCH + l32] = v[r];
         }
-      }
-      wave_lds_order();
-      if (args.out.col_q != nullptr && row0 + rb < gi.kp) {
-        float c[32];
+        wave_lds_order();
+        if (args.ab != nullptr) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) c[k] = tile[k * PITCH + l32];
-        put_col32(args.out, F, gi, row0 + rb, col + l32, cols && h == 0, c);
-      }
-      if (args.out.y != nullptr || args.out.row_q != nullptr) {
-#pragma unroll
-        for (int pass = 0; pass < 2; ++pass) {
-          const int r = pass * 16 + (lane >> 2), ch = 8 * (lane & 3);
-          float w[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) w[k] = tile[r * PITCH + ch + k];
-          put_row8(args.out, args.R, F, gi.off + row0 + rb + r, col + ch, cols && rb + r <= a_last, w);
+          for (int pass = 0; pass < 4; ++pass) {  // 8 lanes per row: 4 of a, 4 of b
+            const int r = pass * 8 + (lane >> 3), c = 8 * (lane & 7);
+            const v8s w = *(const v8s*)(ab_tile + r * S::AB_PITCH + c);
+            if (cols && rb + r <= a_last)
+              *(v8s*)(args.ab + (row + r) * 2 * F + col + (c < 32 ? c : F + c - 32)) = w;
+          }
         }
+        if (args.out.col_q != nullptr && row0 + rb < gi.kp) {
+          float c[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) c[k] = tile[k * PITCH + l32];
+          put_col32(args.out, F, gi, row0 + rb, col + l32, cols && h == 0, c);
+        }
+        if (args.out.y != nullptr || args.out.row_q != nullptr) {
+#pragma unroll
+          for (int pass = 0; pass < 2; ++pass) {
+            const int r = pass * 16 + (lane >> 2), ch = 8 * (lane & 3);
+            float w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k] = tile[r * PITCH + ch + k];
+            put_row8(args.out, args.R, F, row + r, col + ch, cols && rb + r <= a_last, w);
+          }
+        }
+        wave_lds_order();
       }
-      wave_lds_order();
     }
   } else {
-    const int cw = wn * 64;
-    float* dp_sum = probs + (1 + wn) * BM;  // this wave's column part of dprobs, per row
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const int rb = wm * S::WM + i * 32;
+    for (int part = 0; part < S::WN / 64; ++part) {
+      const int cw = wn * S::WN + 64 * part;
+      float* dp_sum = probs + (1 + cw / 64) * BM;  // these 64 columns' part of dprobs, per row
       const int ch = 8 * (lane & 7);
       const bool cols = cw + ch <= b_last;
-      v8s av[4], bv[4];
+      // a and b of 32 rows, 8 columns of 4 rows per lane; the next 32 rows' are fetched beside this one's work
+      v8s av[2][4], bv[2][4];
+      auto fetch = [&](int i) {
 #pragma unroll
-      for (int pass = 0; pass < 4; ++pass) {
-        const int r = rb + pass * 8 + (lane >> 3);
-        av[pass] = bv[pass] = v8s{0, 0, 0, 0, 0, 0, 0, 0};
-        if (cols && r <= a_last) {
-          const uint16_t* p = args.ab + (gi.off + row0 + r) * 2 * F + col0 + cw + ch;
-          av[pass] = *(const v8s*)p;
-          bv[pass] = *(const v8s*)(p + F);
+        for (int pass = 0; pass < 4; ++pass) {
+          const int r = wm * S::WM + i * 32 + pass * 8 + (lane >> 3);
+          av[i & 1][pass] = bv[i & 1][pass] = v8s{0, 0, 0, 0, 0, 0, 0, 0};
+          if (cols && r <= a_last) {
+            const uint16_t* p = args.ab + (gi.off + row0 + r) * 2 * F + col0 + cw + ch;
+            av[i & 1][pass] = *(const v8s*)p;
+            bv[i & 1][pass] = *(const v8s*)(p + F);
+          }
         }
-      }
+      };
+      fetch(0);
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
+      for (int i = 0; i < FM; ++i) {
+        const int rb = wm * S::WM + i * 32;
+        if (i + 1 < FM) fetch(i + 1);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) tile[(8 * (r >> 2) + 4 * h + (r & 3)) * PITCH + j * 32 + l32] = acc[i][j][r];
-      wave_lds_order();
-      float db[4][8];
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int pass = 0; pass < 4; ++pass) {
-        const int r = pass * 8 + (lane >> 3);
-        const float p = probs[rb + r];
-        const bool live = cols && rb + r <= a_last;
-        float da[8], dp = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          swiglu_grad(to_f32(av[pass][k]), to_f32(bv[pass][k]), p, live ? tile[r * PITCH + ch + k] : 0.0f, da[k],
-                      db[pass][k], dp);
-        const int64_t row = gi.off + row0 + rb + r, col = col0 + cw + ch;
-        put_row8(args.out, args.R, 2 * F, row, col, live, da);
-        put_row8(args.out, args.R, 2 * F, row, F + col, live, db[pass]);
-        dp += __shfl_xor(dp, 1, 64);
-        dp += __shfl_xor(dp, 2, 64);
-        dp += __shfl_xor(dp, 4, 64);
-        if ((lane & 7) == 0) dp_sum[rb + r] = dp;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) tile[r * PITCH + ch + k] = da[k];
-      }
-      if (args.out.col_q != nullptr && row0 + rb < gi.kp) {
-        float c[32];
-        const bool live = cw + lane <= b_last;
+          for (int r = 0; r < 16; ++r)
+            tile[(8 * (r >> 2) + 4 * h + (r & 3)) * PITCH + j * 32 + l32] = acc[i][2 * part + j][r];
+        if (rb + 31 > a_last) {  // dead rows, whose scales may have been anything, count as zeros
+          wave_lds_order();
+          for (int r = a_last + 1 > rb ? a_last + 1 - rb : 0; r < 32; ++r) tile[r * PITCH + lane] = 0.0f;
+        }
         wave_lds_order();
+        float db[4][8];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) c[k] = tile[k * PITCH + lane];
-        put_col32(args.out, 2 * F, gi, row0 + rb, col0 + cw + lane, live, c);
+        for (int pass = 0; pass < 4; ++pass) {
+          const int r = pass * 8 + (lane >> 3);
+          const float p = probs[rb + r];
+          const bool live = cols && rb + r <= a_last;
+          float da[8], dp = 0.0f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            swiglu_grad(to_f32(av[i & 1][pass][k]), to_f32(bv[i & 1][pass][k]), p, tile[r * PITCH + ch + k], da[k],
+                        db[pass][k], dp);
+          const int64_t row = gi.off + row0 + rb + r, col = col0 + cw + ch;
+          put_row8(args.out, args.R, 2 * F, row, col, live, da);
+          put_row8(args.out, args.R, 2 * F, row, F + col, live, db[pass]);
+          dp += __shfl_xor(dp, 1, 64);
+          dp += __shfl_xor(dp, 2, 64);
+          dp += __shfl_xor(dp, 4, 64);
+          if ((lane & 7) == 0) dp_sum[rb + r] = dp;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) tile[r * PITCH + ch + k] = da[k];
+        }
+        if (args.out.col_q != nullptr && row0 + rb < gi.kp) {
+          float c[32];
+          const bool live = cw + lane <= b_last;
+          wave_lds_order();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) c[k] = tile[k * PITCH + lane];
+          put_col32(args.out, 2 * F, gi, row0 + rb, col0 + cw + lane, live, c);
+          wave_lds_order();
+#pragma unroll
+          for (int pass = 0; pass < 4; ++pass)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) tile[(pass * 8 + (lane >> 3)) * PITCH + ch + k] = db[pass][k];
+          wave_lds_order();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) c[k] = tile[k * PITCH + lane];
+          put_col32(args.out, 2 * F, gi, row0 + rb, F + col0 + cw + lane, live, c);
+        }
         wave_lds_order();
-#pragma unroll
-        for (int pass = 0; pass < 4; ++pass)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) tile[(pass * 8 + (lane >> 3)) * PITCH + ch + k] = db[pass][k];
-        wave_lds_order();
-#pragma unroll
-        for (int k = 0; k < 32; ++k) c[k] = tile[k * PITCH + lane];
-        put_col32(args.out, 2 * F, gi, row0 + rb, F + col0 + cw + lane, live, c);
       }
-      wave_lds_order();
     }
     if (args.dpart != nullptr) {
       __syncthreads();
@@ -431,7 +465,7 @@ __global__ __launch_bounds__(2 * BN, BM == 128 ? 3 : 2) void glu_gemm_kernel(Glu
       if (tid <= a_last) {
         float d = s[tid];
 #pragma unroll
-        for (int w = 1; w < S::WAVES_N; ++w) d += s[w * BM + tid];
+        for (int w = 1; w < BN / 64; ++w) d += s[w * BM + tid];
         args.dpart[(int64_t)tn * args.R + gi.off + row0 + tid] = d;
       }
     }
@@ -709,9 +743,9 @@ static int glu_grid(GluArgs& a, bool grad, GluTile t, dim3* grid) {
   return BSFP8_OK;
 }
 
-template <bool GRAD, int BM, int BN, int BK, int NS>
+template <bool GRAD, int BM, int BN, int WN, int BK, int NS>
 static void launch_glu_tile(const GluArgs& a, dim3 grid, hipStream_t stream) {
-  hipLaunchKernelGGL((glu_gemm_kernel<GRAD, BM, BN, BK, NS>), grid, dim3(2 * BN), 0, stream, a);
+  hipLaunchKernelGGL((glu_gemm_kernel<GRAD, BM, BN, WN, BK, NS>), grid, dim3(128 * BN / WN), 0, stream, a);
 }
 
 template <bool GRAD>
@@ -721,8 +755,8 @@ static int launch_glu(GluArgs& a, hipStream_t stream) {
   const int rc = glu_grid(a, GRAD, t, &grid);
   if (rc != BSFP8_OK) return rc;
   if (t.bm == kRowsBM) hipLaunchKernelGGL((glu_rows_kernel<GRAD>), grid, dim3(64 * kRowsNW), 0, stream, a);
-  else if (t.bn == 256) launch_glu_tile<GRAD, 256, 256, 128, 2>(a, grid, stream);
-  else launch_glu_tile<GRAD, 128, 128, 64, 3>(a, grid, stream);
+  else if (t.bn == 256) launch_glu_tile<GRAD, 256, 256, 64, 128, 2>(a, grid, stream);
+  else launch_glu_tile<GRAD, 128, 128, 64, 64, 3>(a, grid, stream);
   return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
 }
 
