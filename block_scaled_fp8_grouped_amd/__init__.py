@@ -366,10 +366,39 @@ def grouped_gemm_dgrad(dy_q, n, w_q, k, split_sizes, capacity_rows, out, out_dty
 # gated feed-forward projection
 # ------------------------------------------------------------------------------------------
 
-def _which(out):
-    """The layouts that a dict of quantized outputs holds."""
-    out = out or {}
-    return (ROWWISE if out.get("row_q") is not None else 0) | (COLWISE if out.get("col_q") is not None else 0)
+def _buf(t, what, key, dtypes, nbytes):
+    """_dev and _need in one, the argument's name put together only for an error."""
+    if t is None or not isinstance(t, torch.Tensor):
+        return _ptr(t)
+    if t.dtype not in dtypes or not t.is_cuda or not t.is_contiguous():
+        return _dev(t, what if key is None else f"{what}[{key!r}]", dtypes)
+    if t.numel() * t.element_size() < nbytes:
+        _need(t, nbytes, what if key is None else f"{what}[{key!r}]")
+    return t.data_ptr()
+
+
+def _glu_quantized(q, rows, cols, num_groups):
+    """What a dict of quantized outputs [rows, cols] asks for: the layouts and the four pointers."""
+    if not q:
+        return 0, None, None, None, None
+    which, ptrs = 0, [None] * 4
+    if q.get("row_q") is not None:
+        which |= ROWWISE
+        ptrs[0] = _buf(q["row_q"], "out", "row_q", _U8, rows * cols)
+        ptrs[1] = _buf(q.get("row_s"), "out", "row_s", _U8, rows * cols // 32)
+    if q.get("col_q") is not None:
+        which |= COLWISE
+        bound = 128 * ((rows + 127 * num_groups) // 128) if rows else 0
+        ptrs[2] = _buf(q["col_q"], "out", "col_q", _U8, cols * bound)
+        ptrs[3] = _buf(q.get("col_s"), "out", "col_s", _U8, cols * bound // 32)
+    return (which, *ptrs)
+
+
+def _glu_result(q, **more):
+    out = {k: v for k, v in more.items() if v is not None}
+    if q:
+        out.update(q)
+    return out
 
 
 def grouped_gemm_swiglu(x_q, hidden, w_q, ffn, split_sizes, capacity_rows, recipe=RECIPE_MX, probs=None, ab=None,
@@ -379,23 +408,21 @@ def grouped_gemm_swiglu(x_q, hidden, w_q, ffn, split_sizes, capacity_rows, recip
     then its b rows).  Any of: ab bf16 [R, 2 ffn] (kept for the gradient), y [R, ffn] (bf16 or fp32, as
     y_dtype says), out (alloc_quantized for [R, ffn]) receives y quantized in the layouts it holds.
     Returns a dict of those.  Rows past sum(split_sizes) are untouched."""
-    E = int(split_sizes.numel())
-    which, q = _which(out), out or {}
-    args = (_quant(x_q, "row_q", "x_q"), _quant(x_q, "row_s", "x_q"), capacity_rows, hidden,
-            _quant(w_q, "row_q", "w_q"), _quant(w_q, "row_s", "w_q"), ffn, _dev(probs, "probs", _F32),
-            _dev(split_sizes, "split_sizes", _I32), E, recipe, _dev(ab, "ab", _BF16),
-            _dev(y, "y", _F32_BITS if y_dtype == OUT_F32 else _BF16), y_dtype, which, _quant(q, "row_q", "out"),
-            _quant(q, "row_s", "out"), _quant(q, "col_q", "out"), _quant(q, "col_s", "out"),
-            _dev(status, "status", _I32), _stream(stream))
-    _need_quant(x_q, RECIPE_MX, capacity_rows, hidden, E, ROWWISE, "x_q")
-    _need_quant(w_q, RECIPE_MX, E * 2 * ffn, hidden, 1, ROWWISE, "w_q")
-    _need_quant(q, RECIPE_MX, capacity_rows, ffn, E, which, "out")
-    _need(probs, capacity_rows * 4, "probs")
-    _need(ab, capacity_rows * 2 * ffn * 2, "ab")
-    _need(y, capacity_rows * ffn * (4 if y_dtype == OUT_F32 else 2), "y")
-    rc = lib().bsfp8_grouped_gemm_swiglu(*args)
-    _check(rc, "grouped_gemm_swiglu")
-    return {k: v for k, v in dict(ab=ab, y=y, **q).items() if v is not None}
+    E, R = int(split_sizes.numel()), capacity_rows
+    f32 = y_dtype == OUT_F32
+    which, *q = _glu_quantized(out, R, ffn, E)
+    rc = lib().bsfp8_grouped_gemm_swiglu(
+        _buf(x_q.get("row_q"), "x_q", "row_q", _U8, R * hidden),
+        _buf(x_q.get("row_s"), "x_q", "row_s", _U8, R * hidden // 32), R, hidden,
+        _buf(w_q.get("row_q"), "w_q", "row_q", _U8, E * 2 * ffn * hidden),
+        _buf(w_q.get("row_s"), "w_q", "row_s", _U8, E * 2 * ffn * hidden // 32), ffn,
+        _buf(probs, "probs", None, _F32, R * 4), _dev(split_sizes, "split_sizes", _I32), E, recipe,
+        _buf(ab, "ab", None, _BF16, R * ffn * 4),
+        _buf(y, "y", None, _F32_BITS if f32 else _BF16, R * ffn * (4 if f32 else 2)), y_dtype, which, *q,
+        _dev(status, "status", _I32), _stream(stream))
+    if rc:
+        _check(rc, "grouped_gemm_swiglu")
+    return _glu_result(out, ab=ab, y=y)
 
 
 def grouped_gemm_swiglu_grad_workspace_bytes(capacity_rows, ffn, num_groups):
@@ -410,31 +437,27 @@ def grouped_gemm_swiglu_grad(dy_q, hidden, w_q, ffn, ab, split_sizes, capacity_r
     bf16 dab [R, 2 ffn] and / or quantized into out (alloc_quantized for [R, 2 ffn]), and that of the
     probabilities, dprobs fp32 [R].  Returns a dict of those.  workspace: a device tensor of
     grouped_gemm_swiglu_grad_workspace_bytes, for dprobs (None: a new one)."""
-    E = int(split_sizes.numel())
-    which, q = _which(out), out or {}
-    need = grouped_gemm_swiglu_grad_workspace_bytes(capacity_rows, ffn, E) if dprobs is not None else 0
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=split_sizes.device)
-    args = (_quant(dy_q, "row_q", "dy_q"), _quant(dy_q, "row_s", "dy_q"), capacity_rows, hidden,
-            _quant(w_q, "col_q", "w_q"), _quant(w_q, "col_s", "w_q"), ffn, _dev(ab, "ab", _BF16),
-            _dev(probs, "probs", _F32), _dev(split_sizes, "split_sizes", _I32), E, recipe, _dev(dab, "dab", _BF16),
-            which, _quant(q, "row_q", "out"), _quant(q, "row_s", "out"), _quant(q, "col_q", "out"),
-            _quant(q, "col_s", "out"), _dev(dprobs, "dprobs", _F32),
-            None if workspace is None else _dev(workspace, "workspace", (workspace.dtype,)),
-            _dev(status, "status", _I32), _stream(stream))
-    _need_quant(dy_q, RECIPE_MX, capacity_rows, hidden, E, ROWWISE, "dy_q")
+    E, R = int(split_sizes.numel()), capacity_rows
+    which, *q = _glu_quantized(out, R, 2 * ffn, E)
     hp = 128 * ((hidden + 127) // 128)
-    _need(w_q.get("col_q"), ffn * E * hp, "w_q['col_q']")
-    _need(w_q.get("col_s"), ffn * E * hp // 32, "w_q['col_s']")
-    _need_quant(q, RECIPE_MX, capacity_rows, 2 * ffn, E, which, "out")
-    _need(ab, capacity_rows * 2 * ffn * 2, "ab")
-    _need(dab, capacity_rows * 2 * ffn * 2, "dab")
-    _need(probs, capacity_rows * 4, "probs")
-    _need(dprobs, capacity_rows * 4, "dprobs")
-    _need(workspace, need, "workspace")
-    rc = lib().bsfp8_grouped_gemm_swiglu_grad(*args)
-    _check(rc, "grouped_gemm_swiglu_grad")
-    return {k: v for k, v in dict(dab=dab, dprobs=dprobs, **q).items() if v is not None}
+    ptrs = (_buf(dy_q.get("row_q"), "dy_q", "row_q", _U8, R * hidden),
+            _buf(dy_q.get("row_s"), "dy_q", "row_s", _U8, R * hidden // 32), R, hidden,
+            _buf(w_q.get("col_q"), "w_q", "col_q", _U8, ffn * E * hp),
+            _buf(w_q.get("col_s"), "w_q", "col_s", _U8, ffn * E * hp // 32), ffn,
+            _buf(ab, "ab", None, _BF16, R * ffn * 4), _buf(probs, "probs", None, _F32, R * 4),
+            _dev(split_sizes, "split_sizes", _I32), E, recipe, _buf(dab, "dab", None, _BF16, R * ffn * 4))
+    pws = None
+    if dprobs is not None:
+        need = grouped_gemm_swiglu_grad_workspace_bytes(R, ffn, E)
+        if workspace is None and need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=split_sizes.device)
+        if workspace is not None:
+            pws = _buf(workspace, "workspace", None, (workspace.dtype,), need)
+    rc = lib().bsfp8_grouped_gemm_swiglu_grad(*ptrs, which, *q, _buf(dprobs, "dprobs", None, _F32, R * 4), pws,
+                                              _dev(status, "status", _I32), _stream(stream))
+    if rc:
+        _check(rc, "grouped_gemm_swiglu_grad")
+    return _glu_result(out, dab=dab, dprobs=dprobs)
 
 
 # ------------------------------------------------------------------------------------------

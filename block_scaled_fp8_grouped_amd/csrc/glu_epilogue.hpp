@@ -68,20 +68,43 @@ struct GluOut {
   uint8_t *row_q, *row_s, *col_q, *col_s;
 };
 
-// 8 consecutive columns of a row: kept in the row-major output and quantized along the row, the 4
-// lanes of a block of 32 columns side by side.  `live` says whether this lane's row and columns exist.
-__device__ __forceinline__ void put_row8(const GluOut& o, int64_t R, int64_t N, int64_t row, int64_t col, bool live,
-                                         const float* v) {
+// The same at a tile's first row and a first column: uniform bases, so that a lane's place is a 32-bit offset.
+struct GluTileOut {
+  void* y;
+  int y_f32;
+  uint8_t *row_q, *row_s, *col_q, *col_s;
+  uint32_t N;
+  int64_t R, kp;
+};
+__device__ __forceinline__ GluTileOut glu_tile_out(const GluOut& o, int64_t R, int64_t N, const GroupInfo& g, int64_t row0,
+                                                   int64_t col) {
+  const int64_t row = g.off + row0, at = row * N + col;
+  return {o.y == nullptr ? nullptr : (uint8_t*)o.y + at * (o.y_f32 ? 4 : 2),
+          o.y_f32,
+          o.row_q == nullptr ? nullptr : o.row_q + at,
+          o.row_q == nullptr ? nullptr : o.row_s + col / 32 * R + row,
+          o.col_q == nullptr ? nullptr : o.col_q + col_elem(N, g.p, g.kp, col, row0),
+          o.col_q == nullptr ? nullptr : o.col_s + col_e8m0(N, g.p, row0 / 32, col),
+          (uint32_t)N,
+          R,
+          g.kp};
+}
+
+// 8 consecutive columns of a row (r, c from the tile's own): kept in the row-major output and quantized along the
+// row, the 4 lanes of a block of 32 columns side by side.  `live` says whether this lane's row and columns
+// exist.
+__device__ __forceinline__ void put_row8(const GluTileOut& o, int r, int c, bool live, const float* v) {
+  const uint32_t at = (uint32_t)r * o.N + (uint32_t)c;
   if (o.y != nullptr && live) {
     if (o.y_f32) {
-      float* p = (float*)o.y + row * N + col;
+      float* p = (float*)o.y + at;
       *(v4f*)p = v4f{v[0], v[1], v[2], v[3]};
       *(v4f*)(p + 4) = v4f{v[4], v[5], v[6], v[7]};
     } else {
       v8s w;
 #pragma unroll
       for (int k = 0; k < 8; ++k) w[k] = (short)f32_to_bf16(v[k]);
-      *(v8s*)((uint16_t*)o.y + row * N + col) = w;
+      *(v8s*)((uint16_t*)o.y + at) = w;
     }
   }
   if (o.row_q != nullptr) {
@@ -96,16 +119,15 @@ __device__ __forceinline__ void put_row8(const GluOut& o, int64_t R, int64_t N, 
       v2i q;
       q[0] = (int)e4m3x4_scaled(v[0], v[1], v[2], v[3], s);
       q[1] = (int)e4m3x4_scaled(v[4], v[5], v[6], v[7], s);
-      *(v2i*)(o.row_q + row * N + col) = q;
-      if ((col & 31) == 0) o.row_s[col / 32 * R + row] = (uint8_t)byte;
+      *(v2i*)(o.row_q + at) = q;
+      if ((c & 31) == 0) o.row_s[(c >> 5) * o.R + r] = (uint8_t)byte;
     }
   }
 }
 
-// 32 consecutive tokens (from t, a multiple of 32, inside the group's padded rows) of one channel,
-// all in this lane.
-__device__ __forceinline__ void put_col32(const GluOut& o, int64_t N, const GroupInfo& g, int64_t t, int64_t col,
-                                          bool live, const float* v) {
+// 32 consecutive tokens of one channel (t, a multiple of 32, and c from the tile's own; inside the group's padded
+// rows), all in this lane.
+__device__ __forceinline__ void put_col32(const GluTileOut& o, int t, int c, bool live, const float* v) {
   float m = 0.0f;
 #pragma unroll
   for (int k = 0; k < 32; k += 2) m = max3_abs(m, v[k], v[k + 1]);
@@ -115,10 +137,10 @@ __device__ __forceinline__ void put_col32(const GluOut& o, int64_t N, const Grou
 #pragma unroll
   for (int k = 0; k < 8; ++k) q[k >> 2][k & 3] = (int)e4m3x4_scaled(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3], s);
   if (live) {
-    uint8_t* dst = o.col_q + col_elem(N, g.p, g.kp, col, t);
+    uint8_t* dst = o.col_q + (c * o.kp + t);
     *(v4i*)dst = q[0];
     *(v4i*)(dst + 16) = q[1];
-    o.col_s[col_e8m0(N, g.p, t / 32, col)] = (uint8_t)byte;
+    o.col_s[(uint32_t)(t >> 5) * o.N + (uint32_t)c] = (uint8_t)byte;
   }
 }
 

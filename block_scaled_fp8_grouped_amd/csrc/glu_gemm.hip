@@ -126,8 +126,68 @@ struct GluShape {
   static_assert(NS * STAGE <= 160 * 1024, "LDS budget");
 };
 
+// Inclusive sum over a wave, with data-parallel lane moves.
+__device__ __forceinline__ int glu_wave_scan(int v) {
+  auto add = [&](auto ctrl, auto rows) {
+    v += __builtin_amdgcn_update_dpp(0, v, decltype(ctrl)::value, decltype(rows)::value, 0xf, false);
+  };
+  using std::integral_constant;
+  add(integral_constant<int, 0x111>(), integral_constant<int, 0xf>());  // 1, 2, 4, 8 lanes below in the row of 16
+  add(integral_constant<int, 0x112>(), integral_constant<int, 0xf>());
+  add(integral_constant<int, 0x114>(), integral_constant<int, 0xf>());
+  add(integral_constant<int, 0x118>(), integral_constant<int, 0xf>());
+  add(integral_constant<int, 0x142>(), integral_constant<int, 0xa>());  // row 0's total to row 1, 2's to 3
+  add(integral_constant<int, 0x143>(), integral_constant<int, 0xc>());  // the first half's total to the second
+  return v;
+}
+
+// A value that is the same in every lane, in scalar registers.
+__device__ __forceinline__ int64_t glu_uniform(int64_t v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32));
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+// The tile's group, as group_scan gives it (tiles of BM rows).  Up to 64 groups in a buffer of less than 2^24
+// rows (sums below 2^31) every wave scans the sizes by itself: no LDS, no barrier, a third of the time, which
+// counts where a workgroup is alone on its CU.
+template <int NT>
+__device__ __forceinline__ uint32_t glu_place(const GluArgs& args, int BM, int64_t mt, GroupScanSmem<NT>& sm,
+                                              GroupInfo& gi) {
+  if (args.E > 64 || args.R >= (1 << 24)) {
+    const uint32_t flags = group_scan<NT>(args.splits, args.E, args.R, BM, mt, 0, sm, gi);
+    gi.e = __builtin_amdgcn_readfirstlane(gi.e);
+    gi.k = glu_uniform(gi.k);
+    gi.off = glu_uniform(gi.off);
+    gi.kp = glu_uniform(gi.kp);
+    gi.p = glu_uniform(gi.p);
+    gi.tile = glu_uniform(gi.tile);
+    return __builtin_amdgcn_readfirstlane((int)flags);
+  }
+  const int lane = threadIdx.x & 63;
+  const int v = lane < args.E ? args.splits[lane] : 0;
+  const bool negative = __ballot(v < 0) != 0;
+  const bool large = __ballot((int64_t)v > args.R) != 0;
+  const int k = v < 0 || (int64_t)v > args.R ? 0 : v, kp = (k + 127) & ~127, tl = (k + BM - 1) / BM;
+  const int sk = glu_wave_scan(k), skp = glu_wave_scan(kp), stl = glu_wave_scan(tl);
+  gi.e = -1;
+  uint32_t flags = negative ? BSFP8_STATUS_NEGATIVE_SPLIT : 0u;
+  if (large || (int64_t)__builtin_amdgcn_readlane(sk, 63) > args.R) flags |= BSFP8_STATUS_EXCEEDS_CAPACITY;
+  if (flags) return flags;
+  const uint64_t own = __ballot(mt >= stl - tl && mt < stl);
+  if (own == 0) return 0;
+  const int e = __builtin_ctzll(own);
+  gi.e = e;
+  gi.k = __builtin_amdgcn_readlane(k, e);
+  gi.off = __builtin_amdgcn_readlane(sk - k, e);
+  gi.kp = __builtin_amdgcn_readlane(kp, e);
+  gi.p = __builtin_amdgcn_readlane(skp - kp, e);
+  gi.tile = __builtin_amdgcn_readlane(stl - tl, e);
+  return 0;
+}
+
 template <bool GRAD, int BM, int BN, int WN, int BK, int NS>
-__global__ __launch_bounds__(128 * BN / WN, BM == 128 ? 3 : WN == 128 ? 1 : 2) void glu_gemm_kernel(GluArgs args) {
+__global__ __launch_bounds__(128 * BN / WN, NS == 3 ? 3 : 2) void glu_gemm_kernel(GluArgs args) {
   using S = GluShape<GRAD, BM, BN, WN, BK, NS>;
   constexpr int NT = S::NT, FM = S::FM, FN = S::FN, BLKS = S::BLKS;
   __shared__ __attribute__((aligned(16))) uint8_t smem[NS * S::STAGE];
@@ -143,8 +203,8 @@ __global__ __launch_bounds__(128 * BN / WN, BM == 128 ? 3 : WN == 128 ? 1 : 2) v
   int64_t mt;
   int tn;
   fprop_tile(L, args.tiles_n, &mt, &tn);
-  GroupInfo gi;
-  const uint32_t flags = group_scan<NT>(args.splits, args.E, args.R, BM, mt, 0, gsm, gi);
+  GroupInfo gi{};
+  const uint32_t flags = glu_place<NT>(args, BM, mt, gsm, gi);
   report_status(args.status, flags);
   if (gi.e < 0) return;
   const int64_t row0 = (mt - gi.tile) * BM;  // the tile's first row within the group (< gi.k)
@@ -318,15 +378,15 @@ __global__ __launch_bounds__(128 * BN / WN, BM == 128 ? 3 : WN == 128 ? 1 : 2) v
   constexpr int PITCH = S::PITCH;
   if constexpr (!GRAD) {
     uint16_t* ab_tile = (uint16_t*)(tile + 32 * PITCH);
+    const GluTileOut o = glu_tile_out(args.out, args.R, F, gi, row0, col0);
+    uint16_t* ab = args.ab == nullptr ? nullptr : args.ab + (gi.off + row0) * 2 * F + col0;
 #pragma unroll
     for (int pair = 0; pair < FN / 2; ++pair) {
       const int cw = wn * (S::WN / 2) + 32 * pair;  // the pair's first column within the tile
-      const int64_t col = col0 + cw;
       const bool cols = cw <= b_last;  // its 32 columns all exist, or none
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const int rb = wm * S::WM + i * 32;
-        const int64_t row = gi.off + row0 + rb;
         const v16f &a = acc[i][2 * pair], &b = acc[i][2 * pair + 1];
         float v[16];
 #pragma unroll
@@ -360,14 +420,15 @@ __global__ __launch_bounds__(128 * BN / WN, BM == 128 ? 3 : WN == 128 ? 1 : 2) v
             const int r = pass * 8 + (lane >> 3), c = 8 * (lane & 7);
             const v8s w = *(const v8s*)(ab_tile + r * S::AB_PITCH + c);
             if (cols && rb + r <= a_last)
-              *(v8s*)(args.ab + (row + r) * 2 * F + col + (c < 32 ? c : F + c - 32)) = w;
+              *(v8s*)(ab + ((uint32_t)(rb + r) * (uint32_t)(2 * F) + (uint32_t)cw +
+                            (c < 32 ? (uint32_t)c : (uint32_t)F + (uint32_t)c - 32u))) = w;
           }
         }
         if (args.out.col_q != nullptr && row0 + rb < gi.kp) {
           float c[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) c[k] = tile[k * PITCH + l32];
-          put_col32(args.out, F, gi, row0 + rb, col + l32, cols && h == 0, c);
+          put_col32(o, rb, cw + l32, cols && h == 0, c);
         }
         if (args.out.y != nullptr || args.out.row_q != nullptr) {
 #pragma unroll
@@ -376,30 +437,33 @@ __global__ __launch_bounds__(128 * BN / WN, BM == 128 ? 3 : WN == 128 ? 1 : 2) v
             float w[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) w[k] = tile[r * PITCH + ch + k];
-            put_row8(args.out, args.R, F, row + r, col + ch, cols && rb + r <= a_last, w);
+            put_row8(o, rb + r, cw + ch, cols && rb + r <= a_last, w);
           }
         }
         wave_lds_order();
       }
     }
   } else {
+    const GluTileOut oa = glu_tile_out(args.out, args.R, 2 * F, gi, row0, col0);
+    const GluTileOut ob = glu_tile_out(args.out, args.R, 2 * F, gi, row0, F + col0);
+    const uint16_t* ab = args.ab + (gi.off + row0) * 2 * F + col0;
 #pragma unroll
     for (int part = 0; part < S::WN / 64; ++part) {
       const int cw = wn * S::WN + 64 * part;
       float* dp_sum = probs + (1 + cw / 64) * BM;  // these 64 columns' part of dprobs, per row
       const int ch = 8 * (lane & 7);
       const bool cols = cw + ch <= b_last;
-      // a and b of 32 rows, 8 columns of 4 rows per lane; the next 32 rows' are fetched beside this one's work
-      v8s av[2][4], bv[2][4];
+      // a and b of 32 rows, 8 columns of 4 rows per lane; the next 32 rows' are fetched once these are used
+      v8s av[4], bv[4];
       auto fetch = [&](int i) {
 #pragma unroll
         for (int pass = 0; pass < 4; ++pass) {
           const int r = wm * S::WM + i * 32 + pass * 8 + (lane >> 3);
-          av[i & 1][pass] = bv[i & 1][pass] = v8s{0, 0, 0, 0, 0, 0, 0, 0};
+          av[pass] = bv[pass] = v8s{0, 0, 0, 0, 0, 0, 0, 0};
           if (cols && r <= a_last) {
-            const uint16_t* p = args.ab + (gi.off + row0 + r) * 2 * F + col0 + cw + ch;
-            av[i & 1][pass] = *(const v8s*)p;
-            bv[i & 1][pass] = *(const v8s*)(p + F);
+            const uint16_t* p = ab + ((uint32_t)r * (uint32_t)(2 * F) + (uint32_t)(cw + ch));
+            av[pass] = *(const v8s*)p;
+            bv[pass] = *(const v8s*)(p + F);
           }
         }
       };
@@ -407,7 +471,6 @@ __global__ __launch_bounds__(128 * BN / WN, BM == 128 ? 3 : WN == 128 ? 1 : 2) v
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const int rb = wm * S::WM + i * 32;
-        if (i + 1 < FM) fetch(i + 1);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -427,25 +490,26 @@ __global__ __launch_bounds__(128 * BN / WN, BM == 128 ? 3 : WN == 128 ? 1 : 2) v
           float da[8], dp = 0.0f;
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            swiglu_grad(to_f32(av[i & 1][pass][k]), to_f32(bv[i & 1][pass][k]), p, tile[r * PITCH + ch + k], da[k],
+            swiglu_grad(to_f32(av[pass][k]), to_f32(bv[pass][k]), p, tile[r * PITCH + ch + k], da[k],
                         db[pass][k], dp);
-          const int64_t row = gi.off + row0 + rb + r, col = col0 + cw + ch;
-          put_row8(args.out, args.R, 2 * F, row, col, live, da);
-          put_row8(args.out, args.R, 2 * F, row, F + col, live, db[pass]);
+          put_row8(oa, rb + r, cw + ch, live, da);
+          put_row8(ob, rb + r, cw + ch, live, db[pass]);
           dp += __shfl_xor(dp, 1, 64);
           dp += __shfl_xor(dp, 2, 64);
           dp += __shfl_xor(dp, 4, 64);
           if ((lane & 7) == 0) dp_sum[rb + r] = dp;
 #pragma unroll
           for (int k = 0; k < 8; ++k) tile[r * PITCH + ch + k] = da[k];
+          __builtin_amdgcn_sched_barrier(0);  // (the rows' temporaries end here: registers)
         }
+        if (i + 1 < FM) fetch(i + 1);
         if (args.out.col_q != nullptr && row0 + rb < gi.kp) {
           float c[32];
           const bool live = cw + lane <= b_last;
           wave_lds_order();
 #pragma unroll
           for (int k = 0; k < 32; ++k) c[k] = tile[k * PITCH + lane];
-          put_col32(args.out, 2 * F, gi, row0 + rb, col0 + cw + lane, live, c);
+          put_col32(oa, rb, cw + lane, live, c);
           wave_lds_order();
 #pragma unroll
           for (int pass = 0; pass < 4; ++pass)
@@ -454,7 +518,7 @@ __global__ __launch_bounds__(128 * BN / WN, BM == 128 ? 3 : WN == 128 ? 1 : 2) v
           wave_lds_order();
 #pragma unroll
           for (int k = 0; k < 32; ++k) c[k] = tile[k * PITCH + lane];
-          put_col32(args.out, 2 * F, gi, row0 + rb, F + col0 + cw + lane, live, c);
+          put_col32(ob, rb, cw + lane, live, c);
         }
         wave_lds_order();
       }
@@ -500,8 +564,8 @@ __global__ __launch_bounds__(256, 2) void glu_rows_kernel(GluArgs args) {
   int64_t mt;
   int tn;
   fprop_tile(L, args.tiles_n, &mt, &tn);
-  GroupInfo gi;
-  const uint32_t flags = group_scan<NT>(args.splits, args.E, args.R, BM, mt, 0, gsm, gi);
+  GroupInfo gi{};
+  const uint32_t flags = glu_place<NT>(args, BM, mt, gsm, gi);
   report_status(args.status, flags);
   if (gi.e < 0) return;
   const int64_t row0 = (mt - gi.tile) * BM, col0 = (int64_t)tn * COLS;
@@ -509,50 +573,60 @@ __global__ __launch_bounds__(256, 2) void glu_rows_kernel(GluArgs args) {
   const int a_last = (int)(gi.k - row0 < BM ? gi.k - row0 : BM) - 1;
   const int b_last = (int)(F - col0 < COLS ? F - col0 : COLS) - 1;
 
-  // fragments: tokens 16 i + l16; weight rows 16 j + l16 of the tile's 64 (forward: j < 2 of a, j >= 2 of b)
+  // Fragments: tokens 16 i + l16; weight rows 16 j + l16 of the tile's 64 (forward: j < 2 of a, j >= 2 of b).  All
+  // loads go through buffer resources that end with the last live row: what lies past it, or past K, reads as
+  // zeros (a scale of 0 stands for 2^-127).
+  const int nblk = (int)(K / 32), nk = (nblk + 3) / 4;
   const __amdgpu_buffer_rsrc_t a_rs = __builtin_amdgcn_make_buffer_rsrc(
       (void*)(args.a_q + (gi.off + row0) * K), (short)0, (int)((a_last + 1) * K), 0x00020000);
+  const int64_t b_half = GRAD ? 32 : F;  // weight rows from fragment 0 to fragment 2
   const uint8_t* b_base = args.b_q + gi.e * args.b_estride + col0 * args.b_ld;
-  const uint32_t b_bytes = (uint32_t)((GRAD ? b_last + 1 : 32) * args.b_ld);
   __amdgpu_buffer_rsrc_t b_rs[2];
-  b_rs[0] = __builtin_amdgcn_make_buffer_rsrc((void*)b_base, (short)0, (int)b_bytes, 0x00020000);
-  b_rs[1] = GRAD ? b_rs[0]
-                 : __builtin_amdgcn_make_buffer_rsrc((void*)(b_base + F * args.b_ld), (short)0, (int)b_bytes, 0x00020000);
-  uint32_t a_off[2], b_off[4];
-  const uint8_t *a_sc[2], *b_sc[4];
+  int b_rows[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    b_rows[k] = GRAD ? b_last + 1 - 32 * k : 32;
+    b_rows[k] = b_rows[k] < 0 ? 0 : b_rows[k] > 32 ? 32 : b_rows[k];
+    b_rs[k] = __builtin_amdgcn_make_buffer_rsrc((void*)(b_base + k * b_half * args.b_ld), (short)0,
+                                                (int)(b_rows[k] * args.b_ld), 0x00020000);
+  }
+  uint32_t a_off[2], b_off[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int r = 16 * i + l16;
-    a_off[i] = (uint32_t)r * (uint32_t)K + 32 * q;
-    a_sc[i] = args.a_s + gi.off + row0 + (r < a_last ? r : a_last);
+    a_off[i] = (uint32_t)(16 * i + l16) * (uint32_t)K + 32 * q;
+    b_off[i] = (uint32_t)(16 * i + l16) * (uint32_t)args.b_ld + 32 * q;
   }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = 16 * (GRAD ? j : j & 1) + l16;
-    b_off[j] = (uint32_t)r * (uint32_t)args.b_ld + 32 * q;
-    b_sc[j] = args.b_s + gi.e * args.bs_estride + (GRAD ? 0 : (j >> 1) * F) + col0 + (r < b_last ? r : b_last);
-  }
-  const int nblk = (int)(K / 32), nk = (nblk + 3) / 4;
+  const uint32_t as_off = (uint32_t)q * (uint32_t)args.R + l16, bs_off = (uint32_t)q * (uint32_t)args.bs_bstride + l16;
+  const uint8_t* a_sc = args.a_s + gi.off + row0;
+  const uint8_t* b_sc = args.b_s + gi.e * args.bs_estride + col0;
 
   struct Frag {
     v4i a[2][2], b[4][2];
     uint8_t as[2], bs[4];
   };
   auto load = [&](Frag& f, int kk) {
-    const int kb = 4 * kk + q, kc = kb < nblk ? kb : nblk - 1;
-    // a block past K reads as zeros (an offset past every resource's range) under a live scale
-    const uint32_t k0 = kb < nblk ? (uint32_t)kk * 128u : 0x80000000u;
+    const int left = nblk - 4 * kk;  // blocks from this step on; may be negative
+    const uint32_t k0 = q < left ? (uint32_t)kk * 128u : 0x80000000u;
+    // the block rows of this step's scales, to their last live entry
+    auto scales = [&](const uint8_t* base, int64_t stride, int live) {
+      const int m = left < 4 ? left : 4;
+      return __builtin_amdgcn_make_buffer_rsrc((void*)(base + 4 * (left > 0 ? kk : 0) * stride), (short)0,
+                                               m > 0 && live > 0 ? (int)((m - 1) * stride + live) : 0, 0x00020000);
+    };
+    const __amdgpu_buffer_rsrc_t as = scales(a_sc, args.R, a_last + 1);
+    const __amdgpu_buffer_rsrc_t bs[2] = {scales(b_sc, args.bs_bstride, b_rows[0]),
+                                          scales(b_sc + b_half, args.bs_bstride, b_rows[1])};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      f.b[j][0] = __builtin_amdgcn_raw_buffer_load_b128(b_rs[GRAD ? 0 : j >> 1], (int)(b_off[j] + k0), 0, 0);
-      f.b[j][1] = __builtin_amdgcn_raw_buffer_load_b128(b_rs[GRAD ? 0 : j >> 1], (int)(b_off[j] + k0 + 16), 0, 0);
-      f.bs[j] = b_sc[j][kc * args.bs_bstride];
+      f.b[j][0] = __builtin_amdgcn_raw_buffer_load_b128(b_rs[j >> 1], (int)(b_off[j & 1] + k0), 0, 0);
+      f.b[j][1] = __builtin_amdgcn_raw_buffer_load_b128(b_rs[j >> 1], (int)(b_off[j & 1] + k0 + 16), 0, 0);
+      f.bs[j] = __builtin_amdgcn_raw_buffer_load_b8(bs[j >> 1], (int)bs_off + (j & 1) * 16, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       f.a[i][0] = __builtin_amdgcn_raw_buffer_load_b128(a_rs, (int)(a_off[i] + k0), 0, 0);
       f.a[i][1] = __builtin_amdgcn_raw_buffer_load_b128(a_rs, (int)(a_off[i] + k0 + 16), 0, 0);
-      f.as[i] = a_sc[i][kc * args.R];
+      f.as[i] = __builtin_amdgcn_raw_buffer_load_b8(as, (int)as_off + i * 16, 0, 0);
     }
   };
   v4f acc[2][4];
@@ -581,11 +655,15 @@ __global__ __launch_bounds__(256, 2) void glu_rows_kernel(GluArgs args) {
   load(f0, wave);
   load(f1, wave + NW);
   for (int s = 0; s < steps; s += 3) {
+    // (the fences keep the loads in front of the products)
     load(f2, wave + NW * (s + 2));
+    __builtin_amdgcn_sched_barrier(0);
     multiply(f0);
     load(f0, wave + NW * (s + 3));
+    __builtin_amdgcn_sched_barrier(0);
     multiply(f1);
     load(f1, wave + NW * (s + 4));
+    __builtin_amdgcn_sched_barrier(0);
     multiply(f2);
   }
 
@@ -621,7 +699,8 @@ __global__ __launch_bounds__(256, 2) void glu_rows_kernel(GluArgs args) {
       const float b = __shfl_xor(v[k], 4, 64);
       v[k] = live_row ? swiglu(v[k], b, p) : 0.0f;  // in the lanes that hold a
     }
-    put_row8(args.out, args.R, F, at, col0 + ch, live_row && ch < 32, v);
+    const GluTileOut o = glu_tile_out(args.out, args.R, F, gi, row0, col0);
+    put_row8(o, row, ch, live_row && ch < 32, v);
     if (args.out.col_q != nullptr) {
       __syncthreads();  // every thread has read its sums
       if (ch < 32)
@@ -632,7 +711,7 @@ __global__ __launch_bounds__(256, 2) void glu_rows_kernel(GluArgs args) {
         float c[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) c[k] = part[0][k][lane & 31];
-        put_col32(args.out, F, gi, row0, col0 + lane, lane < 32, c);
+        put_col32(o, 0, lane, lane < 32, c);
       }
     }
   } else {
@@ -646,8 +725,10 @@ __global__ __launch_bounds__(256, 2) void glu_rows_kernel(GluArgs args) {
     float da[8], db[8], dp = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) swiglu_grad(to_f32(av[k]), to_f32(bv[k]), p, live ? v[k] : 0.0f, da[k], db[k], dp);
-    put_row8(args.out, args.R, 2 * F, at, col0 + ch, live, da);
-    put_row8(args.out, args.R, 2 * F, at, F + col0 + ch, live, db);
+    const GluTileOut oa = glu_tile_out(args.out, args.R, 2 * F, gi, row0, col0);
+    const GluTileOut ob = glu_tile_out(args.out, args.R, 2 * F, gi, row0, F + col0);
+    put_row8(oa, row, ch, live, da);
+    put_row8(ob, row, ch, live, db);
     dp += __shfl_xor(dp, 1, 64);
     dp += __shfl_xor(dp, 2, 64);
     dp += __shfl_xor(dp, 4, 64);
@@ -664,7 +745,7 @@ __global__ __launch_bounds__(256, 2) void glu_rows_kernel(GluArgs args) {
         float c[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) c[k] = part[wave][k][lane];
-        put_col32(args.out, 2 * F, gi, row0, wave * F + col0 + lane, lane <= b_last, c);
+        put_col32(wave == 0 ? oa : ob, 0, lane, lane <= b_last, c);
       }
     }
   }
@@ -688,12 +769,23 @@ __global__ __launch_bounds__(256, 2) void glu_rows_kernel(GluArgs args) {
 // dprobs[row] = sum of the tile columns' parts, in order; rows past the last group's are not touched.
 __global__ __launch_bounds__(256) void glu_dprobs_kernel(const float* __restrict__ part, int tiles_n, int64_t R,
                                                          const int32_t* __restrict__ splits, int E, float* dprobs) {
-  __shared__ GroupScanSmem<256> gsm;
-  GroupInfo gi;
-  // the group of rows [256 b, 256 b + 256) laid end to end: tiles of one row
+  __shared__ int64_t total[4];
+  __shared__ int bad;
   const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const uint32_t flags = group_scan<256>(splits, E, R, 0, 0, E - 1, gsm, gi);
-  if (flags || gi.e < 0 || row >= gi.off + gi.k) return;
+  if (threadIdx.x == 0) bad = 0;
+  __syncthreads();
+  int64_t t = 0;
+  for (int e = threadIdx.x; e < E; e += 256) {
+    const int k = splits[e];
+    if (k < 0) bad = 1;
+    t += k;
+  }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) t += __shfl_xor(t, d, 64);
+  if ((threadIdx.x & 63) == 0) total[threadIdx.x >> 6] = t;
+  __syncthreads();
+  t = total[0] + total[1] + total[2] + total[3];
+  if (bad || t > R || row >= t) return;
   float s = 0.0f;
   for (int n = 0; n < tiles_n; ++n) s += part[(int64_t)n * R + row];
   dprobs[row] = s;
@@ -703,21 +795,30 @@ __global__ __launch_bounds__(256) void glu_dprobs_kernel(const float* __restrict
 // Launchers
 // ------------------------------------------------------------------------------------------
 
-// Tile of a launch.  Up to 32 rows per expert on average take the few-rows kernel; the others the largest
-// tile that still gives every CU its share.  Groups end half a tile early on average, hence R / BM + E / 2
-// rows of tiles.
+// Tile of a launch, by the rows of tiles that it is likely to have (groups end half a tile early on average: R / BM
+// + E / 2).  Measured over 2 to 32 experts, hidden 2048 and 4096, ffn 512 to 2048, 8 to 2048 rows per expert
+// (unequal ones), forward / gradient:
+//  - few rows per expert, or so few tiles that the few-rows kernel's fill the chip better: at most 12 rows per
+//    expert (8 experts of 8, 4096 x 2048: 34 / 34 us, 128 x 128 tiles 45 / 55) or 512 tiles (48 rows, 2048 x 1024: 24 /
+//    25 us, 28 / 37; from 640 tiles on it loses, 39 / 34 to 29 / 37)
+//  - 128 x 128, up to two tiles per CU: K steps of 128 and two workgroups per CU, else steps of 64 and three (8
+//    experts of 128 and of 1024 rows, 2048 x 1024: 28 / 38 and 93 / 78 us, 31 / 41 and 93 / 73)
+//  - 256 x 256 from 1536 tiles on (2048 rows, 32 experts of 2048 x 1024: 595 / 439 us, 128 x 128 tiles 623 / 403 at
+//    2176 / 1088 tiles; 8 experts, 544 tiles: 179 / 149, 158 / 116)
 struct GluTile {
-  int bm, bn;
+  int bm, bn, bk;
 };
 
 static GluTile glu_tile(bool grad, int64_t R, int64_t F, int E) {
-  if (R <= (int64_t)kRowsBM * E) return {kRowsBM, kRowsBN};
   auto tiles = [&](int bm, int bn) {
     const int64_t cols = grad ? bn : bn / 2;
     return (R / bm + (E + 1) / 2) * ((F + cols - 1) / cols);
   };
-  if (tiles(256, 256) >= 512) return {256, 256};
-  return {128, 128};
+  // (the few-rows kernel addresses four block rows of scales with 32-bit offsets)
+  if (R < (1 << 24) && 2 * F * E < (1 << 28) && (R <= 12 * (int64_t)E || tiles(kRowsBM, kRowsBN) <= 512))
+    return {kRowsBM, kRowsBN, 0};
+  if (tiles(256, 256) >= 1536) return {256, 256, 128};
+  return {128, 128, tiles(128, 128) <= 512 ? 128 : 64};
 }
 
 // Columns of one half per tile, and the tiles of a row of them.
@@ -756,6 +857,7 @@ static int launch_glu(GluArgs& a, hipStream_t stream) {
   if (rc != BSFP8_OK) return rc;
   if (t.bm == kRowsBM) hipLaunchKernelGGL((glu_rows_kernel<GRAD>), grid, dim3(64 * kRowsNW), 0, stream, a);
   else if (t.bn == 256) launch_glu_tile<GRAD, 256, 256, 64, 128, 2>(a, grid, stream);
+  else if (t.bk == 128) launch_glu_tile<GRAD, 128, 128, 64, 128, 2>(a, grid, stream);
   else launch_glu_tile<GRAD, 128, 128, 64, 64, 3>(a, grid, stream);
   return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
 }

@@ -378,3 +378,74 @@ def test_rows_do_not_depend_on_their_neighbours(splits):
         s["xq"]["row_q"][T:].random_(0, 256)
         bs.grouped_gemm_swiglu(s["xq"], 416, s["w1q"], 96, s["st"], R, probs=s["p"], y=z, y_dtype=bs.OUT_F32)
         assert torch.equal(z[:T], y[:T])
+
+
+def ragged(experts, rows, seed):
+    """Sizes of `experts` groups with `rows` rows in all, about an eighth of them empty, one holding a tenth."""
+    rng = np.random.default_rng(seed)
+    w = rng.random(experts) * (rng.random(experts) > 0.125)
+    w[experts // 2] = w.sum() / 9 + 1e-3
+    k = np.floor(w / w.sum() * rows).astype(int)
+    k[experts // 2] += rows - k.sum()
+    return [int(v) for v in k]
+
+
+# sizes that take each kernel: 128 x 128 tiles with long and short K steps (the second also with more groups than a
+# wave's lanes), 256 x 256 tiles; each with K that ends inside a step and outputs that end inside a tile
+LARGE = [(9, 2000, 160, 1056), (9, 2000, 1056, 1056), (70, 4100, 96, 1056), (70, 4100, 608, 1056), (64, 16400, 96, 4128),
+         (40, 24000, 416, 4128)]
+
+
+@pytest.mark.parametrize("experts,rows,hidden,ffn", LARGE)
+def test_forward_in_tiles(experts, rows, hidden, ffn):
+    flush(f"{experts} {rows} {hidden} {ffn}")
+    s = operands(ragged(experts, rows, hidden), hidden, ffn, 31)
+    R, T = s["R"], s["T"]
+    ab = torch.full((R, 2 * ffn), float("nan"), dtype=torch.bfloat16, device=DEV)
+    y = torch.full((R, ffn), float("nan"), device=DEV)
+    out = poisoned(R, ffn, experts)
+    bs.grouped_gemm_swiglu(s["xq"], hidden, s["w1q"], ffn, s["st"], R, probs=s["p"], ab=ab, y=y, y_dtype=bs.OUT_F32,
+                           out=out)
+    rab, tab, ry, ty = forward64(s)
+    within(ab[:T], rab, 2.0 ** -8 * rab.abs() + 1.01 * tab, "ab")
+    within(y[:T], ry, ty, "y")
+    assert bool(ab[T:].isnan().all()) and bool(y[T:].isnan().all())
+    check_exact_quantization(out, y, s)
+    check_untouched(out, s, ffn)
+
+
+@pytest.mark.parametrize("experts,rows,hidden,ffn", LARGE)
+def test_gradient_in_tiles(experts, rows, hidden, ffn):
+    flush(f"{experts} {rows} {hidden} {ffn}")
+    s = operands(ragged(experts, rows, hidden + 1), hidden, ffn, 33)
+    R, T = s["R"], s["T"]
+    dab = torch.full((R, 2 * ffn), float("nan"), dtype=torch.bfloat16, device=DEV)
+    dp = torch.full((R,), float("nan"), device=DEV)
+    out = poisoned(R, 2 * ffn, experts)
+    for _ in range(2):  # the second call finds its workspace and outputs used
+        bs.grouped_gemm_swiglu_grad(s["xq"], hidden, s["w2q"], ffn, s["ab"], s["st"], R, probs=s["p"], dab=dab, out=out,
+                                    dprobs=dp)
+    rd, td, rp, tp = backward64(s)
+    within(dab[:T], rd, 2.0 ** -8 * rd.abs() + 1.01 * td, "dab")
+    within(dp[:T], rp, tp, "dprobs")
+    assert bool(dab[T:].isnan().all()) and bool(dp[T:].isnan().all())
+    check_close_quantization(out, rd, td, s)
+    check_untouched(out, s, 2 * ffn)
+
+
+@pytest.mark.parametrize("experts,rows", [(5, 30), (9, 2000), (70, 4100)])
+def test_scales_at_their_ends(experts, rows):
+    """Operand scale bytes from 0 (2^-127) up: rows whose values are subnormal or tiny, beside ordinary ones."""
+    hidden, ffn = 160, 1056
+    s = operands(ragged(experts, rows, 3), hidden, ffn, 35)
+    T = s["T"]
+    s["xq"]["row_s"][:, 0:T:3] = 0
+    s["xq"]["row_s"][:, 1:T:3] = 1
+    s["xv"] = deq(s["xq"]["row_q"][:T], s["xq"]["row_s"][:, :T])
+    s["w1q"]["row_s"].view(-1)[:: 7] = 0
+    s["w1v"] = deq(s["w1q"]["row_q"], s["w1q"]["row_s"]).view(experts, 2 * ffn, hidden)
+    y = torch.empty((s["R"], ffn), device=DEV)
+    bs.grouped_gemm_swiglu(s["xq"], hidden, s["w1q"], ffn, s["st"], s["R"], probs=s["p"], y=y, y_dtype=bs.OUT_F32)
+    _, _, ry, ty = forward64(s)
+    # values below bf16's and fp32's normal range may be flushed: 2^-126 of each of their products' other factors
+    within(y[:T], ry, ty + 2.0 ** -100, "y")
