@@ -41,6 +41,11 @@ GATE_TOKEN = 2  # gate[rows]
 STATE_F32 = 0
 STATE_8BIT = 1
 
+try:  # the checks, allocations and calls of the smallest launches in native code (csrc/binding.cpp)
+    from . import _native
+except ImportError:  # not built: every call goes through ctypes
+    _native = None
+
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
 _vp = ctypes.c_void_p
@@ -205,6 +210,10 @@ def _stream(stream):
             return _raw_stream(_raw_device())
         return torch.cuda.current_stream().cuda_stream
     return getattr(stream, "cuda_stream", stream)
+
+
+def _use_native():
+    return _native is not None and torch.cuda.is_initialized()  # (else there are no device tensors)
 
 
 # ------------------------------------------------------------------------------------------
@@ -408,6 +417,12 @@ def grouped_gemm_swiglu(x_q, hidden, w_q, ffn, split_sizes, capacity_rows, recip
     then its b rows).  Any of: ab bf16 [R, 2 ffn] (kept for the gradient), y [R, ffn] (bf16 or fp32, as
     y_dtype says), out (alloc_quantized for [R, ffn]) receives y quantized in the layouts it holds.
     Returns a dict of those.  Rows past sum(split_sizes) are untouched."""
+    q = out or {}
+    if _use_native() and _native.swiglu(
+            x_q.get("row_q"), x_q.get("row_s"), capacity_rows, hidden, w_q.get("row_q"), w_q.get("row_s"), ffn, split_sizes,
+            recipe, y_dtype, probs, ab, y, q.get("row_q"), q.get("row_s"), q.get("col_q"), q.get("col_s"), status,
+            _stream(stream)):
+        return _glu_result(out, ab=ab, y=y)
     E, R = int(split_sizes.numel()), capacity_rows
     f32 = y_dtype == OUT_F32
     which, *q = _glu_quantized(out, R, ffn, E)
@@ -437,6 +452,12 @@ def grouped_gemm_swiglu_grad(dy_q, hidden, w_q, ffn, ab, split_sizes, capacity_r
     bf16 dab [R, 2 ffn] and / or quantized into out (alloc_quantized for [R, 2 ffn]), and that of the
     probabilities, dprobs fp32 [R].  Returns a dict of those.  workspace: a device tensor of
     grouped_gemm_swiglu_grad_workspace_bytes, for dprobs (None: a new one)."""
+    q = out or {}
+    if _use_native() and _native.swiglu_grad(
+            dy_q.get("row_q"), dy_q.get("row_s"), capacity_rows, hidden, w_q.get("col_q"), w_q.get("col_s"), ffn,
+            split_sizes, recipe, ab, probs, dab, q.get("row_q"), q.get("row_s"), q.get("col_q"), q.get("col_s"), dprobs,
+            workspace, status, _stream(stream)):
+        return _glu_result(out, dab=dab, dprobs=dprobs)
     E, R = int(split_sizes.numel()), capacity_rows
     which, *q = _glu_quantized(out, R, 2 * ffn, E)
     hp = 128 * ((hidden + 127) // 128)
@@ -510,6 +531,16 @@ def residual_norm(x, y=None, post_weight=None, pre_weight=None, gate=None, gate_
     n).  gate: fp32 [cols] (GATE_CHANNEL) or [rows] (GATE_TOKEN).  Returns a dict of r (x's type), n
     (bf16), rstd_y and rstd_r (fp32 [rows], for the gradient), in the tensors given or in new ones;
     r may be x."""
+    if _use_native():
+        got = _native.residual_norm(x, y, post_weight, pre_weight, gate, gate_kind, x_scale, y_scale, eps, weight_offset,
+                                    r, n, rstd_y, rstd_r, _stream(stream))
+        if got is not None:
+            out = {"r": got[0]}
+            if pre_weight is not None:
+                out["n"], out["rstd_r"] = got[1], got[3]
+            if post_weight is not None:
+                out["rstd_y"] = got[2]
+            return out
     if x.dim() != 2:
         raise ValueError("residual_norm: x is [rows, cols]")
     shape = rows, cols = x.shape
@@ -568,6 +599,17 @@ def residual_norm_grad(dn, dr, r=None, rstd_r=None, pre_weight=None, y=None, rst
     the weights and the gate that are there, dpre_weight, dpost_weight, dgate (fp32), in the tensors
     given or in new ones.  accumulate: the weights' and a channel gate's gradients are added to the
     tensors given."""
+    if _use_native():
+        got = _native.residual_norm_grad(dn, dr, r, rstd_r, pre_weight, y, rstd_y, post_weight, gate, gate_kind, x_scale,
+                                         y_scale, weight_offset, dx, dy, dpre_weight, dpost_weight, dgate, accumulate,
+                                         workspace, _stream(stream))
+        if got is not None:
+            out = {"dx": got[0]}
+            for name, of, value in (("dy", y, got[1]), ("dpre_weight", pre_weight, got[2]),
+                                    ("dpost_weight", post_weight, got[3]), ("dgate", gate, got[4])):
+                if of is not None:
+                    out[name] = value
+            return out
     ref = dr if dr is not None else r
     if ref is None:
         raise ValueError("residual_norm_grad: neither dr nor (dn and r)")

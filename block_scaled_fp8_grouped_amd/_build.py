@@ -19,6 +19,10 @@ PEAK_SOURCES = ["mfma_peak.hip"]
 HEADERS = ["common.hpp", "group_layout.hpp", "tile_addr.hpp", "tile_sched.hpp", "norm_layout.hpp", "adamw_plan.hpp",
            "glu_epilogue.hpp"]
 
+# the native host side of the smallest calls (a Python extension on torch's C++ tensors, no GPU code)
+BINDING_PATH = os.path.join(HERE, "_native.so")
+BINDING_SOURCE = "binding.cpp"
+
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
@@ -46,9 +50,26 @@ def _link(objs, path):
     os.replace(tmp, path)
 
 
+def _binding():
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-DAT_PER_OPERATOR_HEADERS",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + sysconfig.get_paths()["include"]]
+    cmd += ["-isystem" + p for p in include_paths()]
+    cmd += [os.path.join(CSRC, BINDING_SOURCE), "-o", BINDING_PATH + ".tmp", "-L" + lib, "-ltorch_python", "-ltorch_cpu",
+            "-lc10", "-L" + HERE, "-lbsfp8", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("binding failed:\n" + r.stderr)
+    os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
+
+
 def build(verbose=True):
-    """Compile every source for gfx950 and link libbsfp8.so (and the probe libbsfp8_peak.so)
-    next to this file."""
+    """Compile every source for gfx950 and link libbsfp8.so (and the probe libbsfp8_peak.so), then the
+    Python extension that calls it, next to this file."""
     objdir = os.path.join(ROOT, "_build")
     os.makedirs(objdir, exist_ok=True)
     srcs = SOURCES + PEAK_SOURCES
@@ -57,8 +78,9 @@ def build(verbose=True):
         list(ex.map(_compile, srcs, objs))
     _link(objs[:len(SOURCES)], LIB_PATH)
     _link(objs[len(SOURCES):], PEAK_LIB_PATH)
+    _binding()
     if verbose:
-        print(f"built {LIB_PATH} and {PEAK_LIB_PATH}", file=sys.stderr)
+        print(f"built {LIB_PATH}, {PEAK_LIB_PATH} and {BINDING_PATH}", file=sys.stderr)
     return LIB_PATH
 
 
