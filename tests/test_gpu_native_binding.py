@@ -145,3 +145,27 @@ def test_native_path_is_the_one_that_runs():
         a = bs.residual_norm(**s)
     side.synchronize()
     same(a, bs.residual_norm(**s))
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_given_stream(raw):
+    """With a stream given, new outputs and workspaces belong to it: busy memory of the current stream, freed while
+    its work still runs, is not written over."""
+    s = norm_args(rows=300, cols=520)
+    f = bs.residual_norm(**s)
+    grad = dict(dn=s["y"], dr=s["x"], r=f["r"], rstd_r=f["rstd_r"], rstd_y=f["rstd_y"],
+                **{k: s[k] for k in ("pre_weight", "y", "post_weight", "gate", "gate_kind")})
+    want = bs.residual_norm_grad(**grad)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        junk = [torch.zeros(300, 520, dtype=torch.bfloat16, device=DEV) for _ in range(8)]
+        torch.cuda._sleep(2000000)
+        kept = [j + 1 for j in junk]
+        del junk
+        at = side.cuda_stream if raw else side
+        a, b = bs.residual_norm(**s, stream=at), bs.residual_norm_grad(**grad, stream=at)
+        torch.cuda.synchronize()
+        same(a, f)
+        same(b, want)
+        assert all(bool((k == 1).all()) for k in kept)
