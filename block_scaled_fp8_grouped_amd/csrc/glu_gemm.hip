@@ -9,13 +9,22 @@
 // Bound by the bf16 MFMA on large inputs: the operands stay e4m3 in HBM and LDS, are widened to
 // bf16 with their block scale folded in (exact) and accumulated in fp32, as in the plain grouped
 // GEMMs.  What the fusion saves is a bf16 round trip of the product through HBM and a launch.
+// Measured (32 experts, 65536 tokens, hidden 4096, ffn 2048, all of the layer's outputs): forward 1.96 ms =
+// 1120 TFLOP/s, gradient 1.22 ms = 900 TFLOP/s; the main loop alone runs at 1450 TFLOP/s (from two values of
+// hidden), the rest is each tile's start and epilogue.  Under that load the chip holds 1.6 to 1.8 of its
+// 2.4 GHz: other schedules of the same instructions (deeper rings, half the step, LDS reads ahead, two workgroups of
+// 256 x 128) end within 3% of each other; waves of 128 x 128 (a third fewer conversions and LDS reads, but one wave
+// per SIMD) are 8% slower.
 //
-// Tile: 256 tokens x 256 rows of the weight, K step 128, 8 waves of 128 x 64, double-buffered LDS
-// filled by LDS DMA, XOR-swizzled 16-byte chunks.  In the forward the 256 weight rows are 128 rows of
-// each projection, interleaved 32 by 32: a wave's two column fragments are a and b of the same 32
-// outputs, so a lane holds both halves of its elements in registers and the activation needs no
-// exchange.  Wave w fetches LDS rows 32 w .. 32 w + 31, which are 32 rows of one projection (w & 1),
-// so the interleave costs one scalar base per wave.
+// Tiles of 256 x 256 or 128 x 128 (tokens x rows of the weight), waves of 128 x 64 or 64 x 64, K steps of 128 or 64
+// bytes in a ring of two or three LDS stages filled by LDS DMA, 16-byte chunks XOR-swizzled; the E8M0 bytes come
+// by DMA too and go into the conversions as they are.  A step's last barrier stands before its last block's
+// MFMAs: behind it the stage is free, the loads of the step a ring ahead go into it and the next step's first
+// fragments are read, both beside those MFMAs.
+//
+// In the forward the weight rows of a tile are half of each projection's, interleaved 32 by 32: a wave's column
+// fragments are a and b of the same 32 outputs, so a lane holds both halves of its elements in registers and the
+// activation needs no exchange; a run of 32 LDS rows has one scalar base, so the interleave costs nothing.
 //
 // Epilogue: a wave owns its block from its accumulators to memory, 32 rows at a time through its own
 // piece of LDS (no barrier): rows of 8 columns per lane for the row-major outputs, whole 32-token
@@ -23,7 +32,7 @@
 //
 // One workgroup per tile, fixed order, no atomics: the same bits every time.  Rows past a group's
 // live rows read as zeros and are not stored; the colwise pad lanes get the zeros that those rows
-// compute.
+// count as.
 #include <type_traits>
 
 #include "glu_epilogue.hpp"
@@ -546,7 +555,9 @@ __global__ __launch_bounds__(128 * BN / WN, NS == 3 ? 3 : 2) void glu_gemm_kerne
 // order at the end: no barrier and no LDS until then, each wave keeps two steps of weights (16 KB) in
 // flight in registers.  16 x 16 x 32 MFMAs; lane (row, q) of a fragment loads the whole scale block q of
 // its row (two 16-byte loads), so it needs one scale byte per step.  The order of K within an MFMA is
-// that of the lanes, the same for both operands.
+// that of the lanes, the same for both operands.  8 tokens at 8 of 32 experts, hidden 7168, ffn 2048: 41 us with
+// the 242 MB of weights in the last-level cache, 49 us = 4.9 TB/s from HBM (256 x 256 tiles, which
+// keep half of the chip busy: 149).
 constexpr int kRowsBM = 32, kRowsBN = 64, kRowsNW = 4, kRowsPitch = 68;
 
 template <bool GRAD>

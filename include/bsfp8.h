@@ -12,6 +12,9 @@
  *   - TransformerEngine PR #3224, "Improve device-init grouped linear module with single
  *     grouped weight support" (per-group scale strides in grouped quantize, output reuse,
  *     zero-row early return, device-resident split sizes).
+ * and, around them, what a training or serving step of such a layer runs next to its GEMMs: the gated projection
+ * with its activation and quantize in one kernel, the norms before and after a block with its gate and residual sum,
+ * their gradients, and the AdamW step over all parameters.
  *
  * Conventions for every entry point:
  *   - All data pointers are DEVICE pointers owned by the caller.  The library allocates
