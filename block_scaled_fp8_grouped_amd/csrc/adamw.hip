@@ -131,9 +131,10 @@ __device__ __forceinline__ float block_scale(const float* v) {
 
 // fp32 states: 512 threads, 4 elements each, one chunk per workgroup.  8-bit states: 256 threads, 8 elements
 // each, up to 4 chunks per workgroup, which spares most of the scalars' fp64 arithmetic (the larger share
-// where an element moves 18 bytes, not 30).  341 million elements (fp32 parameters and gradients, bf16
-// copies), fp32 / 8-bit states: 1.81 / 1.10 ms = 6.2 TB/s, what a large copy reaches; through the caches, with
-// flat accesses and one chunk of 256 threads 2.13 / 1.38 ms.
+// where an element moves 18 bytes, not 30).  376 million elements (fp32 parameters and gradients, bf16
+// copies), fp32 / 8-bit states: 1.81 / 1.10 ms = 6.2 TB/s, what an elementwise pass over large arrays reaches
+// (boxes differ: 1.99 / 1.26 ms on others); through the caches, with flat accesses and one chunk of 256
+// threads 2.13 / 1.38 ms.
 template <bool Q8>
 constexpr int adam_threads() {
   return Q8 ? 256 : 512;
