@@ -264,13 +264,14 @@ __global__ __launch_bounds__(128 * BN / WN, NS == 3 ? 3 : 2) void glu_gemm_kerne
            (r <= b_last ? r : b_last & ~15);
   }
   const int nblk = (int)(K / 32), nk = (int)((K + BK - 1) / BK);
-  // parts [p0, p1): 0 the scales, then A_INS + B_INS DMAs.  A step past the last stores zeros (offsets past
-  // every resource's range, as the host bounds 256 rows by 2^31 bytes), so that the counts stay the same.
+  // step kk into `stage` (kk % NS), parts [p0, p1): 0 the scales, then A_INS + B_INS DMAs.  A step past the last
+  // stores zeros (offsets past every resource's range, as the host bounds 256 rows by 2^31 bytes), so that the
+  // counts stay the same.
   constexpr int NP = S::A_INS + S::B_INS + 1;
-  auto issue = [&](int kk, int p0, int p1) {
+  auto issue = [&](int kk, int stage, int p0, int p1) {
     const uint32_t k0 = kk < nk ? (uint32_t)kk * BK : 0x80000000u;
-    const uint32_t base = smem_lds + (uint32_t)(kk % NS) * S::STAGE;
-    if (p0 == 0 && wave < S::SC_INS) {
+    const uint32_t base = smem_lds + (uint32_t)stage * S::STAGE;
+    if (p0 == 0 && p1 > 0 && wave < S::SC_INS) {
       const int kb = BLKS * kk + sc_blk, kc = kb < nblk ? kb : nblk - 1;
       const uint8_t* src;
       if (sc_is_a) {
@@ -308,74 +309,153 @@ __global__ __launch_bounds__(128 * BN / WN, NS == 3 ? 3 : 2) void glu_gemm_kerne
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-  // The fragments of one scale block (32 bytes of K) of a step and their scales; two such sets alternate, so
-  // that one block's LDS reads go out beside the MFMAs of the block before.
+  // The fragments of one scale block (32 bytes of K) of a step and their scales: of two such sets one is read from
+  // LDS while the other is worked on.
   struct Block {
     v4i a[FM], b[FN];
     float as[FM], bs[FN];
   };
-  auto read = [&](Block& q, int kk, int blk) {
-    const uint8_t* cur = smem + (kk % NS) * S::STAGE;
+  constexpr int NF = FM + FN, NM = FM * FN;
+  auto read = [&](Block& q, int kk, int stage, int blk, int f0, int f1) {  // of the FM + FN fragments [f0, f1)
+    const uint8_t* cur = smem + stage * S::STAGE;
     // where the block's A scales begin in the stage
     const int sh = S::SC_OFF + blk * AL * 16 + (int)((uintptr_t)(a_sc + (int64_t)(BLKS * kk + blk) * args.R) & 15);
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
+      if (i < f0 || i >= f1) continue;
       const int row = wm * S::WM + i * 32 + l32;
       q.a[i] = *(const v4i*)(cur + row * BK + (((2 * blk + h) ^ glu_swz<BK>(row)) << 4));
       q.as[i] = glu_e8m0(cur[sh + row]);
     }
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
+      if (FM + j < f0 || FM + j >= f1) continue;
       const int row = wn * S::WN + j * 32 + l32;
       q.b[j] = *(const v4i*)(cur + S::B_OFF + row * BK + (((2 * blk + h) ^ glu_swz<BK>(row)) << 4));
       q.bs[j] = glu_e8m0(cur[S::SB_OFF + blk * BN + row]);
     }
   };
-  auto multiply = [&](const Block& q, auto between) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      v8bf aw[FM], bw[FN];
-#pragma unroll
-      for (int i = 0; i < FM; ++i) aw[i] = glu_widen8(q.a[i][2 * t], q.a[i][2 * t + 1], q.as[i]);
-#pragma unroll
-      for (int j = 0; j < FN; ++j) bw[j] = glu_widen8(q.b[j][2 * t], q.b[j][2 * t + 1], q.bs[j]);
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(aw[i], bw[j], acc[i][j], 0, 0, 0);
-      between(t);
-    }
-    __builtin_amdgcn_sched_barrier(0);
+  // Half a block, 16 bytes of K per half wave, as the MFMAs take it.
+  struct Half {
+    v8bf a[FM], b[FN];
   };
-  auto nothing = [](int) {};
+  auto widen = [&](Half& w, const Block& q, int t, int f) {
+    if (f < FM) w.a[f] = glu_widen8(q.a[f][2 * t], q.a[f][2 * t + 1], q.as[f]);
+    else w.b[f - FM] = glu_widen8(q.b[f - FM][2 * t], q.b[f - FM][2 * t + 1], q.bs[f - FM]);
+  };
+  auto mfma = [&](const Half& w, int u) {
+    acc[u / FN][u % FN] =
+        __builtin_amdgcn_mfma_f32_32x32x16_bf16(w.a[u / FN], w.b[u % FN], acc[u / FN][u % FN], 0, 0, 0);
+  };
   Block q[2];
-  // One K step; q[0] holds its first block.  Before its last block's MFMAs all its reads have returned and the
-  // next step's loads have landed: behind that barrier its stage is free, the loads of the step NS ahead go
-  // into it, and the next step's first block is read, both beside those MFMAs.  Blocks past K (a last step that
-  // K does not fill) are not multiplied.
-  auto step = [&](int kk) {
-#pragma unroll
-    for (int blk = 0; blk + 1 < BLKS; ++blk) {
-      read(q[(blk + 1) & 1], kk, blk + 1);
-      __builtin_amdgcn_sched_barrier(0);
-      if (blk == 0 || BLKS * kk + blk < nblk) multiply(q[blk & 1], nothing);
-    }
-    wait(std::integral_constant<int, NS - 2>());
-    read(q[0], kk + 1, 0);
-    __builtin_amdgcn_sched_barrier(0);
-    if (BLKS * kk + BLKS - 1 < nblk)
-      multiply(q[(BLKS - 1) & 1], [&](int t) { issue(kk + NS, t * NP / 2, (t + 1) * NP / 2); });
-    else
-      issue(kk + NS, 0, NP);
-  };
 
   __syncthreads();  // the group scan's LDS is free
 #pragma unroll
-  for (int kk = 0; kk < NS; ++kk) issue(kk, 0, NP);
+  for (int kk = 0; kk < NS; ++kk) issue(kk, kk, 0, NP);
   wait(std::integral_constant<int, NS - 1>());
-  read(q[0], 0, 0);
-  for (int kk = 0; kk < nk; ++kk) step(kk);
+
+  if constexpr (BM == 128) {
+    // Few waves per SIMD: the schedule is the wave's own.  Behind each MFMA of a half go its share of the next half's
+    // conversions (32 cycles for 32) and of the LDS reads and the DMAs, and the stages are unrolled, so that their
+    // addresses are constants.  A tile alone on its CU: a step of 128 takes 1.05 us, with the halves one after
+    // another and the DMAs sent together 1.25; K = 4128, 128 / 256 tiles of the gradient 45 / 47 us (50 / 52).
+    Half w[2];
+    auto half = [&](const Half& now, Half& next, const Block& from, int t, auto other) {
+#pragma unroll
+      for (int u = 0; u < NM; ++u) {
+        mfma(now, u);
+#pragma unroll
+        for (int f = u * NF / NM; f < (u + 1) * NF / NM; ++f) widen(next, from, t, f);
+        other(u);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    // One K step.  A block is read two blocks ahead, where its set of registers has been widened.  Behind the first
+    // half of the last block but one the next step's loads have landed and this one's reads have returned, in every
+    // wave: its stage is free, and the loads of the step NS ahead go out over the three halves that are left.
+    auto step = [&](int kk, auto stage_) {
+      constexpr int stage = decltype(stage_)::value, after = (stage + 1) % NS;
+      auto send = [&](int v) { issue(kk + NS, stage, v * NP / (3 * NM), (v + 1) * NP / (3 * NM)); };
+#pragma unroll
+      for (int blk = 0; blk < BLKS; ++blk) {
+        half(w[0], w[1], q[blk & 1], 1, [&](int u) {
+          if (blk == BLKS - 1) send(NM + u);
+        });
+        if (blk == BLKS - 2) wait(std::integral_constant<int, NS - 2>());
+        half(w[1], w[0], q[(blk + 1) & 1], 0, [&](int u) {
+          const int f0 = u * NF / NM, f1 = (u + 1) * NF / NM;
+          if (blk + 2 < BLKS) read(q[blk & 1], kk, stage, blk + 2, f0, f1);
+          else read(q[blk & 1], kk + 1, after, blk + 2 - BLKS, f0, f1);
+          if (blk >= BLKS - 2) send((blk == BLKS - 1 ? 2 * NM : 0) + u);
+        });
+      }
+    };
+    read(q[0], 0, 0, 0, 0, NF);
+    read(q[1], 0, 0, 1, 0, NF);
+#pragma unroll
+    for (int f = 0; f < NF; ++f) widen(w[0], q[0], 0, f);
+    const int whole = nblk / BLKS, rest = nblk % BLKS;
+    int kk = 0;
+    for (; kk + NS <= whole; kk += NS) {
+      step(kk, std::integral_constant<int, 0>());
+      step(kk + 1, std::integral_constant<int, 1>());
+      if constexpr (NS == 3) step(kk + 2, std::integral_constant<int, 2>());
+    }
+    if (kk < whole) step(kk++, std::integral_constant<int, 0>());
+    if constexpr (NS == 3)
+      if (kk < whole) step(kk++, std::integral_constant<int, 1>());
+    // the blocks of a last step that K does not fill
+#pragma unroll
+    for (int blk = 0; blk < BLKS - 1; ++blk) {
+      if (blk >= rest) break;
+      half(w[0], w[1], q[blk & 1], 1, [](int) {});
+      half(w[1], w[0], q[(blk + 1) & 1], 0, [&](int u) {
+        if (blk + 2 < BLKS) read(q[blk & 1], whole, whole % NS, blk + 2, u * NF / NM, (u + 1) * NF / NM);
+      });
+    }
+  } else {
+    // Two waves per SIMD cover for each other, and there are no registers for a half ahead: one block's LDS reads go
+    // out beside the MFMAs of the block before.
+    auto multiply = [&](const Block& from, auto between) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        v8bf aw[FM], bw[FN];
+#pragma unroll
+        for (int i = 0; i < FM; ++i) aw[i] = glu_widen8(from.a[i][2 * t], from.a[i][2 * t + 1], from.as[i]);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) bw[j] = glu_widen8(from.b[j][2 * t], from.b[j][2 * t + 1], from.bs[j]);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(aw[i], bw[j], acc[i][j], 0, 0, 0);
+        between(t);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto nothing = [](int) {};
+    // One K step; q[0] holds its first block.  Before its last block's MFMAs all its reads have returned and the
+    // next step's loads have landed: behind that barrier its stage is free, the loads of the step NS ahead go
+    // into it, and the next step's first block is read, both beside those MFMAs.  Blocks past K (a last step that
+    // K does not fill) are not multiplied.
+    auto step = [&](int kk) {
+#pragma unroll
+      for (int blk = 0; blk + 1 < BLKS; ++blk) {
+        read(q[(blk + 1) & 1], kk, kk % NS, blk + 1, 0, NF);
+        __builtin_amdgcn_sched_barrier(0);
+        if (blk == 0 || BLKS * kk + blk < nblk) multiply(q[blk & 1], nothing);
+      }
+      wait(std::integral_constant<int, NS - 2>());
+      read(q[0], kk + 1, (kk + 1) % NS, 0, 0, NF);
+      __builtin_amdgcn_sched_barrier(0);
+      if (BLKS * kk + BLKS - 1 < nblk)
+        multiply(q[(BLKS - 1) & 1], [&](int t) { issue(kk + NS, kk % NS, t * NP / 2, (t + 1) * NP / 2); });
+      else
+        issue(kk + NS, kk % NS, 0, NP);
+    };
+    read(q[0], 0, 0, 0, 0, NF);
+    for (int kk = 0; kk < nk; ++kk) step(kk);
+  }
   glu_wait_barrier<0>();  // the zeros past the last step have landed: LDS is free
 
   // ---------------- epilogue ----------------
