@@ -18,9 +18,9 @@
 //
 // Tiles of 256 x 256 or 128 x 128 (tokens x rows of the weight), waves of 128 x 64 or 64 x 64, K steps of 128 or 64
 // bytes in a ring of two or three LDS stages filled by LDS DMA, 16-byte chunks XOR-swizzled; the E8M0 bytes come
-// by DMA too and go into the conversions as they are.  A step's last barrier stands before its last block's
-// MFMAs: behind it the stage is free, the loads of the step a ring ahead go into it and the next step's first
-// fragments are read, both beside those MFMAs.
+// by DMA too and go into the conversions as they are.  A step's barrier stands before its last MFMAs: behind it the
+// stage is free, the loads of the step a ring ahead go into it and the next step's first fragments are read, both
+// beside those MFMAs.
 //
 // In the forward the weight rows of a tile are half of each projection's, interleaved 32 by 32: a wave's column
 // fragments are a and b of the same 32 outputs, so a lane holds both halves of its elements in registers and the
@@ -297,7 +297,7 @@ __global__ __launch_bounds__(128 * BN / WN, NS == 3 ? 3 : 2) void glu_gemm_kerne
   // waits until all but the newest `steps` steps' loads have landed, in every wave
   auto wait = [&](auto steps) {
     constexpr int N = decltype(steps)::value;
-    if (wave < S::SC_INS) glu_wait_barrier<N * NP>();
+    if (N == 0 || wave < S::SC_INS) glu_wait_barrier<N * NP>();
     else glu_wait_barrier<N*(NP - 1)>();
   };
 
@@ -890,12 +890,15 @@ __global__ __launch_bounds__(256) void glu_dprobs_kernel(const float* __restrict
 // + E / 2).  Measured over 2 to 32 experts, hidden 2048 and 4096, ffn 512 to 2048, 8 to 2048 rows per expert
 // (unequal ones), forward / gradient:
 //  - few rows per expert, or so few tiles that the few-rows kernel's fill the chip better: at most 12 rows per
-//    expert (8 experts of 8, 4096 x 2048: 34 / 34 us, 128 x 128 tiles 45 / 55) or 512 tiles (48 rows, 2048 x 1024: 24 /
-//    25 us, 28 / 37; from 640 tiles on it loses, 39 / 34 to 29 / 37)
-//  - 128 x 128, up to two tiles per CU: K steps of 128 and two workgroups per CU, else steps of 64 and three (8
-//    experts of 128 and of 1024 rows, 2048 x 1024: 28 / 38 and 93 / 78 us, 31 / 41 and 93 / 73)
-//  - 256 x 256 from 1536 tiles on (2048 rows, 32 experts of 2048 x 1024: 595 / 439 us, 128 x 128 tiles 623 / 403 at
-//    2176 / 1088 tiles; 8 experts, 544 tiles: 179 / 149, 158 / 116)
+//    expert (8 experts of 8, 4096 x 2048: 30 / 30 us, 128 x 128 tiles 41 / 52) or 512 tiles (48 rows, 2048 x 1024: 21 /
+//    20 us, 26 / 34; from 640 tiles on it loses, 39 / 34 to 25 / 34)
+//  - 128 x 128, up to two tiles per CU: K steps of 128 and two workgroups per CU (8 experts of 128 rows, 2048 x 1024 and
+//    4096 x 2048: 26 / 34 and 63 / 51 us, steps of 64 and three workgroups 27 / 37 and 67 / 57)
+//  - 128 x 128, more tiles: steps of 64, three workgroups per CU and loads two steps ahead.  With operands from HBM
+//    4099 rows of 8 experts, 4128 x 1024, 560 tiles, take 102 us, with steps of 128 106; with operands in the
+//    last-level cache the two end within 2% of each other at 2048 x 1024 and steps of 128 are up to 8% faster at 4128
+//  - 256 x 256 from 1536 tiles on (2048 rows, 32 experts of 2048 x 1024, forward, 2176 tiles: 606 us, 128 x 128 tiles
+//    615; below, 1088 tiles: gradient of the same 450 us to 405, 8 experts of 4096 x 2048 567 / 384 to 547 / 340)
 struct GluTile {
   int bm, bn, bk;
 };
