@@ -212,10 +212,23 @@ def _stream(stream):
     return getattr(stream, "cuda_stream", stream)
 
 
+def _elsewhere(stream):
+    """Whether a stream argument asks for another stream than the current one."""
+    if stream is None or not torch.cuda.is_initialized():
+        return False
+    if isinstance(stream, torch.cuda.Stream):
+        return stream != torch.cuda.current_stream()  # (also where only the device differs)
+    return _stream(stream) != _stream(None)
+
+
 def _on(stream):
     """The given stream (a torch stream or a raw handle) as the current one: what a call allocates itself
-    then belongs to the stream that its kernels run on, and is not handed out again before they have run."""
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream))
+    then belongs to the stream that its kernels run on, and is not handed out again before they have run.
+    Handle 0 is the default stream; ExternalStream would take it for no handle and make a stream of its own."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _use_native():
@@ -458,7 +471,7 @@ def grouped_gemm_swiglu_grad(dy_q, hidden, w_q, ffn, ab, split_sizes, capacity_r
     bf16 dab [R, 2 ffn] and / or quantized into out (alloc_quantized for [R, 2 ffn]), and that of the
     probabilities, dprobs fp32 [R].  Returns a dict of those.  workspace: a device tensor of
     grouped_gemm_swiglu_grad_workspace_bytes, for dprobs (None: a new one)."""
-    if stream is not None and dprobs is not None and workspace is None and torch.cuda.is_initialized():
+    if dprobs is not None and workspace is None and _elsewhere(stream):
         with _on(stream):
             return grouped_gemm_swiglu_grad(dy_q, hidden, w_q, ffn, ab, split_sizes, capacity_rows, recipe, probs, dab, out,
                                             dprobs, None, status)
@@ -541,7 +554,7 @@ def residual_norm(x, y=None, post_weight=None, pre_weight=None, gate=None, gate_
     n).  gate: fp32 [cols] (GATE_CHANNEL) or [rows] (GATE_TOKEN).  Returns a dict of r (x's type), n
     (bf16), rstd_y and rstd_r (fp32 [rows], for the gradient), in the tensors given or in new ones;
     r may be x."""
-    if stream is not None and torch.cuda.is_initialized():
+    if _elsewhere(stream):
         with _on(stream):
             return residual_norm(x, y, post_weight, pre_weight, gate, gate_kind, x_scale, y_scale, eps, weight_offset, r, n,
                                  rstd_y, rstd_r)
@@ -613,7 +626,7 @@ def residual_norm_grad(dn, dr, r=None, rstd_r=None, pre_weight=None, y=None, rst
     the weights and the gate that are there, dpre_weight, dpost_weight, dgate (fp32), in the tensors
     given or in new ones.  accumulate: the weights' and a channel gate's gradients are added to the
     tensors given."""
-    if stream is not None and torch.cuda.is_initialized():
+    if _elsewhere(stream):
         with _on(stream):
             return residual_norm_grad(dn, dr, r, rstd_r, pre_weight, y, rstd_y, post_weight, gate, gate_kind, x_scale,
                                       y_scale, weight_offset, dx, dy, dpre_weight, dpost_weight, dgate, accumulate,
