@@ -11,6 +11,7 @@ Functions keep the C names without the ``bsfp8_`` prefix:
 queries.
 """
 import ctypes
+import importlib
 import os
 
 import torch
@@ -40,11 +41,6 @@ GATE_CHANNEL = 1  # gate[cols]
 GATE_TOKEN = 2  # gate[rows]
 STATE_F32 = 0
 STATE_8BIT = 1
-
-try:  # the checks, allocations and calls of the smallest launches in native code (csrc/binding.cpp)
-    from . import _native
-except ImportError:  # not built: every call goes through ctypes
-    _native = None
 
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
@@ -231,8 +227,28 @@ def _on(stream):
     return torch.cuda.stream(stream)
 
 
+def _load_native():
+    """The checks, allocations and calls of the smallest launches in native code (csrc/binding.cpp), or None
+    where it is not built: every call then goes through ctypes.  Loaded when first asked for, since it maps
+    libbsfp8.so, which a process that only builds must not have done."""
+    global _native
+    try:
+        _native = importlib.import_module("._native", __name__)
+    except ImportError:
+        _native = None
+    return _native
+
+
+def __getattr__(name):
+    if name == "_native":
+        return _load_native()
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
 def _use_native():
-    return _native is not None and torch.cuda.is_initialized()  # (else there are no device tensors)
+    if not torch.cuda.is_initialized():  # there are no device tensors
+        return False
+    return (_native if "_native" in globals() else _load_native()) is not None
 
 
 # ------------------------------------------------------------------------------------------
