@@ -13,6 +13,7 @@ queries.
 import ctypes
 import importlib
 import os
+import warnings
 
 import torch
 
@@ -113,6 +114,8 @@ def lib():
         L.bsfp8_adamw_step.restype = ctypes.c_int
         L.bsfp8_adamw_step.argtypes = [_vp, _i32, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _d, _d, _d, _d, _d,
                                        _i64, _vp, _vp, _vp, _vp, _vp]
+        L.bsfp8_adamw_step_stochastic.restype = ctypes.c_int
+        L.bsfp8_adamw_step_stochastic.argtypes = L.bsfp8_adamw_step.argtypes[:-1] + [ctypes.c_uint64, _vp]
         L.bsfp8_strerror.restype = ctypes.c_char_p
         L.bsfp8_strerror.argtypes = [ctypes.c_int]
         _lib = L
@@ -784,13 +787,21 @@ def adamw_plan(params, grads, exp_avgs, exp_avg_sqs, exp_avg_scales=None, exp_av
 
 
 def adamw_step(plan, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, step=1, lr_dev=None, step_dev=None,
-               grad_scale=None, noop_flag=None, stream=None):
+               grad_scale=None, noop_flag=None, stream=None, seed=None):
     """bsfp8_adamw_step: one AdamW step over the plan's tensors, in place.  step counts from 1.  Device
     scalars: lr_dev (fp32) and step_dev (int32) replace lr and step (for a captured graph), grad_scale
-    (fp32) multiplies the gradients, a nonzero noop_flag (fp32) leaves everything as it is."""
-    rc = lib().bsfp8_adamw_step(plan.table.data_ptr(), plan.num_tensors, plan.num_chunks, plan.param_dtype,
-                                plan.grad_dtype, plan.state, lr, beta1, beta2, eps, weight_decay, step,
-                                _dev(lr_dev, "lr_dev", _F32), _dev(step_dev, "step_dev", _I32),
-                                _dev(grad_scale, "grad_scale", _F32), _dev(noop_flag, "noop_flag", _F32),
-                                _stream(stream))
-    _check(rc, "adamw_step")
+    (fp32) multiplies the gradients, a nonzero noop_flag (fp32) leaves everything as it is.
+
+    seed: an int, with 8-bit states, rounds them stochastically (bsfp8_adamw_step_stochastic; the same seed and
+    step give the same states).  Train with one: rounded to nearest (None, with a warning), an element's states
+    stop following its gradients where another element holds its block's scale."""
+    args = (plan.table.data_ptr(), plan.num_tensors, plan.num_chunks, plan.param_dtype, plan.grad_dtype, plan.state, lr,
+            beta1, beta2, eps, weight_decay, step, _dev(lr_dev, "lr_dev", _F32), _dev(step_dev, "step_dev", _I32),
+            _dev(grad_scale, "grad_scale", _F32), _dev(noop_flag, "noop_flag", _F32))
+    if seed is None:
+        if plan.state == STATE_8BIT:
+            warnings.warn("adamw_step: 8-bit states rounded to nearest do not follow changes of less than half a code's step "
+                          "(3 to 6%) a step; give a seed to train with them", stacklevel=2)
+        _check(lib().bsfp8_adamw_step(*args, _stream(stream)), "adamw_step")
+    else:
+        _check(lib().bsfp8_adamw_step_stochastic(*args, int(seed) & 0xFFFFFFFFFFFFFFFF, _stream(stream)), "adamw_step")

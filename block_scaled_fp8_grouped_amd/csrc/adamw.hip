@@ -11,8 +11,16 @@
 // u's codes keep 2^17 of it with 4 significant bits each, and u is what the update divides by.  A
 // scale in fp32 rather than a power of two: the block's largest state is then always the code 448
 // and decays with the scale step by step, where a power-of-two scale would leave the code itself
-// to decay, which by less than half a code's step a time it cannot.  The update itself uses m and
-// u before they are rounded.
+// to decay.  The update itself uses m and u before they are rounded.
+//
+// Rounding of the 8-bit states.  To nearest, a code that another element's scale holds up stays where
+// it is as long as a step changes its state by less than half a code's step, 3 to 6 percent: u, which
+// loses 1 - sqrt(beta2) a step (2.5 percent at 0.95, 0.05 at 0.999), never falls again, and m's lowest
+// codes do not either.  Stochastic rounding goes up with the probability of the part cut off: the
+// expected state is the unrounded one at any beta.  Its bits are SplitMix64 outputs (Steele, Lea and
+// Flood 2014, a bijective mix of a counter) of the caller's seed, the step, the tensor's place in the
+// plan and the element, 16 per state: the same call gives the same bits on any launch shape.  A graph
+// replayed with a new step_dev takes new ones.
 //
 // Every operation is rounded to fp32 in the order written.
 #include "adamw_plan.hpp"
@@ -27,6 +35,7 @@ struct AdamArgs {
   float beta1, one_minus_beta1, beta2, one_minus_beta2, eps;
   const float *lr_dev, *grad_scale, *noop_flag;
   const int32_t* step_dev;
+  uint64_t seed;  // stochastic rounding
   int64_t num_chunks;
   int per;  // chunks per workgroup
 };
@@ -129,6 +138,25 @@ __device__ __forceinline__ float block_scale(const float* v) {
   return fmaxf(m * (1.0f / 448.0f), 1e-30f);
 }
 
+__device__ __forceinline__ uint64_t mix64(uint64_t z) {
+  z = (z ^ (z >> 30)) * 0xbf58476d1ce4e5b9ull;
+  z = (z ^ (z >> 27)) * 0x94d049bb133111ebull;
+  return z ^ (z >> 31);
+}
+constexpr uint64_t kWeyl = 0x9e3779b97f4a7c15ull;  // the counter's stride (2^64 over the golden ratio, odd)
+
+// w, in units of its block's scale, to a neighbouring e4m3 value: away from zero with the probability of
+// its distance from the one below, by 16 random bits (each standing for the middle of its 2^-16).  448, and
+// what is not a number, stay as they are.
+__device__ __forceinline__ float round_by(float w, uint32_t r) {
+  const float a = fabsf(w);
+  if (!(a < 448.0f)) return w;
+  const float fine = floorf(a * 512.0f + ((float)r + 0.5f) * 0x1p-16f) * 0x1p-9f;  // below 2^-6: steps of 2^-9
+  // else 3 of the 23 bits of the mantissa are kept (a carry into the exponent is the next power of two)
+  const float wide = __uint_as_float((__float_as_uint(a) + ((r << 4) | 8u)) & 0xfff00000u);
+  return copysignf(a < 0x1p-6f ? fine : wide, w);
+}
+
 // fp32 states: 512 threads, 4 elements each, one chunk per workgroup.  8-bit states: 256 threads, 8 elements
 // each, up to 4 chunks per workgroup, which spares most of the scalars' fp64 arithmetic (the larger share
 // where an element moves 18 bytes, not 30).  376 million elements (fp32 parameters and gradients, bf16
@@ -140,7 +168,8 @@ constexpr int adam_threads() {
   return Q8 ? 256 : 512;
 }
 
-template <class PT, class GT, bool Q8, bool NT>
+// SR: stochastic rounding of 8-bit states.
+template <class PT, class GT, bool Q8, bool NT, bool SR>
 __global__ __launch_bounds__(adam_threads<Q8>()) void adamw_kernel(AdamArgs a) {
   constexpr int kThreads = adam_threads<Q8>();
   if (a.noop_flag != nullptr && *a.noop_flag != 0.0f) return;
@@ -148,6 +177,7 @@ __global__ __launch_bounds__(adam_threads<Q8>()) void adamw_kernel(AdamArgs a) {
   const double t = a.step_dev != nullptr ? (double)*a.step_dev : a.step;
   const double c1 = 1.0 - exp(t * a.log_beta1), c2 = 1.0 - exp(t * a.log_beta2);
   const float root = (float)(1.0 / sqrt(c2));
+  const uint64_t step_key = SR ? mix64(a.seed + kWeyl * (uint64_t)(int64_t)t) : 0;
   const int64_t from = (int64_t)blockIdx.x * a.per;
   const int64_t to = from + a.per < a.num_chunks ? from + a.per : a.num_chunks;
   int tensor = -1;
@@ -211,6 +241,15 @@ __global__ __launch_bounds__(adam_threads<Q8>()) void adamw_kernel(AdamArgs a) {
           m[i] *= im;
           root_v[i] *= iv;
         }
+        if constexpr (SR) {
+          const uint64_t at_key = mix64(step_key + kWeyl * (uint64_t)tensor) + kWeyl * (uint64_t)(at / 2);
+          const uint64_t bits_m = mix64(at_key), bits_v = mix64(at_key + kWeyl);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            m[i] = round_by(m[i], (uint32_t)(bits_m >> (16 * i)) & 0xffffu);
+            root_v[i] = round_by(root_v[i], (uint32_t)(bits_v >> (16 * i)) & 0xffffu);
+          }
+        }
         store4_codes<NT>(m8 + at, n, m);
         store4_codes<NT>(v8 + at, n, root_v);
         if ((threadIdx.x & 31) == 0 && n > 0) {
@@ -238,7 +277,8 @@ constexpr int64_t kAdamStreamChunks = 8192;
 
 int launch_adamw(const void* plan, int32_t num_tensors, int64_t chunks, int p_f32, int g_f32, int q8, double lr,
                  double beta1, double beta2, double eps, double decay, int64_t step, const float* lr_dev,
-                 const int32_t* step_dev, const float* grad_scale, const float* noop_flag, hipStream_t stream) {
+                 const int32_t* step_dev, const float* grad_scale, const float* noop_flag, const uint64_t* seed,
+                 hipStream_t stream) {
   AdamArgs a{};
   a.tensors = (const AdamTensor*)plan;
   a.chunks = (const AdamChunk*)((const uint8_t*)plan + adam_table_bytes(num_tensors));
@@ -254,6 +294,7 @@ int launch_adamw(const void* plan, int32_t num_tensors, int64_t chunks, int p_f3
   a.eps = (float)eps;
   a.lr_dev = lr_dev;
   a.step_dev = step_dev;
+  a.seed = seed != nullptr ? *seed : 0;
   a.grad_scale = grad_scale;
   a.noop_flag = noop_flag;
   a.num_chunks = chunks;
@@ -263,13 +304,11 @@ int launch_adamw(const void* plan, int32_t num_tensors, int64_t chunks, int p_f3
   auto go = [&](auto p, auto g) {
     using P = decltype(p);
     using G = decltype(g);
-    if (q8) {
-      if (nt) hipLaunchKernelGGL((adamw_kernel<P, G, true, true>), grid, dim3(adam_threads<true>()), 0, stream, a);
-      else hipLaunchKernelGGL((adamw_kernel<P, G, true, false>), grid, dim3(adam_threads<true>()), 0, stream, a);
-    } else {
-      if (nt) hipLaunchKernelGGL((adamw_kernel<P, G, false, true>), grid, dim3(adam_threads<false>()), 0, stream, a);
-      else hipLaunchKernelGGL((adamw_kernel<P, G, false, false>), grid, dim3(adam_threads<false>()), 0, stream, a);
-    }
+    auto run = [&](auto kernel, int threads) { hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, stream, a); };
+    if (!q8) run(nt ? adamw_kernel<P, G, false, true, false> : adamw_kernel<P, G, false, false, false>, adam_threads<false>());
+    else if (seed == nullptr)
+      run(nt ? adamw_kernel<P, G, true, true, false> : adamw_kernel<P, G, true, false, false>, adam_threads<true>());
+    else run(nt ? adamw_kernel<P, G, true, true, true> : adamw_kernel<P, G, true, false, true>, adam_threads<true>());
   };
   if (p_f32) {
     if (g_f32) go(float(), float());

@@ -49,7 +49,8 @@ int launch_residual_norm_grad(int64_t R, int64_t C, int x_f32, const void* dn, c
                               int accumulate, float* workspace, hipStream_t stream);
 int launch_adamw(const void* plan, int32_t num_tensors, int64_t chunks, int p_f32, int g_f32, int q8, double lr,
                  double beta1, double beta2, double eps, double decay, int64_t step, const float* lr_dev,
-                 const int32_t* step_dev, const float* grad_scale, const float* noop_flag, hipStream_t stream);
+                 const int32_t* step_dev, const float* grad_scale, const float* noop_flag, const uint64_t* seed,
+                 hipStream_t stream);
 }  // namespace bsfp8
 
 namespace {
@@ -114,6 +115,27 @@ int check_glu_shape(int64_t capacity_rows, int64_t hidden, int64_t ffn, int32_t 
   return BSFP8_OK;
 }
 
+
+// an AdamW step; seed: NULL, or that of the 8-bit states' stochastic rounding
+int adamw_step(const void* device_plan, int32_t num_tensors, int64_t num_chunks, int param_dtype, int grad_dtype,
+               int state, double lr, double beta1, double beta2, double eps, double weight_decay, int64_t step,
+               const float* lr_dev, const int32_t* step_dev, const float* grad_scale, const float* noop_flag,
+               const uint64_t* seed, void* stream) {
+  if (!valid_dtype(param_dtype) || !valid_dtype(grad_dtype) || (state != BSFP8_STATE_F32 && state != BSFP8_STATE_8BIT))
+    return BSFP8_ERR_ARGUMENT;
+  if (!finite_nonnegative(lr) || !finite_nonnegative(eps) || !finite_nonnegative(weight_decay) ||
+      !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || step < 1)
+    return BSFP8_ERR_ARGUMENT;
+  if (num_tensors <= 0 || num_chunks < 0 || num_chunks > 0x7fffffff) return BSFP8_ERR_SHAPE;
+  if (num_chunks == 0) return BSFP8_OK;  // only empty tensors
+  if (device_plan == nullptr) return BSFP8_ERR_NULL_POINTER;
+  if (!aligned16(device_plan) || !aligned4(lr_dev) || !aligned4(step_dev) || !aligned4(grad_scale) ||
+      !aligned4(noop_flag))
+    return BSFP8_ERR_ALIGNMENT;
+  return bsfp8::launch_adamw(device_plan, num_tensors, num_chunks, param_dtype == BSFP8_F32, grad_dtype == BSFP8_F32,
+                             state == BSFP8_STATE_8BIT, lr, beta1, beta2, eps, weight_decay, step, lr_dev, step_dev,
+                             grad_scale, noop_flag, seed, (hipStream_t)stream);
+}
 }  // namespace
 
 extern "C" {
@@ -442,20 +464,16 @@ int bsfp8_adamw_step(const void* device_plan, int32_t num_tensors, int64_t num_c
                      int grad_dtype, int state, double lr, double beta1, double beta2, double eps,
                      double weight_decay, int64_t step, const float* lr_dev, const int32_t* step_dev,
                      const float* grad_scale, const float* noop_flag, void* stream) {
-  if (!valid_dtype(param_dtype) || !valid_dtype(grad_dtype) || (state != BSFP8_STATE_F32 && state != BSFP8_STATE_8BIT))
-    return BSFP8_ERR_ARGUMENT;
-  if (!finite_nonnegative(lr) || !finite_nonnegative(eps) || !finite_nonnegative(weight_decay) ||
-      !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || step < 1)
-    return BSFP8_ERR_ARGUMENT;
-  if (num_tensors <= 0 || num_chunks < 0 || num_chunks > 0x7fffffff) return BSFP8_ERR_SHAPE;
-  if (num_chunks == 0) return BSFP8_OK;  // only empty tensors
-  if (device_plan == nullptr) return BSFP8_ERR_NULL_POINTER;
-  if (!aligned16(device_plan) || !aligned4(lr_dev) || !aligned4(step_dev) || !aligned4(grad_scale) ||
-      !aligned4(noop_flag))
-    return BSFP8_ERR_ALIGNMENT;
-  return bsfp8::launch_adamw(device_plan, num_tensors, num_chunks, param_dtype == BSFP8_F32, grad_dtype == BSFP8_F32,
-                             state == BSFP8_STATE_8BIT, lr, beta1, beta2, eps, weight_decay, step, lr_dev, step_dev,
-                             grad_scale, noop_flag, (hipStream_t)stream);
+  return adamw_step(device_plan, num_tensors, num_chunks, param_dtype, grad_dtype, state, lr, beta1, beta2, eps,
+                    weight_decay, step, lr_dev, step_dev, grad_scale, noop_flag, nullptr, stream);
+}
+
+int bsfp8_adamw_step_stochastic(const void* device_plan, int32_t num_tensors, int64_t num_chunks, int param_dtype,
+                                int grad_dtype, int state, double lr, double beta1, double beta2, double eps,
+                                double weight_decay, int64_t step, const float* lr_dev, const int32_t* step_dev,
+                                const float* grad_scale, const float* noop_flag, uint64_t seed, void* stream) {
+  return adamw_step(device_plan, num_tensors, num_chunks, param_dtype, grad_dtype, state, lr, beta1, beta2, eps,
+                    weight_decay, step, lr_dev, step_dev, grad_scale, noop_flag, &seed, stream);
 }
 
 const char* bsfp8_strerror(int code) {

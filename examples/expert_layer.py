@@ -29,7 +29,7 @@ class ExpertLayer:
         def rand(*shape, scale):
             return torch.randn(shape, generator=g, device=device) * scale
 
-        self.h, self.f, self.e, self.dev = hidden, ffn, experts, device
+        self.h, self.f, self.e, self.dev, self.seed = hidden, ffn, experts, device, seed
         self.w1 = rand(experts * 2 * ffn, hidden, scale=hidden ** -0.5)  # each expert's a rows, then its b rows
         self.w2 = rand(experts * hidden, ffn, scale=ffn ** -0.5)
         # norm weights are kept as their distance from 1 (weight_offset), so that weight decay pulls them there
@@ -101,7 +101,7 @@ class ExpertLayer:
 
     def update(self, lr, **more):
         self.step += 1
-        bs.adamw_step(self.plan, lr, step=self.step, **more)
+        bs.adamw_step(self.plan, lr, step=self.step, seed=self.seed, **more)  # (8-bit states: stochastic rounding)
         self.quantize_weights()
 
 

@@ -412,7 +412,11 @@ int bsfp8_residual_norm_grad(int64_t rows, int64_t cols, int stream_dtype, const
  * BSFP8_STATE_8BIT: m and u = sqrt(v) are e4m3 arrays; every 128 consecutive elements of a tensor
  *   (the last block may be shorter) share one fp32 scale sf = max(amax * (1/448), 1e-30), a code
  *   standing for code * sf.  New states are stored as e4m3(m * (1 / sf)); p uses them unrounded.
- *   Zeroed codes and scales are a valid start.
+ *   Zeroed codes and scales are a valid start.  bsfp8_adamw_step rounds to nearest: while another
+ *   element holds its block's scale, a state that changes by less than half a code's step (3 to 6
+ *   percent) a step stays where it is.  sqrt(v) loses 1 - sqrt(beta2) a step, so under nearest rounding it
+ *   does not follow gradients that become smaller (the element's updates stay small), and the lowest
+ *   codes of m do not vanish when its gradients stop.  bsfp8_adamw_step_stochastic is for training.
  * Non-finite gradients enter the states; noop_flag is for skipping such a step.
  */
 #define BSFP8_STATE_F32 0
@@ -451,6 +455,17 @@ int bsfp8_adamw_step(const void* device_plan, int32_t num_tensors, int64_t num_c
                      int grad_dtype, int state, double lr, double beta1, double beta2, double eps,
                      double weight_decay, int64_t step, const float* lr_dev, const int32_t* step_dev,
                      const float* grad_scale, const float* noop_flag, void* stream);
+/*
+ * The same step with stochastic rounding of 8-bit states: each goes to one of the two e4m3 values around it,
+ * with the probability (to 2^-17) that makes the expected state the unrounded one; a state that is a code
+ * stays.  The random bits are a function of seed, step, the tensor's index in the plan and the element alone:
+ * the same arguments give the same states.  p and copy are those of bsfp8_adamw_step.  With
+ * BSFP8_STATE_F32 nothing is rounded and seed has no effect.
+ */
+int bsfp8_adamw_step_stochastic(const void* device_plan, int32_t num_tensors, int64_t num_chunks, int param_dtype,
+                                int grad_dtype, int state, double lr, double beta1, double beta2, double eps,
+                                double weight_decay, int64_t step, const float* lr_dev, const int32_t* step_dev,
+                                const float* grad_scale, const float* noop_flag, uint64_t seed, void* stream);
 
 /* Static description of a return code. */
 const char* bsfp8_strerror(int code);
