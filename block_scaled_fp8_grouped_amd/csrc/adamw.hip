@@ -8,7 +8,8 @@
 //
 // 8-bit states: m and u = sqrt(v) as e4m3, one fp32 scale (largest magnitude times 1/448) per 128
 // consecutive elements of a tensor.  u instead of v: v spans the square of the gradients' range,
-// u's codes keep 2^17 of it with 4 significant bits each, and u is what the update divides by.  A
+// u's codes span 2^18, the upper 2^15 of it with 4 significant bits each, and u is what the update
+// divides by; a u below the smallest code is raised to it, so that no update is divided by nothing.  A
 // scale in fp32 rather than a power of two: the block's largest state is then always the code 448
 // and decays with the scale step by step, where a power-of-two scale would leave the code itself
 // to decay.  The update itself uses m and u before they are rounded.
@@ -236,8 +237,10 @@ __global__ __launch_bounds__(adam_threads<Q8>()) void adamw_kernel(AdamArgs a) {
         // lanes past the tensor's end hold zeros, which leave their block's largest as it is
         const float sm = block_scale(m), sv = block_scale(root_v);
         const float im = 1.0f / sm, iv = 1.0f / sv;
+        bool nonzero[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+          nonzero[i] = root_v[i] > 0.0f;
           m[i] *= im;
           root_v[i] *= iv;
         }
@@ -250,6 +253,11 @@ __global__ __launch_bounds__(adam_threads<Q8>()) void adamw_kernel(AdamArgs a) {
             root_v[i] = round_by(root_v[i], (uint32_t)(bits_v >> (16 * i)) & 0xffffu);
           }
         }
+        // A second state that is not zero keeps a code that is not: m, which has a scale of its own, may keep one
+        // there, and the next step divides it by this. 
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (nonzero[i] && root_v[i] < 0x1p-9f) root_v[i] = 0x1p-9f;
         store4_codes<NT>(m8 + at, n, m);
         store4_codes<NT>(v8 + at, n, root_v);
         if ((threadIdx.x & 31) == 0 && n > 0) {

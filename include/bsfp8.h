@@ -411,11 +411,12 @@ int bsfp8_residual_norm_grad(int64_t rows, int64_t cols, int stream_dtype, const
  * BSFP8_STATE_F32: m and v are fp32 arrays.
  * BSFP8_STATE_8BIT: m and u = sqrt(v) are e4m3 arrays; every 128 consecutive elements of a tensor
  *   (the last block may be shorter) share one fp32 scale sf = max(amax * (1/448), 1e-30), a code
- *   standing for code * sf.  New states are stored as e4m3(m * (1 / sf)); p uses them unrounded.
- *   Zeroed codes and scales are a valid start.  bsfp8_adamw_step rounds to nearest: while another
- *   element holds its block's scale, a state that changes by less than half a code's step (3 to 6
- *   percent) a step stays where it is.  sqrt(v) loses 1 - sqrt(beta2) a step, so under nearest rounding it
- *   does not follow gradients that become smaller (the element's updates stay small), and the lowest
+ *   standing for code * sf.  New states are stored as e4m3(m * (1 / sf)), a u that is not zero as at
+ *   least the smallest code, 2^-9; p uses them unrounded.  Zeroed codes and scales are a valid start.
+ *   bsfp8_adamw_step rounds to nearest: while another element holds its block's scale, a state that
+ *   changes by less than half a code's step (3 to 6 percent) a step stays where it is.  sqrt(v) loses
+ *   1 - sqrt(beta2) a step, so under nearest rounding it does not follow gradients that become smaller
+ *   (the element's updates stay small) and lags behind ones that grow, and the lowest
  *   codes of m do not vanish when its gradients stop.  bsfp8_adamw_step_stochastic is for training.
  * Non-finite gradients enter the states; noop_flag is for skipping such a step.
  */
