@@ -248,6 +248,15 @@ def __getattr__(name):
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
+def _native_done(got, what):
+    """Whether the native path took a call; raises for one that it made and that failed."""
+    if got is None:
+        return False
+    if type(got) is int:
+        _check(got, what)
+    return True
+
+
 def _use_native():
     if not torch.cuda.is_initialized():  # there are no device tensors
         return False
@@ -456,10 +465,10 @@ def grouped_gemm_swiglu(x_q, hidden, w_q, ffn, split_sizes, capacity_rows, recip
     y_dtype says), out (alloc_quantized for [R, ffn]) receives y quantized in the layouts it holds.
     Returns a dict of those.  Rows past sum(split_sizes) are untouched."""
     q = out or {}
-    if _use_native() and _native.swiglu(
+    if _use_native() and _native_done(_native.swiglu(
             x_q.get("row_q"), x_q.get("row_s"), capacity_rows, hidden, w_q.get("row_q"), w_q.get("row_s"), ffn, split_sizes,
             recipe, y_dtype, probs, ab, y, q.get("row_q"), q.get("row_s"), q.get("col_q"), q.get("col_s"), status,
-            _stream(stream)):
+            _stream(stream)), "grouped_gemm_swiglu"):
         return _glu_result(out, ab=ab, y=y)
     E, R = int(split_sizes.numel()), capacity_rows
     f32 = y_dtype == OUT_F32
@@ -495,10 +504,10 @@ def grouped_gemm_swiglu_grad(dy_q, hidden, w_q, ffn, ab, split_sizes, capacity_r
             return grouped_gemm_swiglu_grad(dy_q, hidden, w_q, ffn, ab, split_sizes, capacity_rows, recipe, probs, dab, out,
                                             dprobs, None, status)
     q = out or {}
-    if _use_native() and _native.swiglu_grad(
+    if _use_native() and _native_done(_native.swiglu_grad(
             dy_q.get("row_q"), dy_q.get("row_s"), capacity_rows, hidden, w_q.get("col_q"), w_q.get("col_s"), ffn,
             split_sizes, recipe, ab, probs, dab, q.get("row_q"), q.get("row_s"), q.get("col_q"), q.get("col_s"), dprobs,
-            workspace, status, _stream(stream)):
+            workspace, status, _stream(stream)), "grouped_gemm_swiglu_grad"):
         return _glu_result(out, dab=dab, dprobs=dprobs)
     E, R = int(split_sizes.numel()), capacity_rows
     which, *q = _glu_quantized(out, R, 2 * ffn, E)
@@ -580,7 +589,7 @@ def residual_norm(x, y=None, post_weight=None, pre_weight=None, gate=None, gate_
     if _use_native():
         got = _native.residual_norm(x, y, post_weight, pre_weight, gate, gate_kind, x_scale, y_scale, eps, weight_offset,
                                     r, n, rstd_y, rstd_r, _stream(stream))
-        if got is not None:
+        if _native_done(got, "residual_norm"):
             out = {"r": got[0]}
             if pre_weight is not None:
                 out["n"], out["rstd_r"] = got[1], got[3]
@@ -654,7 +663,7 @@ def residual_norm_grad(dn, dr, r=None, rstd_r=None, pre_weight=None, y=None, rst
         got = _native.residual_norm_grad(dn, dr, r, rstd_r, pre_weight, y, rstd_y, post_weight, gate, gate_kind, x_scale,
                                          y_scale, weight_offset, dx, dy, dpre_weight, dpost_weight, dgate, accumulate,
                                          workspace, _stream(stream))
-        if got is not None:
+        if _native_done(got, "residual_norm_grad"):
             out = {"dx": got[0]}
             for name, of, value in (("dy", y, got[1]), ("dpre_weight", pre_weight, got[2]),
                                     ("dpost_weight", post_weight, got[3]), ("dgate", gate, got[4])):

@@ -2,8 +2,9 @@
 // allocations and the C ABI call of the residual norms and the gated projections in one native function each.
 //
 // Every function answers None where an argument is not what the kernels take (another type, host memory, a wrong
-// shape, a size too small, an error code of the library): the caller then takes its own path, which names the
-// argument in its error.  Nothing is launched in that case.  Four tokens of 7168 columns: 12.4 us per call with
+// shape, a size too small, an argument that the library refuses): the caller then takes its own path, which names
+// the argument in its error.  Nothing has been launched in that case.  A failed launch is answered with the
+// library's code instead: a kernel may have been queued before it, so the call must not be made again.  Four tokens of 7168 columns: 12.4 us per call with
 // the checks and the allocations in Python.
 #include <Python.h>
 
@@ -94,6 +95,12 @@ struct Out {
   }
 };
 
+// What a call that returned an error answers.
+PyObject* refused(int rc) {
+  if (rc == BSFP8_ERR_LAUNCH) return PyLong_FromLong(rc);
+  Py_RETURN_NONE;
+}
+
 constexpr at::ScalarType F32 = at::kFloat, BF16 = at::kBFloat16;
 
 // (x, y, post_weight, pre_weight, gate, gate_kind, x_scale, y_scale, eps, weight_offset, r, n, rstd_y, rstd_r,
@@ -120,7 +127,7 @@ PyObject* residual_norm(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   const int rc = bsfp8_residual_norm(rows, cols, ptr(x), x->scalar_type() == F32 ? BSFP8_F32 : BSFP8_BF16, ptr(y),
                                      (const float*)ptr(post), (const float*)ptr(pre), (const float*)ptr(gate), kind, xs,
                                      ys, eps, off, pr, pn, py, prr, (void*)stream);
-  if (rc != BSFP8_OK) Py_RETURN_NONE;
+  if (rc != BSFP8_OK) return refused(rc);
   return Py_BuildValue("(NNNN)", r.object(), n.object(), ry.object(), rr.object());
 }
 
@@ -166,7 +173,7 @@ PyObject* residual_norm_grad(PyObject*, PyObject* const* argv, Py_ssize_t argc) 
       rows, cols, type == F32 ? BSFP8_F32 : BSFP8_BF16, ptr(dn), ptr(dr), ptr(r), (const float*)ptr(rr),
       (const float*)ptr(pre), ptr(y), (const float*)ptr(ry), (const float*)ptr(post), (const float*)ptr(gate), kind, xs,
       ys, off, pdx, pdy, pp, pq, pg, accumulate, work.data_ptr(), (void*)stream);
-  if (rc != BSFP8_OK) Py_RETURN_NONE;
+  if (rc != BSFP8_OK) return refused(rc);
   return Py_BuildValue("(NNNNN)", dx.object(), dy.object(), dpre.object(), dpost.object(), dgate.object());
 }
 
@@ -219,7 +226,7 @@ PyObject* swiglu(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
       (const float*)ptr(probs), (const int32_t*)ptr(splits), (int32_t)E, recipe, ptr(ab), ptr(y), y_dtype, q.which,
       (uint8_t*)ptr(q.row_q), (uint8_t*)ptr(q.row_s), (uint8_t*)ptr(q.col_q), (uint8_t*)ptr(q.col_s),
       (uint32_t*)ptr(status), (void*)stream);
-  if (rc != BSFP8_OK) Py_RETURN_NONE;
+  if (rc != BSFP8_OK) return refused(rc);
   Py_RETURN_TRUE;
 }
 
@@ -265,7 +272,7 @@ PyObject* swiglu_grad(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
       ptr(ab), (const float*)ptr(probs), (const int32_t*)ptr(splits), (int32_t)E, recipe, ptr(dab), q.which,
       (uint8_t*)ptr(q.row_q), (uint8_t*)ptr(q.row_s), (uint8_t*)ptr(q.col_q), (uint8_t*)ptr(q.col_s),
       (float*)ptr(dprobs), work.defined() ? work.data_ptr() : nullptr, (uint32_t*)ptr(status), (void*)stream);
-  if (rc != BSFP8_OK) Py_RETURN_NONE;
+  if (rc != BSFP8_OK) return refused(rc);
   Py_RETURN_TRUE;
 }
 
