@@ -290,8 +290,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024, VPT == 1 ? 7 : 4) void residual_
 // ROWS rows at a time: their loads are in flight together and their reductions share a barrier.  With two,
 // the last thread of a row whose length is not a multiple of 8 takes the row's last 8 elements instead of a
 // part of a chunk (loads by element cost more registers than 16 waves leave); the first `shift` of them are
-// its neighbour's: their factors are zero here, which keeps them out of the row's sums, and they are not
-// stored.
+// its neighbour's: their factors are zero here, which keeps them out of the row's sums, what has come from dr
+// is dropped, and they are not stored.
 template <class XT, bool WAVE, int VPT, int ROWS>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void residual_norm_grad_kernel(NormArgs a) {
   constexpr bool HOLD = VPT == 1;
@@ -401,6 +401,15 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void residual_norm_grad_kernel(N
           d[j][i][e] = a.dr != nullptr ? d0[j][i][e] : 0.0f;
           if (has_n)
             d[j][i][e] = __builtin_fmaf(rr[j], __builtin_fmaf(-r[j][i][e], m, n[j][i][e] * wq[i][e]), d[j][i][e]);
+        }
+        if constexpr (WHOLE) {
+          // the neighbour's elements: where dx is dr it may have written them before they were read here, and a zero
+          // factor does not keep an infinity out of the row's sum
+          if (shift != 0) {
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+              if (e < shift) d[j][i][e] = 0.0f;
+          }
         }
         if (a.dx != nullptr) {
           const uint32_t c = (t + i * NT) * 8 - shift;
