@@ -169,9 +169,12 @@ struct RowSum {
   }
 };
 
-// (the hardware's reciprocal square root, within 1 ulp of fp32)
+// The hardware's reciprocal square root, within 1 ulp of fp32.  It takes subnormal numbers for zero: small arguments (an
+// eps below 2^-100 and a row that is smaller still) are scaled by an even power of two.
 __device__ __forceinline__ float rstd_of(float sum, float inv_c, float eps) {
-  return __builtin_amdgcn_rsqf(sum * inv_c + eps);
+  const float v = sum * inv_c + eps;
+  const bool small = v < 0x1p-100f;
+  return __builtin_amdgcn_rsqf(small ? v * 0x1p100f : v) * (small ? 0x1p50f : 1.0f);
 }
 
 // The factors of 8 columns: pre_weight + offset, and (post_weight + offset) times a channel's gate.

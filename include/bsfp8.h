@@ -359,7 +359,8 @@ int bsfp8_grouped_gemm_swiglu_grad(const uint8_t* dy_row_q, const uint8_t* dy_ro
  * r            [rows][cols] of stream_dtype; may be x itself, and may be NULL where pre_weight is given
  * n            [rows][cols] bf16 (required with pre_weight, NULL without)
  * rstd_y, rstd_r  fp32 [rows], kept for the gradient, or NULL
- * r and n are each rounded once from the fp32 values (n from r before its rounding).  Any rows and
+ * r and n are each rounded once from the fp32 values (n from r before its rounding).  A row of zeros
+ * with eps == 0 gives NaN, and a mean square below 2^-126 has the precision of a subnormal fp32.  Any rows and
  * any cols in [1, 32768]; data pointers aligned to 16 bytes, each array contiguous.  Without y,
  * post_weight and gate must be NULL.
  * rows == 0 returns BSFP8_OK without touching any pointer.
