@@ -10,9 +10,11 @@ typedef short v8s __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ float to_f32(short b) { return __uint_as_float((uint32_t)(uint16_t)b << 16); }
 
-// Sigmoid in fp32 from the hardware's 2^x and reciprocal (each within 1 ulp; the result within 4,
-// below the rounding of every form the outputs are kept in): 2^x beyond fp32's range is inf or 0,
-// which gives the limits 0 and 1.
+// Sigmoid in fp32 from the hardware's 2^x and reciprocal, each within 1 ulp.  The argument of 2^x is rounded, which for
+// a < 0 is an error of up to 1.22 |a| units of 2^-24 beside the 5 of the rest: as much as an a off by 1 ulp, where a's own sum
+// is off by more.  Below the rounding of bf16 and e4m3 outputs (8 |a| 2^-24 < 2^-9 up to the largest |a| with a sigmoid above 0);
+// fp32 outputs of y and dprobs carry it.  2^x beyond fp32's range is inf or 0, which gives the limits 0 and 1; a sigmoid
+// below 2^-126 (a < -87.3) is 0.
 __device__ __forceinline__ float sigmoid_fast(float a) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(a * -1.44269504f));
 }
@@ -31,7 +33,8 @@ __device__ __forceinline__ void swiglu_grad(float a, float b, float p, float d, 
   da = d * p * b * slope;
 }
 
-// max(m, |a|, |b|) in one instruction (NaN operands are passed over)
+// max(m, |a|, |b|) in one instruction.  NaN operands are passed over: a NaN leaves the scale of its block to the other values
+// (the quantize kernels, whose maximum is one of bit patterns, take the scale of an infinity for it).
 __device__ __forceinline__ float max3_abs(float m, float a, float b) {
   asm("v_max3_f32 %0, %0, |%1|, |%2|" : "+v"(m) : "v"(a), "v"(b));
   return m;
@@ -44,8 +47,8 @@ __device__ __forceinline__ uint32_t e8m0_byte(float amax) {
   return f > 8u ? f - 8u : 0u;
 }
 // Four fp32 -> four e4m3 codes of v / 2^(byte - 127): the conversion divides by its scale operand, of which it uses
-// the exponent field alone (equal to the multiplication by 2^-e and the plain conversion: checked on the
-// GPU for every byte over 252 million values).
+// the exponent field alone (0 stands for 2^-127), and rounds as the multiplication by 2^-e and the plain conversion do.  Infinities
+// and NaN become NaN codes.
 __device__ __forceinline__ uint32_t e4m3x4_scaled(float a, float b, float c, float d, float scale) {
   typedef short v2s __attribute__((ext_vector_type(2)));
   v2s w = {0, 0};

@@ -288,7 +288,8 @@ int bsfp8_grouped_gemm_dgrad(const uint8_t* dy_row_q, const uint8_t* dy_row_s, i
 /*
  * For the live rows t of expert e, products accumulated in fp32 (operands widened exactly):
  *     a = x[t] W1_e[0 .. ffn)^T,  b = x[t] W1_e[ffn .. 2 ffn)^T,  y = probs[t] * silu(a) * b
- * with silu(a) = a / (1 + exp(-a)) in fp32, from the unrounded a and b.
+ * with silu(a) = a / (1 + exp(-a)) in fp32, from the unrounded a and b (y within (1.25 |a| + 12) 2^-24 of its value at
+ * these a and b).
  * x_row_q, x_row_s  rowwise output of bsfp8_grouped_quantize for x [capacity_rows][hidden]
  * w_q, w_s          rowwise output for W1 [num_groups * 2 ffn][hidden] (split_sizes NULL): expert e's
  *                   a rows, then its b rows
@@ -297,7 +298,9 @@ int bsfp8_grouped_gemm_dgrad(const uint8_t* dy_row_q, const uint8_t* dy_row_s, i
  * y                 [capacity_rows][ffn] of y_dtype (BSFP8_OUT_F32 or BSFP8_OUT_BF16), or NULL
  * which, row_q, row_s, col_q, col_s   y quantized from its fp32 values, laid out as
  *                   bsfp8_grouped_quantize does for [capacity_rows][ffn]; which == 0: none
- * At least one of ab, y and the quantized layouts is asked for.  Rows at or past sum(k_e) are not
+ * At least one of ab, y and the quantized layouts is asked for.  In the quantized layouts of both directions a value
+ * that is not finite has a NaN code; a NaN leaves its block's scale to the block's other values (bsfp8_grouped_quantize
+ * gives such a block the scale of an infinity, 2^120).  Rows at or past sum(k_e) are not
  * written.  hidden and ffn are multiples of 32, hidden at most 2^22, ffn at most 2^20.
  * capacity_rows == 0 returns BSFP8_OK without touching any pointer.
  */
