@@ -51,25 +51,34 @@ def _link(objs, path):
 
 
 def _binding():
-    import sysconfig
+    """The native host path, or None and the reason where it cannot be compiled (no C++ compiler, no Python or torch
+    headers): the package then takes the ctypes path.  What was built before is not left beside a new library."""
+    if os.path.exists(BINDING_PATH):
+        os.remove(BINDING_PATH)
+    try:
+        import sysconfig
 
-    import torch
-    from torch.utils.cpp_extension import include_paths
-    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-DAT_PER_OPERATOR_HEADERS",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + sysconfig.get_paths()["include"]]
-    cmd += ["-isystem" + p for p in include_paths()]
-    cmd += [os.path.join(CSRC, BINDING_SOURCE), "-o", BINDING_PATH + ".tmp", "-L" + lib, "-ltorch_python", "-ltorch_cpu",
-            "-lc10", "-L" + HERE, "-lbsfp8", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+        import torch
+        from torch.utils.cpp_extension import include_paths
+        lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-DAT_PER_OPERATOR_HEADERS",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               "-I" + sysconfig.get_paths()["include"]]
+        cmd += ["-isystem" + p for p in include_paths()]
+        cmd += [os.path.join(CSRC, BINDING_SOURCE), "-o", BINDING_PATH + ".tmp", "-L" + lib, "-ltorch_python",
+                "-ltorch_cpu", "-lc10", "-L" + HERE, "-lbsfp8", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except (OSError, ImportError) as e:
+        return None, str(e)
     if r.returncode != 0:
-        raise RuntimeError("binding failed:\n" + r.stderr)
+        return None, r.stderr
     os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
+    return BINDING_PATH, ""
 
 
 def build(verbose=True):
-    """Compile every source for gfx950 and link libbsfp8.so (and the probe libbsfp8_peak.so), then the
-    Python extension that calls it, next to this file."""
+    """Compile every source for gfx950 and link libbsfp8.so (and the probe libbsfp8_peak.so), then, where a C++
+    compiler and torch's headers are there, the Python extension that calls it, next to this file."""
     objdir = os.path.join(ROOT, "_build")
     os.makedirs(objdir, exist_ok=True)
     srcs = SOURCES + PEAK_SOURCES
@@ -78,9 +87,11 @@ def build(verbose=True):
         list(ex.map(_compile, srcs, objs))
     _link(objs[:len(SOURCES)], LIB_PATH)
     _link(objs[len(SOURCES):], PEAK_LIB_PATH)
-    _binding()
+    binding, why = _binding()
     if verbose:
-        print(f"built {LIB_PATH}, {PEAK_LIB_PATH} and {BINDING_PATH}", file=sys.stderr)
+        print(f"built {LIB_PATH}, {PEAK_LIB_PATH}" + (f" and {binding}" if binding else ""), file=sys.stderr)
+    if not binding:
+        print(f"{BINDING_PATH} is not built, small calls take longer on the host: {why}", file=sys.stderr)
     return LIB_PATH
 
 

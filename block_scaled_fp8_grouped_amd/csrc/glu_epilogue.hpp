@@ -14,7 +14,7 @@ __device__ __forceinline__ float to_f32(short b) { return __uint_as_float((uint3
 // a < 0 is an error of up to 1.22 |a| units of 2^-24 beside the 5 of the rest: as much as an a off by 1 ulp, where a's own sum
 // is off by more.  Below the rounding of bf16 and e4m3 outputs (8 |a| 2^-24 < 2^-9 up to the largest |a| with a sigmoid above 0);
 // fp32 outputs of y and dprobs carry it.  2^x beyond fp32's range is inf or 0, which gives the limits 0 and 1; a sigmoid
-// below 2^-126 (a < -87.3) is 0.
+// below 2^-126 (a < -87.3) may be 0.
 __device__ __forceinline__ float sigmoid_fast(float a) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(a * -1.44269504f));
 }
