@@ -9,14 +9,14 @@
 // Bound by the bf16 MFMA on large inputs: the operands stay e4m3 in HBM and LDS, are widened to
 // bf16 with their block scale folded in (exact) and accumulated in fp32, as in the plain grouped
 // GEMMs.  What the fusion saves is a bf16 round trip of the product through HBM and a launch.
-// Measured (32 experts, 65536 tokens, hidden 4096, ffn 2048, all of the layer's outputs): forward 1.96 ms =
-// 1120 TFLOP/s, gradient 1.22 ms = 900 TFLOP/s; the main loop alone runs at 1450 TFLOP/s (from two values of
+// Measured (32 experts, 65536 tokens, hidden 4096, ffn 2048, all of the layer's outputs): forward 1.97 ms =
+// 1120 TFLOP/s, gradient 1.18 ms = 930 TFLOP/s; the forward's main loop alone runs at 1450 TFLOP/s (from two values of
 // hidden), the rest is each tile's start and epilogue.  Under that load the chip holds 1.6 to 1.8 of its
-// 2.4 GHz: other schedules of the same instructions (deeper rings, half the step, LDS reads ahead, two workgroups of
-// 256 x 128) end within 3% of each other; waves of 128 x 128 (a third fewer conversions and LDS reads, but one wave
-// per SIMD) are 8% slower.
+// 2.4 GHz: other schedules of the same instructions in the 256 x 256 tiles (deeper rings, half the step, LDS reads ahead,
+// two workgroups of 256 x 128) end within 3% of each other; waves of 128 x 128 (a third fewer conversions and LDS reads,
+// but one wave per SIMD) are 8% slower.
 //
-// Tiles of 256 x 256 or 128 x 128 (tokens x rows of the weight), waves of 128 x 64 or 64 x 64, K steps of 128 or 64
+// Tiles of 256 x 256 (large forwards) or 128 x 128 (tokens x rows of the weight), waves of 128 x 64 or 64 x 64, K steps of 128 or 64
 // bytes in a ring of two or three LDS stages filled by LDS DMA, 16-byte chunks XOR-swizzled; the E8M0 bytes come
 // by DMA too and go into the conversions as they are.  A step's barrier stands before its last MFMAs: behind it the
 // stage is free, the loads of the step a ring ahead go into it and the next step's first fragments are read, both
@@ -892,18 +892,27 @@ __global__ __launch_bounds__(256) void glu_dprobs_kernel(const float* __restrict
 //  - few rows per expert, or so few tiles that the few-rows kernel's fill the chip better: at most 12 rows per
 //    expert (8 experts of 8, 4096 x 2048: 30 / 30 us, 128 x 128 tiles 41 / 52) or 512 tiles (48 rows, 2048 x 1024: 21 /
 //    20 us, 26 / 34; from 640 tiles on it loses, 39 / 34 to 25 / 34)
-//  - 128 x 128, up to two tiles per CU: K steps of 128 and two workgroups per CU (8 experts of 128 rows, 2048 x 1024 and
-//    4096 x 2048: 26 / 34 and 63 / 51 us, steps of 64 and three workgroups 27 / 37 and 67 / 57)
-//  - 128 x 128, more tiles: steps of 64, three workgroups per CU and loads two steps ahead.  With operands from HBM
-//    4099 rows of 8 experts, 4128 x 1024, 560 tiles, take 102 us, with steps of 128 106; with operands in the
-//    last-level cache the two end within 2% of each other at 2048 x 1024 and steps of 128 are up to 8% faster at 4128
-//  - 256 x 256 from 1536 tiles on (2048 rows, 32 experts of 2048 x 1024, forward, 2176 tiles: 606 us, 128 x 128 tiles
-//    615; below, 1088 tiles: gradient of the same 450 us to 405, 8 experts of 4096 x 2048 567 / 384 to 547 / 340)
+//  - the gradient: 128 x 128, K steps of 128, two workgroups per CU.  Steps of 64 and three workgroups take 0 to 11% longer
+//    (8 experts, 4128 x 1024, 6500 rows: 93 us to 86; 16384 rows: 196 to 192; 16 experts of 512 rows, 2048 x 1024, are the
+//    one shape that they suit: 79 to 81), 256 x 256 tiles 1 to 40% (16384 rows of 8 experts, 4096 x 2048: 392 to 328; 65536
+//    rows: 8 experts of 2048 x 2048 797 to 747, 32 of 4096 x 2048 1235 to 1220, 16 of 7168 x 2048 1890 to 1876)
+//  - the forward, up to two tiles per CU: the same (8 experts of 128 rows, 2048 x 1024 and 4096 x 2048: 26 and 63 us, steps
+//    of 64 27 and 67)
+//  - the forward, 128 x 128, more tiles: steps of 64, three workgroups per CU and loads two steps ahead where all tiles are
+//    on the chip at once (768; 4099 rows of 8 experts at hidden 2048, 4128, 7168 and ffn 1024: 61, 120, 170 us, steps of 128
+//    63, 120, 172) or K is short (16384 rows, 2048 x 1024, 8 and 32 experts: 179 and 187, steps of 128 181 and 192); else
+//    steps of 128, whose barriers are half as many (6500 rows of 8 experts, 4128 and 7168 x 1024: 149 and 222, steps of 64
+//    162 and 235; 16384 rows, 4128 x 1024: 318 to 336)
+//  - the forward, 256 x 256 from 4096 tiles on (65536 rows: 8 experts of 2048 x 2048 1117 us, 32 of 4096 x 2048 2012, 16 of
+//    7168 x 2048 3264; the better 128 x 128 tiles 1144, 2068, 3334.  Below: 49152 rows of 32 experts, 2048 x 2048, 3328
+//    tiles, 909 to 893, 20480 rows, 4096 x 2048, 1536 tiles, 727 to 710)
+// (operands from HBM, in sets taken in turn; random codes, which draw more power than a layer's)
 struct GluTile {
   int bm, bn, bk;
 };
 
-static GluTile glu_tile(bool grad, int64_t R, int64_t F, int E) {
+// (K is not asked for where the gradient's workspace is sized)
+static GluTile glu_tile(bool grad, int64_t R, int64_t F, int E, int64_t K) {
   auto tiles = [&](int bm, int bn) {
     const int64_t cols = grad ? bn : bn / 2;
     return (R / bm + (E + 1) / 2) * ((F + cols - 1) / cols);
@@ -911,8 +920,10 @@ static GluTile glu_tile(bool grad, int64_t R, int64_t F, int E) {
   // (the few-rows kernel addresses four block rows of scales with 32-bit offsets)
   if (R < (1 << 24) && 2 * F * E < (1 << 28) && (R <= 12 * (int64_t)E || tiles(kRowsBM, kRowsBN) <= 512))
     return {kRowsBM, kRowsBN, 0};
-  if (tiles(256, 256) >= 1536) return {256, 256, 128};
-  return {128, 128, tiles(128, 128) <= 512 ? 128 : 64};
+  if (grad) return {128, 128, 128};
+  if (tiles(256, 256) >= 4096) return {256, 256, 128};
+  const int64_t n = tiles(128, 128);
+  return {128, 128, n > 512 && (n <= 768 || K <= 2048) ? 64 : 128};
 }
 
 // Columns of one half per tile, and the tiles of a row of them.
@@ -922,7 +933,7 @@ static int64_t glu_tiles_n(bool grad, GluTile t, int64_t F) {
 }
 
 size_t glu_grad_workspace_bytes(int64_t R, int64_t F, int E) {
-  const int64_t n = glu_tiles_n(true, glu_tile(true, R, F, E), F);
+  const int64_t n = glu_tiles_n(true, glu_tile(true, R, F, E, 0), F);
   return n > 1 ? (size_t)(n * R * 4) : 0;
 }
 
@@ -945,14 +956,14 @@ static void launch_glu_tile(const GluArgs& a, dim3 grid, hipStream_t stream) {
 
 template <bool GRAD>
 static int launch_glu(GluArgs& a, hipStream_t stream) {
-  const GluTile t = glu_tile(GRAD, a.R, a.F, a.E);
+  const GluTile t = glu_tile(GRAD, a.R, a.F, a.E, a.K);
   dim3 grid;
   const int rc = glu_grid(a, GRAD, t, &grid);
   if (rc != BSFP8_OK) return rc;
   if (t.bm == kRowsBM) hipLaunchKernelGGL((glu_rows_kernel<GRAD>), grid, dim3(64 * kRowsNW), 0, stream, a);
-  else if (t.bn == 256) launch_glu_tile<GRAD, 256, 256, 64, 128, 2>(a, grid, stream);
-  else if (t.bk == 128) launch_glu_tile<GRAD, 128, 128, 64, 128, 2>(a, grid, stream);
-  else launch_glu_tile<GRAD, 128, 128, 64, 64, 3>(a, grid, stream);
+  else if (GRAD || (t.bn == 128 && t.bk == 128)) launch_glu_tile<GRAD, 128, 128, 64, 128, 2>(a, grid, stream);
+  else if (t.bn == 256) launch_glu_tile<false, 256, 256, 64, 128, 2>(a, grid, stream);
+  else launch_glu_tile<false, 128, 128, 64, 64, 3>(a, grid, stream);
   return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
 }
 
@@ -1005,7 +1016,7 @@ int launch_grouped_gemm_swiglu_grad(const uint8_t* dy_q, const uint8_t* dy_s, in
   a.ab = (uint16_t*)const_cast<void*>(ab);
   a.out = GluOut{dab, 0, row_q, row_s, col_q, col_s};
   a.status = status;
-  const bool parts = dprobs != nullptr && glu_tiles_n(true, glu_tile(true, R, F, E), F) > 1;
+  const bool parts = dprobs != nullptr && glu_tiles_n(true, glu_tile(true, R, F, E, hidden), F) > 1;
   a.dpart = parts ? workspace : dprobs;
   const int rc = launch_glu<true>(a, stream);
   if (rc != BSFP8_OK || !parts) return rc;
