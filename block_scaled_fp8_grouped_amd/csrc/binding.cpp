@@ -47,6 +47,14 @@ struct Args {
     }
     return v;
   }
+  bool truth() {
+    const int v = PyObject_IsTrue(next());
+    if (v < 0) {
+      PyErr_Clear();
+      ok = false;
+    }
+    return v == 1;
+  }
   // a contiguous device tensor of one of two element types, or nullptr for None
   const at::Tensor* tensor(at::ScalarType a, at::ScalarType b) {
     PyObject* o = next();
@@ -146,7 +154,7 @@ PyObject* residual_norm_grad(PyObject*, PyObject* const* argv, Py_ssize_t argc) 
   Out dx{a.tensor(type), {}, true}, dy{a.tensor(BF16, at::kShort), {}, y != nullptr};
   Out dpre{a.tensor(F32), {}, pre != nullptr}, dpost{a.tensor(F32), {}, post != nullptr};
   Out dgate{a.tensor(F32), {}, gate != nullptr};
-  const int accumulate = PyObject_IsTrue(a.next()) == 1;
+  const int accumulate = a.truth();
   const int64_t rows = ref->size(0), cols = ref->size(1), need = bsfp8_residual_norm_grad_workspace_bytes(rows, cols);
   PyObject* ws = a.next();
   at::Tensor work;
