@@ -422,7 +422,8 @@ int bsfp8_residual_norm_grad(int64_t rows, int64_t cols, int stream_dtype, const
  *   1 - sqrt(beta2) a step, so under nearest rounding it does not follow gradients that become smaller
  *   (the element's updates stay small) and lags behind ones that grow, and the lowest
  *   codes of m do not vanish when its gradients stop.  bsfp8_adamw_step_stochastic is for training.
- * Non-finite gradients enter the states; noop_flag is for skipping such a step.
+ * Non-finite gradients enter the states (8-bit: an infinite one makes its block's scale infinite, and all 128
+ * elements NaN in the next step); noop_flag is for skipping such a step.
  */
 #define BSFP8_STATE_F32 0
 #define BSFP8_STATE_8BIT 1
@@ -452,7 +453,8 @@ int bsfp8_adamw_plan(const bsfp8_adamw_tensor* tensors, int32_t num_tensors, int
  * One step over the plan's tensors (param_dtype, grad_dtype, state and the counts as it was made with).
  * lr >= 0, 0 <= beta1, beta2 < 1, eps >= 0, weight_decay >= 0, step >= 1 (BSFP8_ERR_ARGUMENT).
  * lr_dev, step_dev  NULL, or device scalars that replace lr and step, read when the kernel runs (a
- *                   captured graph is replayed with new values)
+ *                   captured graph is replayed with new values); the same bounds hold for them, which
+ *                   are not checked there
  * grad_scale        NULL (1), or a device fp32 scalar (clipping, loss scale)
  * noop_flag         NULL, or a device fp32 scalar: nonzero leaves everything as it is
  */
@@ -462,10 +464,10 @@ int bsfp8_adamw_step(const void* device_plan, int32_t num_tensors, int64_t num_c
                      const float* grad_scale, const float* noop_flag, void* stream);
 /*
  * The same step with stochastic rounding of 8-bit states: each goes to one of the two e4m3 values around it,
- * with the probability (to 2^-17) that makes the expected state the unrounded one; a state that is a code
- * stays.  The random bits are a function of seed, step, the tensor's index in the plan and the element alone:
- * the same arguments give the same states.  p and copy are those of bsfp8_adamw_step.  With
- * BSFP8_STATE_F32 nothing is rounded and seed has no effect.
+ * with the probability that makes the expected state the unrounded one; a state that is a code stays.  The
+ * random bits are a function of seed, step, the tensor's index in the plan and the element alone: the same
+ * arguments give the same states.  p and copy are those of bsfp8_adamw_step.  With BSFP8_STATE_F32 nothing
+ * is rounded and seed has no effect.
  */
 int bsfp8_adamw_step_stochastic(const void* device_plan, int32_t num_tensors, int64_t num_chunks, int param_dtype,
                                 int grad_dtype, int state, double lr, double beta1, double beta2, double eps,
