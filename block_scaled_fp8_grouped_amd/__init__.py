@@ -581,7 +581,7 @@ def residual_norm(x, y=None, post_weight=None, pre_weight=None, gate=None, gate_
     post_weight, pre_weight: fp32 [cols]; None leaves out that norm (without pre_weight there is no
     n).  gate: fp32 [cols] (GATE_CHANNEL) or [rows] (GATE_TOKEN).  Returns a dict of r (x's type), n
     (bf16), rstd_y and rstd_r (fp32 [rows], for the gradient), in the tensors given or in new ones;
-    r may be x."""
+    r may be x.  Data begins at multiples of 16 bytes."""
     if _elsewhere(stream):
         with _on(stream):
             return residual_norm(x, y, post_weight, pre_weight, gate, gate_kind, x_scale, y_scale, eps, weight_offset, r, n,
@@ -748,7 +748,8 @@ def adamw_plan(params, grads, exp_avgs, exp_avg_sqs, exp_avg_scales=None, exp_av
     states exp_avgs and exp_avg_sqs as fp32, or as e4m3 codes (uint8 or float8_e4m3fn) with the fp32
     scales [ceil(numel / 128)] in exp_avg_scales and exp_avg_sq_scales (the second state is sqrt(v);
     zeroed codes and scales are a valid start).  copies: bf16 tensors (or None) that receive the new
-    params.  lr_scales, decay_scales: factors on lr and weight_decay per tensor (default 1)."""
+    params.  lr_scales, decay_scales: factors on lr and weight_decay per tensor (default 1).  Laid out once
+    for tensors that stay where they are: it takes some 4 us per tensor on the host."""
     n = len(params)
     if n == 0:
         raise ValueError("adamw_plan: no tensors")

@@ -115,7 +115,6 @@ int check_glu_shape(int64_t capacity_rows, int64_t hidden, int64_t ffn, int32_t 
   return BSFP8_OK;
 }
 
-
 // an AdamW step; seed: NULL, or that of the 8-bit states' stochastic rounding
 int adamw_step(const void* device_plan, int32_t num_tensors, int64_t num_chunks, int param_dtype, int grad_dtype,
                int state, double lr, double beta1, double beta2, double eps, double weight_decay, int64_t step,
@@ -136,6 +135,7 @@ int adamw_step(const void* device_plan, int32_t num_tensors, int64_t num_chunks,
                              state == BSFP8_STATE_8BIT, lr, beta1, beta2, eps, weight_decay, step, lr_dev, step_dev,
                              grad_scale, noop_flag, seed, (hipStream_t)stream);
 }
+
 }  // namespace
 
 extern "C" {
