@@ -42,6 +42,9 @@ GATE_CHANNEL = 1  # gate[cols]
 GATE_TOKEN = 2  # gate[rows]
 STATE_F32 = 0
 STATE_8BIT = 1
+ROUTE_SOFTMAX = 1  # BSFP8_ROUTE_SOFTMAX: scores of softmax(logits)
+ROUTE_SIGMOID = 2  # BSFP8_ROUTE_SIGMOID: scores of sigmoid(logits)
+MAX_TOP_K = 32
 
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
@@ -116,6 +119,36 @@ def lib():
                                        _i64, _vp, _vp, _vp, _vp, _vp]
         L.bsfp8_adamw_step_stochastic.restype = ctypes.c_int
         L.bsfp8_adamw_step_stochastic.argtypes = L.bsfp8_adamw_step.argtypes[:-1] + [ctypes.c_uint64, _vp]
+        L.bsfp8_route_topk_workspace_bytes.restype = _sz
+        L.bsfp8_route_topk_workspace_bytes.argtypes = [_i64, _i32]
+        L.bsfp8_route_topk.restype = ctypes.c_int
+        L.bsfp8_route_topk.argtypes = [_vp, ctypes.c_int, _i64, _i32, _i32, ctypes.c_int, _vp, ctypes.c_int, _f, _vp, _vp,
+                                       _vp, _vp, _vp]
+        L.bsfp8_route_topk_grad.restype = ctypes.c_int
+        L.bsfp8_route_topk_grad.argtypes = [_vp, _vp, ctypes.c_int, _vp, _i64, _i32, _i32, ctypes.c_int, ctypes.c_int, _f,
+                                            _vp, _vp, _vp]
+        L.bsfp8_dispatch_plan_workspace_bytes.restype = _sz
+        L.bsfp8_dispatch_plan_workspace_bytes.argtypes = [_i64, _i32, _i32]
+        L.bsfp8_dispatch_plan.restype = ctypes.c_int
+        L.bsfp8_dispatch_plan.argtypes = [_vp, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp]
+        L.bsfp8_dispatch.restype = ctypes.c_int
+        L.bsfp8_dispatch.argtypes = [_vp, ctypes.c_int, _i64, _i64, _vp, _i32, _vp, _vp, _i64, _vp]
+        L.bsfp8_dispatch_quantize.restype = ctypes.c_int
+        L.bsfp8_dispatch_quantize.argtypes = [_vp, _i64, _i64, _vp, _i32, _vp, _i64, _vp, _i32, ctypes.c_int, ctypes.c_int,
+                                              _vp, _vp, _vp, _vp, _vp, _vp]
+        L.bsfp8_combine.restype = ctypes.c_int
+        L.bsfp8_combine.argtypes = [_vp, ctypes.c_int, _i64, _i64, _vp, _i64, _i32, _vp, _vp, _vp, _vp]
+        L.bsfp8_combine_grad.restype = ctypes.c_int
+        L.bsfp8_combine_grad.argtypes = [_vp, ctypes.c_int, _i64, _i64, _vp, _i64, _vp, _i32, _vp, _vp, _vp, _vp]
+        L.bsfp8_grouped_act_checkpoint.restype = ctypes.c_int
+        L.bsfp8_grouped_act_checkpoint.argtypes = [ctypes.c_int, _vp, _vp, _i64, _i64, _vp, _i32, ctypes.c_int,
+                                                   ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+        L.bsfp8_grouped_act_checkpoint_grad_workspace_bytes.restype = _sz
+        L.bsfp8_grouped_act_checkpoint_grad_workspace_bytes.argtypes = [_i64, _i64]
+        L.bsfp8_grouped_act_checkpoint_grad.restype = ctypes.c_int
+        L.bsfp8_grouped_act_checkpoint_grad.argtypes = [ctypes.c_int, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _i32,
+                                                        ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                                        _vp, _vp, _vp]
         L.bsfp8_strerror.restype = ctypes.c_char_p
         L.bsfp8_strerror.argtypes = [ctypes.c_int]
         _lib = L
@@ -815,3 +848,270 @@ def adamw_step(plan, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, st
         _check(lib().bsfp8_adamw_step(*args, _stream(stream)), "adamw_step")
     else:
         _check(lib().bsfp8_adamw_step_stochastic(*args, int(seed) & 0xFFFFFFFFFFFFFFFF, _stream(stream)), "adamw_step")
+
+
+# ------------------------------------------------------------------------------------------
+# tokens to their experts and back
+# ------------------------------------------------------------------------------------------
+
+def _arg(t, what, dtypes, shape=None):
+    """Pointer of a tensor argument of the calls below: as _dev checks it, on the current device, of this shape."""
+    p = _dev(t, what, dtypes)
+    if isinstance(t, torch.Tensor):
+        if shape is not None:
+            _like(t, shape, what)
+        if t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"{what}: on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return p
+
+
+def _matrix(t, what, dtypes):
+    """Pointer and shape of a [rows, cols] tensor, which has to be given."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{what}: a two-dimensional tensor is needed")
+    return _arg(t, what, dtypes), t.shape
+
+
+def _workspace(workspace, nbytes, like):
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device) if nbytes > 0 else None
+    _need(workspace, nbytes, "workspace")
+    _arg(workspace, "workspace", (workspace.dtype,))
+    return workspace
+
+
+def route_topk_workspace_bytes(tokens, num_experts):
+    return int(lib().bsfp8_route_topk_workspace_bytes(tokens, num_experts))
+
+
+def route_topk(logits, top_k, scoring=ROUTE_SOFTMAX, bias=None, renormalize=True, scale=1.0, probs=None, experts=None,
+               score_sum=None, workspace=None, stream=None):
+    """bsfp8_route_topk: each token's top_k experts and their probabilities from the router's logits [tokens, experts]
+    (fp32 or bf16).  scoring: ROUTE_SOFTMAX or ROUTE_SIGMOID; bias: fp32 [experts], moves the choice alone; renormalize:
+    the chosen scores are divided by their sum; then they are multiplied by scale.  A logit of -inf masks an expert.
+    score_sum: fp32 [experts], receives the sum of the scores over the tokens (for a load-balancing loss).  Returns a
+    dict of probs (fp32 [tokens, top_k]), experts (int32, -1 where none is left) and score_sum, where given."""
+    if _elsewhere(stream):
+        with _on(stream):
+            return route_topk(logits, top_k, scoring, bias, renormalize, scale, probs, experts, score_sum, workspace)
+    pl, (T, E) = _matrix(logits, "logits", _STREAM)
+    pb, ps = _arg(bias, "bias", _F32, (E,)), _arg(score_sum, "score_sum", _F32, (E,))
+    if probs is None:
+        probs = logits.new_empty((T, top_k), dtype=torch.float32)
+    if experts is None:
+        experts = logits.new_empty((T, top_k), dtype=torch.int32)
+    pp, pe = _arg(probs, "probs", _F32, (T, top_k)), _arg(experts, "experts", _I32, (T, top_k))
+    if score_sum is not None:
+        workspace = _workspace(workspace, route_topk_workspace_bytes(T, E), logits)
+    rc = lib().bsfp8_route_topk(pl, _dtype_code(logits), T, E, top_k, scoring, pb, 1 if renormalize else 0, scale, pp, pe,
+                                ps, _ptr(workspace) if score_sum is not None else None, _stream(stream))
+    _check(rc, "route_topk")
+    out = {"probs": probs, "experts": experts}
+    if score_sum is not None:
+        out["score_sum"] = score_sum
+    return out
+
+
+def route_topk_grad(dprobs, logits, experts, scoring=ROUTE_SOFTMAX, renormalize=True, scale=1.0, dscore_sum=None,
+                    dlogits=None, stream=None):
+    """bsfp8_route_topk_grad: the gradient at the logits, of their type, from dprobs (fp32 [tokens, top_k]), dscore_sum
+    (fp32 [experts] or None), and the experts that route_topk chose."""
+    if _elsewhere(stream):
+        with _on(stream):
+            return route_topk_grad(dprobs, logits, experts, scoring, renormalize, scale, dscore_sum, dlogits)
+    pl, (T, E) = _matrix(logits, "logits", _STREAM)
+    pe, (_, K) = _matrix(experts, "experts", _I32)
+    _like(experts, (T, K), "experts")
+    pp, ps = _arg(dprobs, "dprobs", _F32, (T, K)), _arg(dscore_sum, "dscore_sum", _F32, (E,))
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    pd = _arg(dlogits, "dlogits", (logits.dtype,), (T, E))
+    rc = lib().bsfp8_route_topk_grad(pp, pl, _dtype_code(logits), pe, T, E, K, scoring, 1 if renormalize else 0, scale, ps,
+                                     pd, _stream(stream))
+    _check(rc, "route_topk_grad")
+    return dlogits
+
+
+def dispatch_plan_workspace_bytes(tokens, top_k, num_experts):
+    return int(lib().bsfp8_dispatch_plan_workspace_bytes(tokens, top_k, num_experts))
+
+
+def dispatch_plan(experts, num_experts, probs=None, out=None, workspace=None, stream=None):
+    """bsfp8_dispatch_plan: the choices of experts (int32 [tokens, top_k]; one outside [0, num_experts) is dropped) sorted
+    by expert.  Returns a dict of splits (int32 [num_experts], the split_sizes of the grouped calls), rows (int32
+    [tokens, top_k], each choice's row or -1), choices (int32 [tokens * top_k], each row's choice or -1 past the last)
+    and, with probs (fp32 [tokens, top_k]), probs (fp32 [tokens * top_k], each row's, 0 past the last), in the tensors of
+    ``out`` or in new ones."""
+    if _elsewhere(stream):
+        with _on(stream):
+            return dispatch_plan(experts, num_experts, probs, out, workspace)
+    pe, (T, K) = _matrix(experts, "experts", _I32)
+    pp, N = _arg(probs, "probs", _F32, (T, K)), T * K
+    given, out = out or {}, {}
+    ptrs = []
+    for name, shape, dtype in (("splits", (num_experts,), torch.int32), ("rows", (T, K), torch.int32),
+                               ("choices", (N,), torch.int32), ("probs", (N,), torch.float32)):
+        if name == "probs" and probs is None:
+            ptrs.append(None)
+            continue
+        t = given.get(name)
+        if t is None:
+            t = experts.new_empty(shape, dtype=dtype)
+        ptrs.append(_arg(t, f"out[{name!r}]", (dtype,), shape))
+        out[name] = t
+    workspace = _workspace(workspace, dispatch_plan_workspace_bytes(T, K, num_experts), experts)
+    rc = lib().bsfp8_dispatch_plan(pe, pp, T, K, num_experts, *ptrs, _ptr(workspace), _stream(stream))
+    _check(rc, "dispatch_plan")
+    return out
+
+
+def _plan_rows(plan):
+    """A plan's rows and what they say: their pointer, the tokens, top_k and the rows that a buffer for them has."""
+    p, (T, K) = _matrix(plan["rows"], "plan['rows']", _I32)
+    return p, T, K, T * K
+
+
+def dispatch(x, plan, weights=None, out=None, stream=None):
+    """bsfp8_dispatch: the rows of x [tokens, cols] (fp32 or bf16) at their experts' places, out [tokens * top_k, cols],
+    times weights (fp32 [tokens, top_k] or None).  Rows past the plan's last are left as they are."""
+    if _elsewhere(stream):
+        with _on(stream):
+            return dispatch(x, plan, weights, out)
+    pr, T, K, N = _plan_rows(plan)
+    px, (_, C) = _matrix(x, "x", _STREAM)
+    _like(x, (T, C), "x")
+    pw = _arg(weights, "weights", _F32, (T, K))
+    if out is None:
+        out = x.new_empty((N, C))
+    po = _arg(out, "out", (x.dtype,), (N, C))
+    _check(lib().bsfp8_dispatch(px, _dtype_code(x), T, C, pr, K, pw, po, N, _stream(stream)), "dispatch")
+    return out
+
+
+def dispatch_quantize(x, plan, recipe, which, out, weights=None, status=None, stream=None):
+    """bsfp8_dispatch_quantize: the same rows of bf16 x [tokens, cols] quantized with an MX recipe into the layouts
+    ``which`` of ``out`` (alloc_quantized for [tokens * top_k, cols] and the plan's experts), without a copy of them in
+    between."""
+    if _elsewhere(stream):
+        with _on(stream):
+            return dispatch_quantize(x, plan, recipe, which, out, weights, status)
+    _, T, K, N = _plan_rows(plan)
+    px, (_, C) = _matrix(x, "x", _BF16)
+    _like(x, (T, C), "x")
+    splits, choices = plan["splits"], plan["choices"]
+    E = int(splits.numel())
+    args = (px, T, C, _arg(choices, "plan['choices']", _I32, (N,)), K, _arg(weights, "weights", _F32, (T, K)), N,
+            _arg(splits, "plan['splits']", _I32), E, recipe, which, _quant(out, "row_q", "out"),
+            _quant(out, "row_s", "out"), _quant(out, "col_q", "out"), _quant(out, "col_s", "out"),
+            _dev(status, "status", _I32))
+    _need_quant(out, recipe, N, C, max(E, 1), which, "out")
+    _check(lib().bsfp8_dispatch_quantize(*args, _stream(stream)), "dispatch_quantize")
+    return out
+
+
+def combine(y, plan, weights=None, add=None, out=None, stream=None):
+    """bsfp8_combine: out[t] = add[t] + sum_j weights[t, j] * y[plan["rows"][t, j]] of y [tokens * top_k, cols] (fp32 or
+    bf16), in y's type; weights fp32 [tokens, top_k] or None (1), add [tokens, cols] or None (may be out)."""
+    if _elsewhere(stream):
+        with _on(stream):
+            return combine(y, plan, weights, add, out)
+    pr, T, K, N = _plan_rows(plan)
+    py, (_, C) = _matrix(y, "y", _STREAM)
+    _like(y, (N, C), "y")
+    pw, pa = _arg(weights, "weights", _F32, (T, K)), _arg(add, "add", (y.dtype,), (T, C))
+    if out is None:
+        out = y.new_empty((T, C))
+    po = _arg(out, "out", (y.dtype,), (T, C))
+    _check(lib().bsfp8_combine(py, _dtype_code(y), N, C, pr, T, K, pw, pa, po, _stream(stream)), "combine")
+    return out
+
+
+def combine_grad(dout, plan, y=None, weights=None, dy=None, dweights=None, stream=None):
+    """bsfp8_combine_grad: from dout [tokens, cols], dy [tokens * top_k, cols] of its type (the given tensor or a new one;
+    False: not wanted, where dispatch_quantize makes it) and, with weights and the y [tokens * top_k, cols] that they
+    were applied to, dweights (fp32 [tokens, top_k]).  Returns a dict of those.  Rows of dy past the plan's last are left
+    as they are."""
+    if _elsewhere(stream):
+        with _on(stream):
+            return combine_grad(dout, plan, y, weights, dy, dweights)
+    pr, T, K, N = _plan_rows(plan)
+    pd, (_, C) = _matrix(dout, "dout", _STREAM)
+    _like(dout, (T, C), "dout")
+    py, pw = _arg(y, "y", (dout.dtype,), (N, C)), _arg(weights, "weights", _F32, (T, K))
+    out = {}
+    if dy is None:
+        dy = dout.new_empty((N, C))
+    if dy is not False:
+        out["dy"] = dy
+    if weights is not None and y is not None and dweights is None:
+        dweights = torch.empty_like(weights)
+    if dweights is not None:
+        if y is None:
+            raise ValueError("combine_grad: dweights need y")
+        out["dweights"] = dweights
+    rc = lib().bsfp8_combine_grad(pd, _dtype_code(dout), T, C, py, N, pr, K, pw,
+                                  _arg(out.get("dy"), "dy", (dout.dtype,), (N, C)),
+                                  _arg(dweights, "dweights", _F32, (T, K)), _stream(stream))
+    _check(rc, "combine_grad")
+    return out
+
+
+# ------------------------------------------------------------------------------------------
+# activations kept in 8 bits
+# ------------------------------------------------------------------------------------------
+
+def grouped_act_checkpoint(activation, h, split_sizes, recipe, which, out, kept, probs=None, status=None, stream=None):
+    """bsfp8_grouped_act_checkpoint: as grouped_act_quantize with ACT_SRELU (h [R, C] bf16) or ACT_SWIGLU (h [R, 2F]), and
+    in the same pass h itself in 8 bits into ``kept`` (alloc_quantized for h's shape, RECIPE_MX, ROWWISE), which is what
+    grouped_act_checkpoint_grad needs of it."""
+    ph, (R, wide) = _matrix(h, "h", _BF16)
+    if activation == ACT_SWIGLU and wide % 2:
+        raise ValueError("grouped_act_checkpoint: a GLU input has an even number of columns")
+    F = wide // 2 if activation == ACT_SWIGLU else wide
+    E = int(split_sizes.numel())
+    args = (activation, ph, _arg(probs, "probs", _F32, (R,)), R, F, _arg(split_sizes, "split_sizes", _I32), E, recipe,
+            which, _quant(out, "row_q", "out"), _quant(out, "row_s", "out"), _quant(out, "col_q", "out"),
+            _quant(out, "col_s", "out"), _quant(kept, "row_q", "kept"), _quant(kept, "row_s", "kept"),
+            _dev(status, "status", _I32))
+    _need_quant(out, recipe, R, F, max(E, 1), which, "out")
+    _need_quant(kept, RECIPE_MX, R, wide, 1, ROWWISE, "kept")
+    _check(lib().bsfp8_grouped_act_checkpoint(*args, _stream(stream)), "grouped_act_checkpoint")
+    return out
+
+
+def grouped_act_checkpoint_grad_workspace_bytes(capacity_rows, cols):
+    return int(lib().bsfp8_grouped_act_checkpoint_grad_workspace_bytes(capacity_rows, cols))
+
+
+def grouped_act_checkpoint_grad(activation, kept, dy, split_sizes, recipe, which, out, probs=None, y=None, dprobs=None,
+                                workspace=None, status=None, stream=None):
+    """bsfp8_grouped_act_checkpoint_grad: from ``kept`` and the bf16 gradient dy [R, F] at the activation's output, the
+    gradient at its input quantized into the layouts ``which`` (0: none) of ``out`` (alloc_quantized for [R, F] with
+    ACT_SRELU, [R, 2F] with ACT_SWIGLU).  y: a dict with col_q and col_s (alloc_quantized for [R, F], COLWISE) that
+    receives the activation again, for the second projection's weight gradient.  dprobs: fp32 [R], receives the
+    gradient of the probabilities.  Returns a dict of out's tensors, y and dprobs, where given."""
+    if dprobs is not None and workspace is None and _elsewhere(stream):
+        with _on(stream):
+            return grouped_act_checkpoint_grad(activation, kept, dy, split_sizes, recipe, which, out, probs, y, dprobs,
+                                               None, status)
+    pd, (R, F) = _matrix(dy, "dy", _BF16)
+    wide = 2 * F if activation == ACT_SWIGLU else F
+    E = int(split_sizes.numel())
+    out, q = dict(out or {}), y or {}
+    args = (activation, _quant(kept, "row_q", "kept"), _quant(kept, "row_s", "kept"), _arg(probs, "probs", _F32, (R,)), pd,
+            R, F, _arg(split_sizes, "split_sizes", _I32), E, recipe, which, _quant(out, "row_q", "out"),
+            _quant(out, "row_s", "out"), _quant(out, "col_q", "out"), _quant(out, "col_s", "out"),
+            _quant(q, "col_q", "y"), _quant(q, "col_s", "y"), _arg(dprobs, "dprobs", _F32, (R,)))
+    _need_quant(kept, RECIPE_MX, R, wide, 1, ROWWISE, "kept")
+    _need_quant(out, recipe, R, wide, max(E, 1), which, "out")
+    if y is not None:
+        _need_quant(q, recipe, R, F, max(E, 1), COLWISE, "y")
+    if dprobs is not None:
+        workspace = _workspace(workspace, grouped_act_checkpoint_grad_workspace_bytes(R, F), dy)
+    rc = lib().bsfp8_grouped_act_checkpoint_grad(*args, _ptr(workspace) if dprobs is not None else None,
+                                                 _dev(status, "status", _I32), _stream(stream))
+    _check(rc, "grouped_act_checkpoint_grad")
+    for name, value in (("y", y), ("dprobs", dprobs)):
+        if value is not None:
+            out[name] = value
+    return out

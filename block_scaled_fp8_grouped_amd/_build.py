@@ -12,12 +12,13 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB_PATH = os.path.join(HERE, "libbsfp8.so")
-SOURCES = ["bsfp8.cpp", "quantize.hip", "gemm.hip", "norm.hip", "adamw.hip", "glu_gemm.hip"]
+SOURCES = ["bsfp8.cpp", "quantize.hip", "gemm.hip", "norm.hip", "adamw.hip", "glu_gemm.hip", "route.hip", "dispatch.hip",
+           "token_quant.hip"]
 # the MFMA-only throughput probe, a library of its own (measurement, not the path)
 PEAK_LIB_PATH = os.path.join(HERE, "libbsfp8_peak.so")
 PEAK_SOURCES = ["mfma_peak.hip"]
 HEADERS = ["common.hpp", "group_layout.hpp", "tile_addr.hpp", "tile_sched.hpp", "norm_layout.hpp", "adamw_plan.hpp",
-           "glu_epilogue.hpp"]
+           "glu_epilogue.hpp", "row_io.hpp", "act_math.hpp", "token_layout.hpp"]
 
 # the native host side of the smallest calls (a Python extension on torch's C++ tensors, no GPU code)
 BINDING_PATH = os.path.join(HERE, "_native.so")

@@ -12,6 +12,7 @@
 #include "adamw_plan.hpp"
 #include "group_layout.hpp"
 #include "norm_layout.hpp"
+#include "token_layout.hpp"
 
 namespace bsfp8 {
 int launch_grouped_quantize(const void* in, int64_t R, int64_t C, const int32_t* splits, int E, int recipe,
@@ -51,6 +52,32 @@ int launch_adamw(const void* plan, int32_t num_tensors, int64_t chunks, int p_f3
                  double beta1, double beta2, double eps, double decay, int64_t step, const float* lr_dev,
                  const int32_t* step_dev, const float* grad_scale, const float* noop_flag, const uint64_t* seed,
                  hipStream_t stream);
+int launch_route_topk(const void* logits, bool f32, int64_t T, int E, int K, bool sigmoid, const float* bias,
+                      int renormalize, float scale, float* probs, int32_t* experts, float* score_sum, float* workspace,
+                      hipStream_t stream);
+int launch_route_topk_grad(const float* dprobs, const void* logits, bool f32, const int32_t* experts, int64_t T, int E,
+                           int K, bool sigmoid, int renormalize, float scale, const float* dsum, void* dlogits,
+                           hipStream_t stream);
+int launch_dispatch_plan(const int32_t* experts, const float* probs, int64_t N, int E, int32_t* splits, int32_t* rows,
+                         int32_t* choices, float* row_probs, void* workspace, hipStream_t stream);
+int launch_dispatch(const void* x, bool f32, int64_t T, int64_t C, const int32_t* rows, int K, const float* weights,
+                    void* out, int64_t cap, hipStream_t stream);
+int launch_combine(const void* y, bool f32, int64_t cap, int64_t C, const int32_t* rows, int64_t T, int K,
+                   const float* weights, const void* add, void* out, hipStream_t stream);
+int launch_combine_grad(const void* dout, bool f32, int64_t T, int64_t C, const void* y, int64_t cap,
+                        const int32_t* rows, int K, const float* weights, void* dy, float* dweights,
+                        hipStream_t stream);
+int launch_dispatch_quantize(const void* x, int64_t T, int64_t C, const int32_t* choices, int K, const float* weights,
+                             int64_t R, const int32_t* splits, int E, int recipe, uint8_t* row_q, uint8_t* row_s,
+                             uint8_t* col_q, uint8_t* col_s, uint32_t* status, hipStream_t stream);
+int launch_act_checkpoint(int act, const void* h, const float* probs, int64_t R, int64_t F, const int32_t* splits, int E,
+                          int recipe, uint8_t* row_q, uint8_t* row_s, uint8_t* col_q, uint8_t* col_s, uint8_t* kept_q,
+                          uint8_t* kept_s, uint32_t* status, hipStream_t stream);
+size_t act_checkpoint_grad_workspace_bytes(int64_t R, int64_t F);
+int launch_act_checkpoint_grad(int act, const uint8_t* kept_q, const uint8_t* kept_s, const float* probs, const void* dy,
+                               int64_t R, int64_t F, const int32_t* splits, int E, int recipe, uint8_t* row_q,
+                               uint8_t* row_s, uint8_t* col_q, uint8_t* col_s, uint8_t* ycol_q, uint8_t* ycol_s,
+                               float* dprobs, float* workspace, uint32_t* status, hipStream_t stream);
 }  // namespace bsfp8
 
 namespace {
@@ -134,6 +161,38 @@ int adamw_step(const void* device_plan, int32_t num_tensors, int64_t num_chunks,
   return bsfp8::launch_adamw(device_plan, num_tensors, num_chunks, param_dtype == BSFP8_F32, grad_dtype == BSFP8_F32,
                              state == BSFP8_STATE_8BIT, lr, beta1, beta2, eps, weight_decay, step, lr_dev, step_dev,
                              grad_scale, noop_flag, seed, (hipStream_t)stream);
+}
+
+// the router's sizes: every logit's offset fits in int64, every choice's in int32
+bool valid_route(int64_t tokens, int32_t num_experts, int32_t top_k) {
+  return tokens >= 0 && num_experts >= 1 && top_k >= 1 && top_k <= BSFP8_MAX_TOP_K &&
+         tokens <= (int64_t(1) << 30) / top_k;
+}
+int check_route(int64_t tokens, int32_t num_experts, int32_t top_k, int logits_dtype, int scoring, int renormalize,
+                float scale) {
+  if (!valid_groups(num_experts)) return BSFP8_ERR_NUM_GROUPS;
+  if (!valid_route(tokens, num_experts, top_k) || top_k > num_experts) return BSFP8_ERR_SHAPE;
+  if (!valid_dtype(logits_dtype) || (scoring != BSFP8_ROUTE_SOFTMAX && scoring != BSFP8_ROUTE_SIGMOID) ||
+      (renormalize != 0 && renormalize != 1) || !isfinite(scale))
+    return BSFP8_ERR_ARGUMENT;
+  return BSFP8_OK;
+}
+// rows moved between tokens and experts
+bool valid_rows_moved(int64_t tokens, int64_t cols, int32_t top_k, int64_t capacity_rows) {
+  return valid_route(tokens, 1, top_k) && cols >= 1 && cols <= (int64_t(1) << 24) && capacity_rows >= 0 &&
+         capacity_rows <= 0x7fffffff;
+}
+// the activations kept in 8 bits
+int check_checkpoint(int activation, int64_t capacity_rows, int64_t cols, const int32_t* split_sizes,
+                     int32_t num_groups, int recipe, int which) {
+  if (activation != BSFP8_ACT_SRELU && activation != BSFP8_ACT_SWIGLU) return BSFP8_ERR_ARGUMENT;
+  if (!valid_recipe(recipe)) return BSFP8_ERR_RECIPE;
+  if (!mx_recipe(recipe)) return BSFP8_ERR_LAYOUT;
+  if ((which & ~(BSFP8_ROWWISE | BSFP8_COLWISE)) != 0) return BSFP8_ERR_ARGUMENT;
+  if (capacity_rows < 0 || capacity_rows > (int64_t(1) << 31) || !valid_dim(cols) || cols > kMaxOutCols)
+    return BSFP8_ERR_SHAPE;
+  if (split_sizes == nullptr) return BSFP8_ERR_NULL_POINTER;
+  return valid_groups(num_groups) ? BSFP8_OK : BSFP8_ERR_NUM_GROUPS;
 }
 
 }  // namespace
@@ -474,6 +533,175 @@ int bsfp8_adamw_step_stochastic(const void* device_plan, int32_t num_tensors, in
                                 const float* grad_scale, const float* noop_flag, uint64_t seed, void* stream) {
   return adamw_step(device_plan, num_tensors, num_chunks, param_dtype, grad_dtype, state, lr, beta1, beta2, eps,
                     weight_decay, step, lr_dev, step_dev, grad_scale, noop_flag, &seed, stream);
+}
+
+size_t bsfp8_route_topk_workspace_bytes(int64_t tokens, int32_t num_experts) {
+  if (!valid_groups(num_experts) || !valid_route(tokens, num_experts, 1)) return 0;
+  return (size_t)bsfp8::route_blocks(tokens, num_experts) * (size_t)num_experts * sizeof(float);
+}
+
+int bsfp8_route_topk(const void* logits, int logits_dtype, int64_t tokens, int32_t num_experts, int32_t top_k,
+                     int scoring, const float* bias, int renormalize, float scale, float* probs, int32_t* experts,
+                     float* score_sum, void* workspace, void* stream) {
+  const int rc = check_route(tokens, num_experts, top_k, logits_dtype, scoring, renormalize, scale);
+  if (rc != BSFP8_OK) return rc;
+  if (tokens == 0 && score_sum == nullptr) return BSFP8_OK;
+  if (tokens > 0 && (logits == nullptr || probs == nullptr || experts == nullptr ||
+                     (score_sum != nullptr && workspace == nullptr)))
+    return BSFP8_ERR_NULL_POINTER;
+  if (!aligned16(logits) || !aligned4(bias) || !aligned4(probs) || !aligned4(experts) || !aligned4(score_sum) ||
+      !aligned16(workspace))
+    return BSFP8_ERR_ALIGNMENT;
+  return bsfp8::launch_route_topk(logits, logits_dtype == BSFP8_F32, tokens, num_experts, top_k,
+                                  scoring == BSFP8_ROUTE_SIGMOID, bias, renormalize, scale, probs, experts, score_sum,
+                                  (float*)workspace, (hipStream_t)stream);
+}
+
+int bsfp8_route_topk_grad(const float* dprobs, const void* logits, int logits_dtype, const int32_t* experts,
+                          int64_t tokens, int32_t num_experts, int32_t top_k, int scoring, int renormalize, float scale,
+                          const float* dscore_sum, void* dlogits, void* stream) {
+  const int rc = check_route(tokens, num_experts, top_k, logits_dtype, scoring, renormalize, scale);
+  if (rc != BSFP8_OK) return rc;
+  if (tokens == 0) return BSFP8_OK;
+  if (dprobs == nullptr || logits == nullptr || experts == nullptr || dlogits == nullptr) return BSFP8_ERR_NULL_POINTER;
+  if (!aligned4(dprobs) || !aligned16(logits) || !aligned4(experts) || !aligned4(dscore_sum) || !aligned16(dlogits))
+    return BSFP8_ERR_ALIGNMENT;
+  return bsfp8::launch_route_topk_grad(dprobs, logits, logits_dtype == BSFP8_F32, experts, tokens, num_experts, top_k,
+                                       scoring == BSFP8_ROUTE_SIGMOID, renormalize, scale, dscore_sum, dlogits,
+                                       (hipStream_t)stream);
+}
+
+size_t bsfp8_dispatch_plan_workspace_bytes(int64_t tokens, int32_t top_k, int32_t num_experts) {
+  if (!valid_groups(num_experts) || !valid_route(tokens, num_experts, top_k)) return 0;
+  const int64_t chunks = bsfp8::plan_chunks(tokens * top_k);
+  return chunks > 1 ? (size_t)chunks * (size_t)(num_experts + 1) * sizeof(int32_t) : 0;
+}
+
+int bsfp8_dispatch_plan(const int32_t* experts, const float* probs, int64_t tokens, int32_t top_k, int32_t num_experts,
+                        int32_t* split_sizes, int32_t* rows, int32_t* choices, float* row_probs, void* workspace,
+                        void* stream) {
+  if (!valid_groups(num_experts)) return BSFP8_ERR_NUM_GROUPS;
+  if (!valid_route(tokens, num_experts, top_k)) return BSFP8_ERR_SHAPE;
+  if (split_sizes == nullptr) return BSFP8_ERR_NULL_POINTER;
+  if (tokens > 0 && (experts == nullptr || rows == nullptr || choices == nullptr ||
+                     (probs == nullptr) != (row_probs == nullptr) ||
+                     (workspace == nullptr && bsfp8_dispatch_plan_workspace_bytes(tokens, top_k, num_experts) > 0)))
+    return BSFP8_ERR_NULL_POINTER;
+  if (!aligned4(experts) || !aligned4(probs) || !aligned4(split_sizes) || !aligned4(rows) || !aligned4(choices) ||
+      !aligned4(row_probs) || !aligned16(workspace))
+    return BSFP8_ERR_ALIGNMENT;
+  return bsfp8::launch_dispatch_plan(experts, probs, tokens * top_k, num_experts, split_sizes, rows, choices, row_probs,
+                                     workspace, (hipStream_t)stream);
+}
+
+int bsfp8_dispatch(const void* x, int dtype, int64_t tokens, int64_t cols, const int32_t* rows, int32_t top_k,
+                   const float* weights, void* out, int64_t capacity_rows, void* stream) {
+  if (!valid_rows_moved(tokens, cols, top_k, capacity_rows)) return BSFP8_ERR_SHAPE;
+  if (!valid_dtype(dtype)) return BSFP8_ERR_ARGUMENT;
+  if (tokens == 0 || capacity_rows == 0) return BSFP8_OK;
+  if (x == nullptr || rows == nullptr || out == nullptr) return BSFP8_ERR_NULL_POINTER;
+  if (!aligned16(x) || !aligned4(rows) || !aligned4(weights) || !aligned16(out)) return BSFP8_ERR_ALIGNMENT;
+  return bsfp8::launch_dispatch(x, dtype == BSFP8_F32, tokens, cols, rows, top_k, weights, out, capacity_rows,
+                                (hipStream_t)stream);
+}
+
+int bsfp8_dispatch_quantize(const void* x_bf16, int64_t tokens, int64_t cols, const int32_t* choices, int32_t top_k,
+                            const float* weights, int64_t capacity_rows, const int32_t* split_sizes,
+                            int32_t num_groups, int recipe, int which, uint8_t* row_q, uint8_t* row_s, uint8_t* col_q,
+                            uint8_t* col_s, uint32_t* status, void* stream) {
+  if (!valid_recipe(recipe)) return BSFP8_ERR_RECIPE;
+  if (!mx_recipe(recipe)) return BSFP8_ERR_LAYOUT;
+  if (which <= 0 || (which & ~(BSFP8_ROWWISE | BSFP8_COLWISE)) != 0) return BSFP8_ERR_ARGUMENT;
+  if (!valid_rows_moved(tokens, cols, top_k, capacity_rows) || !valid_dim(cols)) return BSFP8_ERR_SHAPE;
+  if (!valid_groups(num_groups)) return BSFP8_ERR_NUM_GROUPS;
+  if (capacity_rows == 0) return BSFP8_OK;
+  if ((x_bf16 == nullptr && tokens > 0) || choices == nullptr || split_sizes == nullptr) return BSFP8_ERR_NULL_POINTER;
+  if (!aligned16(x_bf16) || !aligned4(choices) || !aligned4(weights) || !aligned4(split_sizes) || !aligned4(status))
+    return BSFP8_ERR_ALIGNMENT;
+  const int rc = check_glu_quantized(which, row_q, row_s, col_q, col_s);
+  if (rc != BSFP8_OK) return rc;
+  const bool row = (which & BSFP8_ROWWISE) != 0, col = (which & BSFP8_COLWISE) != 0;
+  return bsfp8::launch_dispatch_quantize(x_bf16, tokens, cols, choices, top_k, weights, capacity_rows, split_sizes,
+                                         num_groups, recipe, row ? row_q : nullptr, row ? row_s : nullptr,
+                                         col ? col_q : nullptr, col ? col_s : nullptr, status, (hipStream_t)stream);
+}
+
+int bsfp8_combine(const void* y, int dtype, int64_t capacity_rows, int64_t cols, const int32_t* rows, int64_t tokens,
+                  int32_t top_k, const float* weights, const void* add, void* out, void* stream) {
+  if (!valid_rows_moved(tokens, cols, top_k, capacity_rows)) return BSFP8_ERR_SHAPE;
+  if (!valid_dtype(dtype)) return BSFP8_ERR_ARGUMENT;
+  if (tokens == 0) return BSFP8_OK;
+  if ((y == nullptr && capacity_rows > 0) || rows == nullptr || out == nullptr) return BSFP8_ERR_NULL_POINTER;
+  if (!aligned16(y) || !aligned4(rows) || !aligned4(weights) || !aligned16(add) || !aligned16(out))
+    return BSFP8_ERR_ALIGNMENT;
+  return bsfp8::launch_combine(y, dtype == BSFP8_F32, capacity_rows, cols, rows, tokens, top_k, weights, add, out,
+                               (hipStream_t)stream);
+}
+
+int bsfp8_combine_grad(const void* dout, int dtype, int64_t tokens, int64_t cols, const void* y, int64_t capacity_rows,
+                       const int32_t* rows, int32_t top_k, const float* weights, void* dy, float* dweights,
+                       void* stream) {
+  if (!valid_rows_moved(tokens, cols, top_k, capacity_rows)) return BSFP8_ERR_SHAPE;
+  if (!valid_dtype(dtype)) return BSFP8_ERR_ARGUMENT;
+  if (tokens == 0) return BSFP8_OK;
+  if (dy == nullptr && dweights == nullptr) return BSFP8_ERR_ARGUMENT;
+  if (dout == nullptr || rows == nullptr || (dweights != nullptr && y == nullptr && capacity_rows > 0))
+    return BSFP8_ERR_NULL_POINTER;
+  if (!aligned16(dout) || !aligned16(y) || !aligned4(rows) || !aligned4(weights) || !aligned16(dy) ||
+      !aligned4(dweights))
+    return BSFP8_ERR_ALIGNMENT;
+  return bsfp8::launch_combine_grad(dout, dtype == BSFP8_F32, tokens, cols, y, capacity_rows, rows, top_k, weights, dy,
+                                    dweights, (hipStream_t)stream);
+}
+
+int bsfp8_grouped_act_checkpoint(int activation, const void* h_bf16, const float* probs, int64_t capacity_rows,
+                                 int64_t cols, const int32_t* split_sizes, int32_t num_groups, int recipe, int which,
+                                 uint8_t* row_q, uint8_t* row_s, uint8_t* col_q, uint8_t* col_s, uint8_t* kept_q,
+                                 uint8_t* kept_s, uint32_t* status, void* stream) {
+  int rc = check_checkpoint(activation, capacity_rows, cols, split_sizes, num_groups, recipe, which);
+  if (rc != BSFP8_OK) return rc;
+  if (which == 0) return BSFP8_ERR_ARGUMENT;
+  if (capacity_rows == 0) return BSFP8_OK;
+  if (h_bf16 == nullptr || kept_q == nullptr || kept_s == nullptr) return BSFP8_ERR_NULL_POINTER;
+  if (!aligned16(h_bf16) || !aligned4(probs) || !aligned4(split_sizes) || !aligned16(kept_q) || !aligned16(kept_s) ||
+      !aligned4(status))
+    return BSFP8_ERR_ALIGNMENT;
+  rc = check_glu_quantized(which, row_q, row_s, col_q, col_s);
+  if (rc != BSFP8_OK) return rc;
+  const bool row = (which & BSFP8_ROWWISE) != 0, col = (which & BSFP8_COLWISE) != 0;
+  return bsfp8::launch_act_checkpoint(activation, h_bf16, probs, capacity_rows, cols, split_sizes, num_groups, recipe,
+                                      row ? row_q : nullptr, row ? row_s : nullptr, col ? col_q : nullptr,
+                                      col ? col_s : nullptr, kept_q, kept_s, status, (hipStream_t)stream);
+}
+
+size_t bsfp8_grouped_act_checkpoint_grad_workspace_bytes(int64_t capacity_rows, int64_t cols) {
+  if (capacity_rows < 0 || capacity_rows > (int64_t(1) << 31) || !valid_dim(cols) || cols > kMaxOutCols) return 0;
+  return bsfp8::act_checkpoint_grad_workspace_bytes(capacity_rows, cols);
+}
+
+int bsfp8_grouped_act_checkpoint_grad(int activation, const uint8_t* kept_q, const uint8_t* kept_s, const float* probs,
+                                      const void* dy_bf16, int64_t capacity_rows, int64_t cols,
+                                      const int32_t* split_sizes, int32_t num_groups, int recipe, int which,
+                                      uint8_t* row_q, uint8_t* row_s, uint8_t* col_q, uint8_t* col_s, uint8_t* y_col_q,
+                                      uint8_t* y_col_s, float* dprobs, void* workspace, uint32_t* status,
+                                      void* stream) {
+  int rc = check_checkpoint(activation, capacity_rows, cols, split_sizes, num_groups, recipe, which);
+  if (rc != BSFP8_OK) return rc;
+  if (capacity_rows == 0) return BSFP8_OK;
+  if (which == 0 && y_col_q == nullptr && dprobs == nullptr) return BSFP8_ERR_ARGUMENT;
+  if (kept_q == nullptr || kept_s == nullptr || dy_bf16 == nullptr || (y_col_q == nullptr) != (y_col_s == nullptr) ||
+      (dprobs != nullptr && workspace == nullptr))
+    return BSFP8_ERR_NULL_POINTER;
+  if (!aligned16(kept_q) || !aligned16(kept_s) || !aligned4(probs) || !aligned16(dy_bf16) || !aligned4(split_sizes) ||
+      !aligned16(y_col_q) || !aligned16(y_col_s) || !aligned4(dprobs) || !aligned16(workspace) || !aligned4(status))
+    return BSFP8_ERR_ALIGNMENT;
+  rc = check_glu_quantized(which, row_q, row_s, col_q, col_s);
+  if (rc != BSFP8_OK) return rc;
+  const bool row = (which & BSFP8_ROWWISE) != 0, col = (which & BSFP8_COLWISE) != 0;
+  return bsfp8::launch_act_checkpoint_grad(activation, kept_q, kept_s, probs, dy_bf16, capacity_rows, cols, split_sizes,
+                                           num_groups, recipe, row ? row_q : nullptr, row ? row_s : nullptr,
+                                           col ? col_q : nullptr, col ? col_s : nullptr, y_col_q, y_col_s, dprobs,
+                                           (float*)workspace, status, (hipStream_t)stream);
 }
 
 const char* bsfp8_strerror(int code) {

@@ -1,0 +1,364 @@
+// Tokens to their experts and back (gfx950): the sort of the choices by expert, the rows gathered, their weighted sum
+// and its gradient.  include/bsfp8.h states the formulas.
+//
+// The sort is a counting sort by expert, stable by construction: a workgroup takes a chunk of consecutive choices, each
+// of its 16 waves a consecutive part of it, and a choice's row is the sum of the choices of lower experts, those of its
+// expert in earlier chunks, in earlier waves and in earlier lanes.  A first launch counts each chunk's choices per
+// expert; the second adds up the chunks before its own by itself (no third launch, no wait between workgroups) and
+// places.  Up to one chunk of choices takes one launch.
+//
+// The row movers walk tokens: a token's row is read once and written (dispatch), or a token's top_k rows are read and
+// summed (combine), each byte moved once in rows of cols elements, 8 elements a thread.  All are bound by HBM.
+#include <type_traits>
+
+#include "common.hpp"
+#include "row_io.hpp"
+#include "token_layout.hpp"
+
+namespace bsfp8 {
+
+// ---------------------------------------------------------------------------------------------
+// plan
+// ---------------------------------------------------------------------------------------------
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWaves = kPlanThreads / 64;
+
+struct PlanArgs {
+  const int32_t* experts;
+  const float* probs;
+  int64_t N;       // choices
+  int E;
+  int64_t chunk;   // choices per workgroup, a multiple of kPlanUnit
+  int chunks;
+  int32_t *hist;   // [chunks][E + 1]: choices of each chunk per expert, dropped ones last
+  int32_t *splits, *rows, *choices;
+  float* row_probs;
+};
+
+__device__ __forceinline__ int plan_bin(int32_t e, int E) { return e < 0 || e >= E ? E : e; }
+
+__global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(PlanArgs a) {
+  __shared__ int32_t count[kMaxGroups + 1];
+  for (int b = threadIdx.x; b <= a.E; b += kPlanThreads) count[b] = 0;
+  __syncthreads();
+  const int64_t begin = a.chunk * blockIdx.x, end = begin + a.chunk < a.N ? begin + a.chunk : a.N;
+  for (int64_t c = begin + threadIdx.x; c < end; c += kPlanThreads) atomicAdd(&count[plan_bin(a.experts[c], a.E)], 1);
+  __syncthreads();
+  for (int b = threadIdx.x; b <= a.E; b += kPlanThreads) a.hist[(int64_t)blockIdx.x * (a.E + 1) + b] = count[b];
+}
+
+// Exclusive prefix over the workgroup of one value a thread.
+__device__ __forceinline__ int32_t plan_scan(int32_t v, int32_t* wave_total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int32_t s = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int32_t u = __shfl_up(s, d, 64);
+    if (lane >= d) s += u;
+  }
+  if (lane == 63) wave_total[wave] = s;
+  __syncthreads();
+  int32_t before = 0;
+  for (int w = 0; w < wave; ++w) before += wave_total[w];
+  __syncthreads();
+  return before + s - v;
+}
+
+__global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanArgs a) {
+  // at[w * bins + b]: first the choices of wave w in bin b, then where its next one goes
+  __shared__ int32_t at[kPlanWaves * (kMaxGroups + 1)];
+  __shared__ int32_t total[kMaxGroups + 1], before[kMaxGroups + 1], wave_total[kPlanWaves];
+  const int bins = a.E + 1, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int i = threadIdx.x; i < kPlanWaves * bins; i += kPlanThreads) at[i] = 0;
+  for (int b = threadIdx.x; b < bins; b += kPlanThreads) total[b] = before[b] = 0;
+  __syncthreads();
+  const int64_t begin = a.chunk * blockIdx.x + a.chunk / kPlanWaves * wave;
+  const int64_t stop = begin + a.chunk / kPlanWaves, end = stop < a.N ? stop : a.N;
+  for (int64_t c = begin + lane; c < end; c += 64) atomicAdd(&at[wave * bins + plan_bin(a.experts[c], a.E)], 1);
+  if (a.hist != nullptr) {
+    for (int b = lane; b < bins; b += 64) {
+      int32_t all = 0, mine = 0;
+      for (int c = wave; c < a.chunks; c += kPlanWaves) {
+        const int32_t n = a.hist[(int64_t)c * bins + b];
+        all += n;
+        mine += c < (int)blockIdx.x ? n : 0;
+      }
+      atomicAdd(&total[b], all);  // (whole numbers: the order does not matter)
+      atomicAdd(&before[b], mine);
+    }
+  }
+  __syncthreads();
+  if (a.hist == nullptr)
+    for (int b = threadIdx.x; b < bins; b += kPlanThreads)
+      for (int w = 0; w < kPlanWaves; ++w) total[b] += at[w * bins + b];
+  if (a.hist == nullptr) __syncthreads();
+  // at most two bins a thread: consecutive ones, so that one prefix over the threads serves them
+  const int b0 = 2 * threadIdx.x;
+  const int32_t n0 = b0 < bins ? total[b0] : 0, n1 = b0 + 1 < bins ? total[b0 + 1] : 0;
+  const int32_t first = plan_scan(n0 + n1, wave_total);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int b = b0 + i;
+    if (b < bins) {
+      if (blockIdx.x == 0 && b < a.E) a.splits[b] = i ? n1 : n0;
+      int32_t next = first + (i ? n0 : 0) + before[b];
+      for (int w = 0; w < kPlanWaves; ++w) {
+        const int32_t n = at[w * bins + b];
+        at[w * bins + b] = next;
+        next += n;
+      }
+    }
+  }
+  __syncthreads();
+  int32_t* next = at + wave * bins;
+  const uint64_t below = (uint64_t(1) << lane) - 1;
+  for (int64_t c0 = begin; c0 < end; c0 += 64) {
+    const int64_t c = c0 + lane;
+    const bool live = c < end;
+    const int b = live ? plan_bin(a.experts[c], a.E) : bins;  // (a bin of their own for the lanes past the end)
+    // the lanes of the same bin
+    uint64_t same = ~uint64_t(0);
+    for (int bit = 0; (bins >> bit) != 0; ++bit) {
+      const bool set = (b >> bit) & 1;
+      const uint64_t m = __ballot(set);
+      same &= set ? m : ~m;
+    }
+    const int rank = __popcll(same & below);
+    if (live) {
+      const int32_t row = next[b] + rank;
+      __builtin_amdgcn_wave_barrier();
+      if (rank == 0) next[b] = row + __popcll(same);  // (a wave's LDS accesses are done in order)
+      const bool dropped = b == a.E;
+      a.rows[c] = dropped ? -1 : row;
+      a.choices[row] = dropped ? -1 : (int32_t)c;
+      if (a.row_probs != nullptr) a.row_probs[row] = dropped ? 0.0f : a.probs[c];
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+__global__ __launch_bounds__(kPlanThreads) void plan_empty_kernel(int32_t* splits, int E) {
+  if ((int)threadIdx.x < E) splits[threadIdx.x] = 0;
+}
+
+int launch_dispatch_plan(const int32_t* experts, const float* probs, int64_t N, int E, int32_t* splits, int32_t* rows,
+                         int32_t* choices, float* row_probs, void* workspace, hipStream_t stream) {
+  const int64_t chunks = plan_chunks(N);
+  if (chunks == 0) {
+    hipLaunchKernelGGL(plan_empty_kernel, dim3(1), dim3(kPlanThreads), 0, stream, splits, E);
+    return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
+  }
+  const PlanArgs a{experts, probs, N, E, plan_chunk(N), (int)chunks, chunks > 1 ? (int32_t*)workspace : nullptr,
+                   splits, rows, choices, row_probs};
+  if (chunks > 1) hipLaunchKernelGGL(plan_count_kernel, dim3((unsigned)chunks), dim3(kPlanThreads), 0, stream, a);
+  hipLaunchKernelGGL(plan_place_kernel, dim3((unsigned)chunks), dim3(kPlanThreads), 0, stream, a);
+  return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
+}
+
+// ---------------------------------------------------------------------------------------------
+// rows out and back
+// ---------------------------------------------------------------------------------------------
+
+struct MoveArgs {
+  int64_t T, C, cap;
+  int K;
+  const int32_t* rows;
+  const float* weights;
+  const void *in, *add;
+  void* out;
+  const void* y;
+  float* dweights;
+};
+
+// Threads over (token, chunk of 8 columns): a workgroup takes 256 chunks of one token, or several whole tokens where
+// their rows are shorter; `shift`: log2 of the threads that a token takes in a workgroup.
+struct MoveShape {
+  int shift;
+  int64_t segments, blocks;
+};
+static MoveShape move_shape(int64_t T, int64_t C) {
+  const int64_t chunks = (C + 7) / 8;
+  int shift = 0;
+  while (shift < 8 && (int64_t(1) << shift) < chunks) ++shift;
+  const int64_t seg = (chunks + (int64_t(1) << shift) - 1) >> shift, per = 256 >> shift;
+  return {shift, seg, (T + per - 1) / per * seg};
+}
+__device__ __forceinline__ bool move_place(const MoveArgs& a, int shift, int64_t segments, int64_t& t, int64_t& c) {
+  const int64_t seg = (int64_t)blockIdx.x % segments, set = (int64_t)blockIdx.x / segments;
+  t = set * (256 >> shift) + (threadIdx.x >> shift);
+  c = 8 * (seg * 256 + (threadIdx.x & ((1 << shift) - 1)));
+  return t < a.T && c < a.C;
+}
+
+// 8 elements as they were loaded, bit for bit.
+__device__ __forceinline__ void copy8(float* p, int n, const Raw8<float>& v) {
+  if (n >= 8) {
+    __builtin_memcpy(p, v.t, sizeof(v.t));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = v.t[i];
+  }
+}
+__device__ __forceinline__ void copy8(uint16_t* p, int n, const Raw8<uint16_t>& v) {
+  if (n >= 8) {
+    __builtin_memcpy(p, v.w, sizeof(v.w));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = (uint16_t)(v.w[i >> 1] >> (16 * (i & 1)));
+  }
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void dispatch_kernel(MoveArgs a, int shift, int64_t segments) {
+  int64_t t, c;
+  if (!move_place(a, shift, segments, t, c)) return;
+  const int n = a.C - c < 8 ? (int)(a.C - c) : 8;
+  Raw8<T> v;
+  v.load((const T*)a.in + t * a.C + c, n);
+  for (int j = 0; j < a.K; ++j) {
+    const int64_t r = a.rows[t * a.K + j];
+    if (r < 0 || r >= a.cap) continue;
+    T* out = (T*)a.out + r * a.C + c;
+    if (a.weights == nullptr) {
+      copy8(out, n, v);
+      continue;
+    }
+    float o[8];
+    const float w = a.weights[t * a.K + j];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = v[i] * w;
+    store8(out, n, o);
+  }
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void combine_kernel(MoveArgs a, int shift, int64_t segments) {
+  int64_t t, c;
+  if (!move_place(a, shift, segments, t, c)) return;
+  const int n = a.C - c < 8 ? (int)(a.C - c) : 8;
+  float sum[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
+  for (int j = 0; j < a.K; ++j) {
+    const int64_t r = a.rows[t * a.K + j];
+    if (r < 0 || r >= a.cap) continue;
+    const float w = a.weights != nullptr ? a.weights[t * a.K + j] : 1.0f;
+    float v[8];
+    load8((const T*)a.in + r * a.C + c, n, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] = __builtin_fmaf(w, v[i], sum[i]);
+  }
+  if (a.add != nullptr) {
+    float v[8];
+    load8((const T*)a.add + t * a.C + c, n, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] += v[i];
+  }
+  store8((T*)a.out + t * a.C + c, n, sum);
+}
+
+// A token per wave (W == 1) or per workgroup of W waves; its K dot products in sets of 8.
+template <class T, int W>
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void combine_grad_kernel(MoveArgs a) {
+  __shared__ float sums[W][8];
+  const int lane = threadIdx.x & 63, wave = W == 1 ? 0 : threadIdx.x >> 6;
+  const int64_t t = W == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (t >= a.T) return;
+  const T* dout = (const T*)a.in + t * a.C;
+  for (int j0 = 0; j0 < a.K; j0 += 8) {
+    const int nj = a.K - j0 < 8 ? a.K - j0 : 8;
+    float dot[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dot[j] = 0.0f;
+    for (int64_t c = 8 * (wave * 64 + lane); c < a.C; c += 512 * W) {
+      const int n = a.C - c < 8 ? (int)(a.C - c) : 8;
+      float d[8];
+      load8(dout + c, n, d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j >= nj) break;
+        const int64_t r = a.rows[t * a.K + j0 + j];
+        if (r < 0 || r >= a.cap) continue;
+        if (a.dweights != nullptr) {
+          float y[8];
+          load8((const T*)a.y + r * a.C + c, n, y);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot[j] = __builtin_fmaf(d[i], y[i], dot[j]);
+        }
+        if (a.out != nullptr) {
+          const float w = a.weights != nullptr ? a.weights[t * a.K + j0 + j] : 1.0f;
+          float o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = d[i] * w;
+          store8((T*)a.out + r * a.C + c, n, o);
+        }
+      }
+    }
+    if (a.dweights == nullptr) continue;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dot[j] = wave_sum(dot[j]);
+    if constexpr (W == 1) {
+      if (lane == 63)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < nj) a.dweights[t * a.K + j0 + j] = dot[j];
+    } else {
+      if (lane == 63)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sums[wave][j] = dot[j];
+      __syncthreads();
+      if ((int)threadIdx.x < nj) {
+        float s = 0.0f;
+        for (int w = 0; w < W; ++w) s += sums[w][threadIdx.x];
+        a.dweights[t * a.K + j0 + threadIdx.x] = s;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+int launch_dispatch(const void* x, bool f32, int64_t T, int64_t C, const int32_t* rows, int K, const float* weights,
+                    void* out, int64_t cap, hipStream_t stream) {
+  const MoveShape s = move_shape(T, C);
+  if (s.blocks > 0x7fffffff) return BSFP8_ERR_SHAPE;
+  const MoveArgs a{T, C, cap, K, rows, weights, x, nullptr, out, nullptr, nullptr};
+  const dim3 grid((unsigned)s.blocks), block(256);
+  if (f32) hipLaunchKernelGGL(dispatch_kernel<float>, grid, block, 0, stream, a, s.shift, s.segments);
+  else hipLaunchKernelGGL(dispatch_kernel<uint16_t>, grid, block, 0, stream, a, s.shift, s.segments);
+  return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
+}
+
+int launch_combine(const void* y, bool f32, int64_t cap, int64_t C, const int32_t* rows, int64_t T, int K,
+                   const float* weights, const void* add, void* out, hipStream_t stream) {
+  const MoveShape s = move_shape(T, C);
+  if (s.blocks > 0x7fffffff) return BSFP8_ERR_SHAPE;
+  const MoveArgs a{T, C, cap, K, rows, weights, y, add, out, nullptr, nullptr};
+  const dim3 grid((unsigned)s.blocks), block(256);
+  if (f32) hipLaunchKernelGGL(combine_kernel<float>, grid, block, 0, stream, a, s.shift, s.segments);
+  else hipLaunchKernelGGL(combine_kernel<uint16_t>, grid, block, 0, stream, a, s.shift, s.segments);
+  return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
+}
+
+int launch_combine_grad(const void* dout, bool f32, int64_t T, int64_t C, const void* y, int64_t cap,
+                        const int32_t* rows, int K, const float* weights, void* dy, float* dweights,
+                        hipStream_t stream) {
+  const MoveArgs a{T, C, cap, K, rows, weights, dout, nullptr, dy, y, dweights};
+  // a token per wave where they fill the chip by themselves
+  const bool wave = T >= 4096 || C <= 512;
+  const int64_t blocks = wave ? (T + 3) / 4 : T;
+  if (blocks > 0x7fffffff) return BSFP8_ERR_SHAPE;
+  const dim3 grid((unsigned)blocks);
+  if (wave) {
+    if (f32) hipLaunchKernelGGL((combine_grad_kernel<float, 1>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((combine_grad_kernel<uint16_t, 1>), grid, dim3(256), 0, stream, a);
+  } else {
+    if (f32) hipLaunchKernelGGL((combine_grad_kernel<float, 8>), grid, dim3(512), 0, stream, a);
+    else hipLaunchKernelGGL((combine_grad_kernel<uint16_t, 8>), grid, dim3(512), 0, stream, a);
+  }
+  return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
+}
+
+}  // namespace bsfp8

@@ -1,0 +1,414 @@
+// The router: each token's top_k experts with their probabilities, the sums of the scores, and the gradient of both
+// (gfx950).  include/bsfp8.h states the formulas.
+//
+// A token's logits lie in the registers of 16 lanes (up to 256 experts) or of a wave (up to 1024), V = 1 to 16
+// consecutive experts a lane, so that a lane's logits are one wide load and its reductions over a token are moves within
+// a row of 16 lanes.  Keys are compared as unsigned numbers whose order is that of the keys (NaN highest, 0 for masked
+// and taken ones).  A choice takes one reduction for the largest key and one for the lowest expert that has it.
+#include <math.h>
+
+#include <type_traits>
+
+#include "act_math.hpp"
+#include "common.hpp"
+#include "row_io.hpp"
+#include "token_layout.hpp"
+
+namespace bsfp8 {
+
+struct RouteArgs {
+  const void* logits;
+  int64_t T;
+  int E, K;
+  const float* bias;
+  int sigmoid, renormalize;
+  float scale;
+  float* probs;        // forward out; gradient: dprobs in
+  int32_t* experts;
+  float* partial;      // forward: [blocks][E] sums of the scores, or NULL
+  const float* dsum;   // gradient: dscore_sum, or NULL
+  void* dlogits;
+};
+
+// Reductions over the G lanes of a token; every lane gets the result.
+template <int G, class Op>
+__device__ __forceinline__ uint32_t over_token(uint32_t v, Op op) {
+  v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xf, 0xf, false));  // the row of 16, turned by 8
+  v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xf, 0xf, false));
+  v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xf, 0xf, false));
+  v = op(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xf, 0xf, false));
+  if constexpr (G == 64) {
+    v = op(v, (uint32_t)__shfl_xor((int)v, 16, 64));
+    v = op(v, (uint32_t)__shfl_xor((int)v, 32, 64));
+  }
+  return v;
+}
+template <int G>
+__device__ __forceinline__ uint32_t max_over(uint32_t v) {
+  return over_token<G>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+template <int G>
+__device__ __forceinline__ uint32_t min_over(uint32_t v) {
+  return over_token<G>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+}
+template <int G>
+__device__ __forceinline__ float sum_over(float v) {
+  return __uint_as_float(over_token<G>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+template <int G>
+__device__ __forceinline__ float fmax_over(float v) {
+  return __uint_as_float(over_token<G>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
+}
+
+// A key as an unsigned number of the same order: 0 below every number, +0 where it was -0, NaN above all.
+__device__ __forceinline__ uint32_t ordered(float key) {
+  const uint32_t b = __float_as_uint(key + 0.0f);
+  return key != key ? 0xffffffffu : b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+
+// 1 / (1 + 2^(-l log2 e)) by the stated steps, and 1 - it without the cancellation.
+__device__ __forceinline__ float sigmoid_stated(float l, float* other = nullptr) {
+  const float t = exp2_stated(-l * 1.44269502f);
+  const float s = recip_rn(1.0f + t);
+  if (other != nullptr) *other = t * s;
+  return s;
+}
+
+// V values of a row from e0 on; past its end: -infinity.
+template <int V, class T>
+__device__ __forceinline__ void load_logits(const T* row, int e0, int E, float (&l)[V]) {
+  if (e0 + V <= E) {
+    T t[V];
+    __builtin_memcpy(t, row + e0, sizeof(t));
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = to_f32(t[v]);
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = e0 + v < E ? to_f32(row[e0 + v]) : -INFINITY;
+  }
+}
+
+// The scores of a token's V logits a lane: s, and for the sigmoid 1 - s (FULL gradients).
+template <int G, int V>
+__device__ __forceinline__ void scores_of(const float (&l)[V], int sigmoid, float (&s)[V], float* other = nullptr) {
+  if (sigmoid) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float o;
+      s[v] = sigmoid_stated(l[v], &o);
+      if (l[v] == -INFINITY) s[v] = 0.0f;
+      if (other != nullptr) other[v] = o;
+    }
+    return;
+  }
+  float m = l[0];
+#pragma unroll
+  for (int v = 1; v < V; ++v) m = fmaxf(m, l[v]);
+  m = fmax_over<G>(m);
+  if (m == -INFINITY) m = 0.0f;  // every expert masked: the scores are 0
+  float sum = 0.0f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    s[v] = expf(l[v] - m);
+    sum += s[v];
+  }
+  sum = sum_over<G>(sum);
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int v = 0; v < V; ++v) s[v] *= inv;
+}
+
+// A lane's choices j = lane, lane + G, ... of a token: up to kMaxPerLane.
+template <int G>
+constexpr int kPerLane = (BSFP8_MAX_TOP_K + G - 1) / G;
+
+// The scores of the chosen over what they are divided by: ph, and for the sigmoid 1 - s.
+template <int G, class T>
+__device__ __forceinline__ void chosen_scores(const T* row, const int (&e)[kPerLane<G>], int sigmoid,
+                                              float (&ph)[kPerLane<G>], float (&other)[kPerLane<G>]) {
+  constexpr int P = kPerLane<G>;
+  float l[P], m = -INFINITY, sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    l[i] = e[i] >= 0 ? to_f32(row[e[i]]) : -INFINITY;
+    m = fmaxf(m, l[i]);
+  }
+  if (!sigmoid) {
+    m = fmax_over<G>(m);
+    if (m == -INFINITY) m = 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    ph[i] = sigmoid ? sigmoid_stated(l[i], &other[i]) : expf(l[i] - m);
+    if (e[i] < 0 || l[i] == -INFINITY) ph[i] = 0.0f;
+    sum += ph[i];
+  }
+  sum = sum_over<G>(sum);
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int i = 0; i < P; ++i) ph[i] *= inv;
+}
+
+template <class T, int G, int V>
+__global__ __launch_bounds__(256) void route_topk_kernel(RouteArgs a) {
+  constexpr int P = kPerLane<G>;
+  __shared__ float sums[256 / G][G * V + 1];
+  const int lane = threadIdx.x & (G - 1), group = threadIdx.x / G, e0 = lane * V;
+  float total[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) total[v] = 0.0f;
+  // every lane of a wave walks as many tokens, so that the moves between lanes find them all
+  for (int64_t t0 = (int64_t)blockIdx.x * (256 / G); t0 < a.T; t0 += (int64_t)gridDim.x * (256 / G)) {
+    const bool live = t0 + group < a.T;
+    const int64_t t = live ? t0 + group : a.T - 1;
+    const T* row = (const T*)a.logits + t * a.E;
+    float l[V], s[V];
+    load_logits<V>(row, e0, a.E, l);
+    if (a.sigmoid || a.partial != nullptr || !a.renormalize) scores_of<G, V>(l, a.sigmoid, s);
+    if (a.partial != nullptr && live) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) total[v] += e0 + v < a.E ? s[v] : 0.0f;
+    }
+    uint32_t u[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float key = a.sigmoid ? s[v] : l[v];
+      if (a.bias != nullptr && e0 + v < a.E) key += a.bias[e0 + v];
+      u[v] = l[v] == -INFINITY || key == -INFINITY ? 0u : ordered(key);
+    }
+    int mine[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) mine[i] = -1;
+    for (int j = 0; j < a.K; ++j) {
+      uint32_t best = u[0];
+#pragma unroll
+      for (int v = 1; v < V; ++v) best = u[v] > best ? u[v] : best;
+      best = max_over<G>(best);
+      uint32_t at = 0xffffffffu;
+#pragma unroll
+      for (int v = V - 1; v >= 0; --v) at = u[v] == best ? (uint32_t)(e0 + v) : at;
+      at = min_over<G>(at);
+#pragma unroll
+      for (int v = 0; v < V; ++v) u[v] = at == (uint32_t)(e0 + v) ? 0u : u[v];
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (j == lane + i * G) mine[i] = best == 0u ? -1 : (int)at;
+    }
+    float p[P], other[P];
+    if (a.renormalize) {
+      chosen_scores<G>(row, mine, a.sigmoid, p, other);
+    } else {
+      // (the chosen logits are read again: a lane holds other experts' than those it writes)
+      float m = l[0], sum = 0.0f;
+      if (!a.sigmoid) {
+#pragma unroll
+        for (int v = 1; v < V; ++v) m = fmaxf(m, l[v]);
+        m = fmax_over<G>(m);
+        if (m == -INFINITY) m = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) sum += expf(l[v] - m);
+        sum = sum_over<G>(sum);
+      }
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const float x = mine[i] >= 0 ? to_f32(row[mine[i]]) : -INFINITY;
+        p[i] = mine[i] < 0 ? 0.0f : a.sigmoid ? sigmoid_stated(x) : expf(x - m) * (1.0f / sum);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int j = lane + i * G;
+      if (live && j < a.K) {
+        a.experts[t * a.K + j] = mine[i];
+        a.probs[t * a.K + j] = p[i] * a.scale;
+      }
+    }
+  }
+  if (a.partial != nullptr) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) sums[group][e0 + v] = total[v];
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += 256) {
+      float s = 0.0f;
+      for (int g = 0; g < 256 / G; ++g) s += sums[g][e];
+      a.partial[(int64_t)blockIdx.x * a.E + e] = s;
+    }
+  }
+}
+
+// The partial sums of 64 experts added in the order of the workgroups: 16 waves each every 16th, then the waves'.
+__global__ __launch_bounds__(1024) void route_sum_kernel(const float* partial, int blocks, int E, float* out) {
+  __shared__ float sums[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e = blockIdx.x * 64 + lane;
+  float s = 0.0f;
+  if (e < E)
+    for (int b = wave; b < blocks; b += 16) s += partial[(int64_t)b * E + e];
+  sums[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && e < E) {
+    for (int w = 1; w < 16; ++w) s += sums[w][lane];
+    out[e] = s;
+  }
+}
+
+// FULL: every score is needed (the scores' sums have a gradient, or the softmax is not renormalized).
+template <class T, int G, int V, bool FULL>
+__global__ __launch_bounds__(256) void route_topk_grad_kernel(RouteArgs a) {
+  constexpr int P = kPerLane<G>;
+  __shared__ int at_sm[256 / G][BSFP8_MAX_TOP_K];
+  __shared__ float part_sm[256 / G][BSFP8_MAX_TOP_K];
+  const int lane = threadIdx.x & (G - 1), group = threadIdx.x / G, e0 = lane * V;
+  for (int64_t t0 = (int64_t)blockIdx.x * (256 / G); t0 < a.T; t0 += (int64_t)gridDim.x * (256 / G)) {
+    const bool live = t0 + group < a.T;
+    const int64_t t = live ? t0 + group : a.T - 1;
+    const T* row = (const T*)a.logits + t * a.E;
+    float l[V], s[V], other[V];
+    if constexpr (FULL) {
+      load_logits<V>(row, e0, a.E, l);
+      scores_of<G, V>(l, a.sigmoid, s, other);
+    }
+    int e[P];
+    float g[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int j = lane + i * G;
+      e[i] = j < a.K ? a.experts[t * a.K + j] : -1;
+      if (e[i] >= a.E) e[i] = -1;
+      g[i] = e[i] >= 0 ? a.probs[t * a.K + j] * a.scale : 0.0f;
+    }
+    // what a choice gives to its expert: at the logit, or (softmax without renormalize) at the score
+    const bool at_score = !a.renormalize && !a.sigmoid;
+    if (a.renormalize) {
+      float ph[P], rest[P], mean = 0.0f;
+      chosen_scores<G>(row, e, a.sigmoid, ph, rest);
+#pragma unroll
+      for (int i = 0; i < P; ++i) mean += g[i] * ph[i];
+      mean = sum_over<G>(mean);
+#pragma unroll
+      for (int i = 0; i < P; ++i) g[i] = e[i] < 0 ? 0.0f : ph[i] * (g[i] - mean) * (a.sigmoid ? rest[i] : 1.0f);
+    } else if (a.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const float x = e[i] >= 0 ? to_f32(row[e[i]]) : -INFINITY;
+        float rest;
+        const float sc = sigmoid_stated(x, &rest);
+        g[i] = x == -INFINITY ? 0.0f : g[i] * sc * rest;
+      }
+    }
+    // the choices, seen by all lanes of the token (a wave's LDS accesses are done in order)
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int j = lane + i * G;
+      if (j < a.K) {
+        at_sm[group][j] = e[i];
+        part_sm[group][j] = g[i];
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    float d[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) d[v] = 0.0f;
+    for (int j = 0; j < a.K; ++j) {
+      const int x = at_sm[group][j] - e0;
+      const float y = part_sm[group][j];
+#pragma unroll
+      for (int v = 0; v < V; ++v) d[v] += x == v ? y : 0.0f;
+    }
+    if constexpr (FULL) {
+      float back[V], mean = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        back[v] = a.dsum != nullptr && e0 + v < a.E ? a.dsum[e0 + v] : 0.0f;
+        if (at_score) {
+          back[v] += d[v];
+          d[v] = 0.0f;
+        }
+        mean += s[v] == 0.0f ? 0.0f : back[v] * s[v];
+      }
+      if (a.sigmoid) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) d[v] += s[v] == 0.0f ? 0.0f : back[v] * s[v] * other[v];
+      } else {
+        mean = sum_over<G>(mean);
+#pragma unroll
+        for (int v = 0; v < V; ++v) d[v] += s[v] == 0.0f ? 0.0f : s[v] * (back[v] - mean);
+      }
+    }
+    if (live) {
+      T* out = (T*)a.dlogits + t * a.E + e0;
+      T o[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) from_f32(d[v], o[v]);
+      if (e0 + V <= a.E) {
+        __builtin_memcpy(out, o, sizeof(o));
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (e0 + v < a.E) out[v] = o[v];
+      }
+    }
+    // (the next token's choices are written after this one's were read: the same wave's accesses stay in order)
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// f with the lanes per token and the values per lane that E experts take.
+template <class F>
+static void for_experts(int E, F f) {
+  auto with = [&](auto g) {
+    constexpr int G = decltype(g)::value;
+    const int v = (E + G - 1) / G;
+    if (v <= 1) f(g, std::integral_constant<int, 1>());
+    else if (v <= 2) f(g, std::integral_constant<int, 2>());
+    else if (v <= 4) f(g, std::integral_constant<int, 4>());
+    else if (v <= 8) f(g, std::integral_constant<int, 8>());
+    else f(g, std::integral_constant<int, 16>());
+  };
+  if (route_lanes(E) == 16) with(std::integral_constant<int, 16>());
+  else with(std::integral_constant<int, 64>());
+}
+
+int launch_route_topk(const void* logits, bool f32, int64_t T, int E, int K, bool sigmoid, const float* bias,
+                      int renormalize, float scale, float* probs, int32_t* experts, float* score_sum, float* workspace,
+                      hipStream_t stream) {
+  const int64_t blocks = route_blocks(T, E);
+  if (blocks > 0) {
+    const RouteArgs a{logits, T, E, K, bias, sigmoid, renormalize, scale, probs, experts,
+                      score_sum != nullptr ? workspace : nullptr, nullptr, nullptr};
+    for_experts(E, [&](auto g, auto v) {
+      constexpr int G = decltype(g)::value, V = decltype(v)::value;
+      if (f32) hipLaunchKernelGGL((route_topk_kernel<float, G, V>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
+      else hipLaunchKernelGGL((route_topk_kernel<uint16_t, G, V>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
+    });
+    if (hipGetLastError() != hipSuccess) return BSFP8_ERR_LAUNCH;
+  }
+  if (score_sum == nullptr) return BSFP8_OK;
+  hipLaunchKernelGGL(route_sum_kernel, dim3((unsigned)((E + 63) / 64)), dim3(1024), 0, stream, workspace, (int)blocks, E,
+                     score_sum);
+  return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
+}
+
+int launch_route_topk_grad(const float* dprobs, const void* logits, bool f32, const int32_t* experts, int64_t T, int E,
+                           int K, bool sigmoid, int renormalize, float scale, const float* dsum, void* dlogits,
+                           hipStream_t stream) {
+  const RouteArgs a{logits, T, E, K, nullptr, sigmoid, renormalize, scale, const_cast<float*>(dprobs),
+                    const_cast<int32_t*>(experts), nullptr, dsum, dlogits};
+  const bool full = dsum != nullptr || (!sigmoid && !renormalize);
+  const dim3 grid((unsigned)route_blocks(T, E)), block(256);
+  for_experts(E, [&](auto g, auto v) {
+    constexpr int G = decltype(g)::value, V = decltype(v)::value;
+    if (f32 && full) hipLaunchKernelGGL((route_topk_grad_kernel<float, G, V, true>), grid, block, 0, stream, a);
+    else if (f32) hipLaunchKernelGGL((route_topk_grad_kernel<float, G, V, false>), grid, block, 0, stream, a);
+    else if (full) hipLaunchKernelGGL((route_topk_grad_kernel<uint16_t, G, V, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((route_topk_grad_kernel<uint16_t, G, V, false>), grid, block, 0, stream, a);
+  });
+  return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
+}
+
+}  // namespace bsfp8

@@ -1,0 +1,26 @@
+// Launch shapes of the router's and the plan's kernels, shared by the launchers and the workspace queries.
+#pragma once
+
+#include <stdint.h>
+
+namespace bsfp8 {
+
+// Router: lanes per token (a row of 16 where 16 values a lane hold all experts, a wave above) and the workgroups of 4
+// waves, each walking every gridDim-th set of tokens: at most 4 per CU, as many as partial sums of the scores.
+inline int route_lanes(int experts) { return experts <= 256 ? 16 : 64; }
+inline int64_t route_blocks(int64_t tokens, int experts) {
+  const int64_t per = 256 / route_lanes(experts), need = (tokens + per - 1) / per;
+  return need < 1024 ? need : 1024;
+}
+
+// Plan: choices are sorted in chunks of whole 4096s, at most 512 of them, one workgroup each.
+constexpr int64_t kPlanUnit = 4096;
+inline int64_t plan_chunk(int64_t choices) {
+  const int64_t units = (choices + kPlanUnit - 1) / kPlanUnit;
+  return (units + 511) / 512 * kPlanUnit;
+}
+inline int64_t plan_chunks(int64_t choices) {
+  return choices == 0 ? 0 : (choices + plan_chunk(choices) - 1) / plan_chunk(choices);
+}
+
+}  // namespace bsfp8

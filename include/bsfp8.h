@@ -14,7 +14,8 @@
  *     zero-row early return, device-resident split sizes).
  * and, around them, what a training or serving step of such a layer runs next to its GEMMs: the gated projection
  * with its activation and quantize in one kernel, the norms before and after a block with its gate and residual sum,
- * their gradients, and the AdamW step over all parameters.
+ * their gradients, the AdamW step over all parameters, the router with the tokens' way to their experts and back, and
+ * activations kept in 8 bits for the backward pass.
  *
  * Conventions for every entry point:
  *   - All data pointers are DEVICE pointers owned by the caller.  The library allocates
@@ -473,6 +474,154 @@ int bsfp8_adamw_step_stochastic(const void* device_plan, int32_t num_tensors, in
                                 int grad_dtype, int state, double lr, double beta1, double beta2, double eps,
                                 double weight_decay, int64_t step, const float* lr_dev, const int32_t* step_dev,
                                 const float* grad_scale, const float* noop_flag, uint64_t seed, void* stream);
+
+/* ----------------------------------------------------------------------------------------- */
+/* Tokens to their experts and back: the router's choice, the sort by expert, the rows        */
+/* gathered for the grouped calls above, and their weighted sum.                              */
+/* ----------------------------------------------------------------------------------------- */
+
+/* Scores of the router. */
+#define BSFP8_ROUTE_SOFTMAX 1
+#define BSFP8_ROUTE_SIGMOID 2
+
+#define BSFP8_MAX_TOP_K 32
+
+/*
+ * The top_k experts of each of `tokens` tokens and their probabilities, in fp32:
+ *     BSFP8_ROUTE_SOFTMAX:  s[t][e] = exp(l[t][e]) / sum_i exp(l[t][i])          key = l + bias
+ *     BSFP8_ROUTE_SIGMOID:  s[t][e] = 1 / (1 + exp2s(-l[t][e] * log2(e)))        key = s + bias
+ *   with exp2s as stated at bsfp8_grouped_act_quantize (each operation rounded in the order written, so that the
+ *   choice is the same on every IEEE machine).
+ * logits    [tokens][num_experts] of logits_dtype (BSFP8_F32 or BSFP8_BF16).  A logit or key of -infinity masks the
+ *           expert for that token: it is not chosen, and a logit of -infinity has the score 0.
+ * bias      fp32 [num_experts], moves the choice alone, or NULL (0)
+ * experts   int32 [tokens][top_k]: the experts of the largest keys, the largest first, the lowest index first among
+ *           equals (+0 equals -0, a NaN key comes before all others); -1 where fewer than top_k are open
+ * probs     fp32 [tokens][top_k]: scale * s of the chosen (0 beside -1); with renormalize == 1
+ *           scale * s / (sum of the chosen s)
+ * score_sum fp32 [num_experts] or NULL: sum of s[t][e] over the tokens, added in a fixed order
+ * workspace bsfp8_route_topk_workspace_bytes() bytes of device memory, needed with score_sum
+ * 1 <= num_experts <= BSFP8_MAX_GROUPS, 1 <= top_k <= min(num_experts, BSFP8_MAX_TOP_K), tokens * top_k <= 2^30.  The
+ * logits begin at a multiple of 16 bytes, rows of any length follow one another.  tokens == 0 writes nothing but zeros to score_sum.
+ */
+size_t bsfp8_route_topk_workspace_bytes(int64_t tokens, int32_t num_experts);
+int bsfp8_route_topk(const void* logits, int logits_dtype, int64_t tokens, int32_t num_experts, int32_t top_k,
+                     int scoring, const float* bias, int renormalize, float scale, float* probs, int32_t* experts,
+                     float* score_sum, void* workspace, void* stream);
+
+/*
+ * Its gradient: dlogits [tokens][num_experts] of logits_dtype, the gradient of
+ *     sum probs[t][j] * dprobs[t][j] + sum_e dscore_sum[e] * score_sum[e]
+ * with respect to the logits, the choice held.  experts as the forward wrote them (an entry outside
+ * [0, num_experts) is no choice; of an expert that stands twice both parts are added); dprobs fp32 [tokens][top_k];
+ * dscore_sum fp32 [num_experts] or NULL (0).
+ */
+int bsfp8_route_topk_grad(const float* dprobs, const void* logits, int logits_dtype, const int32_t* experts,
+                          int64_t tokens, int32_t num_experts, int32_t top_k, int scoring, int renormalize, float scale,
+                          const float* dscore_sum, void* dlogits, void* stream);
+
+/*
+ * The choices c = t * top_k + j sorted by their experts, those of one expert in the order of c.  A choice whose expert
+ * lies outside [0, num_experts) is dropped (no expert: -1; under expert parallelism: another rank's, with the first
+ * local expert's index taken off).
+ * experts      int32 [tokens][top_k]
+ * probs        fp32 [tokens][top_k] or NULL
+ * split_sizes  int32 [num_experts]: rows of each expert
+ * rows         int32 [tokens][top_k]: the row of each choice, -1 if dropped
+ * choices      int32 [tokens * top_k]: the choice of each row, -1 past the last row
+ * row_probs    fp32 [tokens * top_k]: probs of each row's choice, 0 past the last row; NULL without probs
+ * workspace    bsfp8_dispatch_plan_workspace_bytes() bytes of device memory (0 for few choices: may be NULL)
+ * tokens * top_k <= 2^30.  tokens == 0 writes zeros to split_sizes.
+ */
+size_t bsfp8_dispatch_plan_workspace_bytes(int64_t tokens, int32_t top_k, int32_t num_experts);
+int bsfp8_dispatch_plan(const int32_t* experts, const float* probs, int64_t tokens, int32_t top_k, int32_t num_experts,
+                        int32_t* split_sizes, int32_t* rows, int32_t* choices, float* row_probs, void* workspace,
+                        void* stream);
+
+/*
+ * Rows of tokens for their experts: out[rows[t][j]] = weights[t][j] * x[t], rounded once from fp32.
+ * x        [tokens][cols] of dtype (BSFP8_F32 or BSFP8_BF16); out [capacity_rows][cols] of dtype
+ * rows     int32 [tokens][top_k], as bsfp8_dispatch_plan writes them; one outside [0, capacity_rows) is skipped
+ * weights  fp32 [tokens][top_k], or NULL (1: the rows are copied bit for bit)
+ * Rows of out that no choice has are not written.  1 <= cols <= 2^24, tokens * top_k <= 2^30,
+ * capacity_rows <= 2^31 - 1.  This is also the gradient of bsfp8_combine without weights.
+ */
+int bsfp8_dispatch(const void* x, int dtype, int64_t tokens, int64_t cols, const int32_t* rows, int32_t top_k,
+                   const float* weights, void* out, int64_t capacity_rows, void* stream);
+
+/*
+ * The same rows straight into the quantized layouts of bsfp8_grouped_quantize for [capacity_rows][cols]: the bytes
+ * that it writes for the rows of bsfp8_dispatch, except that weighted rows are quantized from their fp32 products.
+ * x_bf16    [tokens][cols] bf16
+ * choices   int32 [capacity_rows], as bsfp8_dispatch_plan writes them.  Rows without a choice in
+ *           [0, tokens * top_k) at or past sum(split_sizes) are not written
+ * recipe    BSFP8_RECIPE_MX_1X32_E8M0 or BSFP8_RECIPE_MXFP4_1X32_E8M0
+ * split_sizes  as bsfp8_dispatch_plan writes them
+ */
+int bsfp8_dispatch_quantize(const void* x_bf16, int64_t tokens, int64_t cols, const int32_t* choices, int32_t top_k,
+                            const float* weights, int64_t capacity_rows, const int32_t* split_sizes,
+                            int32_t num_groups, int recipe, int which, uint8_t* row_q, uint8_t* row_s, uint8_t* col_q,
+                            uint8_t* col_s, uint32_t* status, void* stream);
+
+/*
+ * The experts' rows back at their tokens: out[t] = add[t] + sum_j weights[t][j] * y[rows[t][j]], the sum over j in fp32
+ * in the order of j, rounded once.
+ * y       [capacity_rows][cols] of dtype; a row outside [0, capacity_rows) counts as zero and is not read
+ * weights fp32 [tokens][top_k] or NULL (1: this is the gradient of bsfp8_dispatch without weights)
+ * add     [tokens][cols] of dtype or NULL (0); may be out itself
+ * out     [tokens][cols] of dtype
+ */
+int bsfp8_combine(const void* y, int dtype, int64_t capacity_rows, int64_t cols, const int32_t* rows, int64_t tokens,
+                  int32_t top_k, const float* weights, const void* add, void* out, void* stream);
+
+/*
+ * Its gradient: dy[rows[t][j]] = weights[t][j] * dout[t] and dweights[t][j] = sum over the channels of
+ * dout[t] * y[rows[t][j]] (0 for a choice without a row), the sum in fp32 in a fixed order.  (With x in place of dout
+ * and the rows' gradient in place of y, dweights is that of a weighted bsfp8_dispatch, whose dx is bsfp8_combine of the
+ * rows' gradient with the same weights.)
+ * dout      [tokens][cols] of dtype
+ * y         [capacity_rows][cols] of dtype, needed for dweights
+ * dy        [capacity_rows][cols] of dtype or NULL; may be y itself.  Rows that no choice has are not written
+ * dweights  fp32 [tokens][top_k] or NULL
+ */
+int bsfp8_combine_grad(const void* dout, int dtype, int64_t tokens, int64_t cols, const void* y, int64_t capacity_rows,
+                       const int32_t* rows, int32_t top_k, const float* weights, void* dy, float* dweights,
+                       void* stream);
+
+/* ----------------------------------------------------------------------------------------- */
+/* Activations kept in 8 bits for the backward pass.                                          */
+/* ----------------------------------------------------------------------------------------- */
+/*
+ * bsfp8_grouped_act_quantize (activation BSFP8_ACT_SRELU or BSFP8_ACT_SWIGLU, the same bytes), and in the same pass its
+ * input h, kept for the gradient in 8 bits: the bytes that bsfp8_grouped_quantize writes for h with
+ * BSFP8_RECIPE_MX_1X32_E8M0 and BSFP8_ROWWISE.
+ * kept_q, kept_s  those of [capacity_rows][cols] (SReLU) or [capacity_rows][2 cols] (SwiGLU)
+ */
+int bsfp8_grouped_act_checkpoint(int activation, const void* h_bf16, const float* probs, int64_t capacity_rows,
+                                 int64_t cols, const int32_t* split_sizes, int32_t num_groups, int recipe, int which,
+                                 uint8_t* row_q, uint8_t* row_s, uint8_t* col_q, uint8_t* col_s, uint8_t* kept_q,
+                                 uint8_t* kept_s, uint32_t* status, void* stream);
+
+/*
+ * The gradient from what was kept.  With h the values that kept_q and kept_s stand for, r = max(h, 0),
+ * sg = 1 / (1 + exp(-a)), in fp32:
+ *     SReLU:   g = 2 r p dy                          quantized as [capacity_rows][cols]
+ *              v = r^2
+ *     SwiGLU:  (da | db) = (dy p b sg (1 + a (1 - sg)) | dy p a sg)        as [capacity_rows][2 cols]
+ *              v = a sg b
+ * which, row_q, ...   layouts of the gradient (recipe BSFP8_RECIPE_MX_1X32_E8M0 or BSFP8_RECIPE_MXFP4_1X32_E8M0); 0: none
+ * y_col_q, y_col_s    NULL, or the activation p v again, in the colwise layout of [capacity_rows][cols] (same recipe):
+ *                     the operand of the second projection's weight gradient, so that the forward need not keep it
+ * dprobs     fp32 [capacity_rows] or NULL: sum over the channels of dy v, in a fixed order (live rows only)
+ * workspace  bsfp8_grouped_act_checkpoint_grad_workspace_bytes() bytes of device memory, needed with dprobs
+ * kept_q, kept_s, probs, dy as in the forward; dy_bf16 [capacity_rows][cols].  Some output is asked for.
+ */
+size_t bsfp8_grouped_act_checkpoint_grad_workspace_bytes(int64_t capacity_rows, int64_t cols);
+int bsfp8_grouped_act_checkpoint_grad(int activation, const uint8_t* kept_q, const uint8_t* kept_s, const float* probs,
+                                      const void* dy_bf16, int64_t capacity_rows, int64_t cols,
+                                      const int32_t* split_sizes, int32_t num_groups, int recipe, int which,
+                                      uint8_t* row_q, uint8_t* row_s, uint8_t* col_q, uint8_t* col_s, uint8_t* y_col_q,
+                                      uint8_t* y_col_s, float* dprobs, void* workspace, uint32_t* status, void* stream);
 
 /* Static description of a return code. */
 const char* bsfp8_strerror(int code);
