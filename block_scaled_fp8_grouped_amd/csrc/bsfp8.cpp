@@ -189,7 +189,7 @@ int check_checkpoint(int activation, int64_t capacity_rows, int64_t cols, const 
   if (!valid_recipe(recipe)) return BSFP8_ERR_RECIPE;
   if (!mx_recipe(recipe)) return BSFP8_ERR_LAYOUT;
   if ((which & ~(BSFP8_ROWWISE | BSFP8_COLWISE)) != 0) return BSFP8_ERR_ARGUMENT;
-  if (capacity_rows < 0 || capacity_rows > (int64_t(1) << 31) || !valid_dim(cols) || cols > kMaxOutCols)
+  if (capacity_rows < 0 || capacity_rows + 127 > kMaxKExtent || !valid_dim(cols) || cols > kMaxOutCols)
     return BSFP8_ERR_SHAPE;
   if (split_sizes == nullptr) return BSFP8_ERR_NULL_POINTER;
   return valid_groups(num_groups) ? BSFP8_OK : BSFP8_ERR_NUM_GROUPS;
@@ -613,6 +613,7 @@ int bsfp8_dispatch_quantize(const void* x_bf16, int64_t tokens, int64_t cols, co
   if (!mx_recipe(recipe)) return BSFP8_ERR_LAYOUT;
   if (which <= 0 || (which & ~(BSFP8_ROWWISE | BSFP8_COLWISE)) != 0) return BSFP8_ERR_ARGUMENT;
   if (!valid_rows_moved(tokens, cols, top_k, capacity_rows) || !valid_dim(cols)) return BSFP8_ERR_SHAPE;
+  if (capacity_rows + 127 > kMaxKExtent) return BSFP8_ERR_SHAPE;
   if (!valid_groups(num_groups)) return BSFP8_ERR_NUM_GROUPS;
   if (capacity_rows == 0) return BSFP8_OK;
   if ((x_bf16 == nullptr && tokens > 0) || choices == nullptr || split_sizes == nullptr) return BSFP8_ERR_NULL_POINTER;
@@ -675,7 +676,7 @@ int bsfp8_grouped_act_checkpoint(int activation, const void* h_bf16, const float
 }
 
 size_t bsfp8_grouped_act_checkpoint_grad_workspace_bytes(int64_t capacity_rows, int64_t cols) {
-  if (capacity_rows < 0 || capacity_rows > (int64_t(1) << 31) || !valid_dim(cols) || cols > kMaxOutCols) return 0;
+  if (capacity_rows < 0 || capacity_rows + 127 > kMaxKExtent || !valid_dim(cols) || cols > kMaxOutCols) return 0;
   return bsfp8::act_checkpoint_grad_workspace_bytes(capacity_rows, cols);
 }
 

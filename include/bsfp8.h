@@ -557,6 +557,8 @@ int bsfp8_dispatch(const void* x, int dtype, int64_t tokens, int64_t cols, const
  *           [0, tokens * top_k) at or past sum(split_sizes) are not written
  * recipe    BSFP8_RECIPE_MX_1X32_E8M0 or BSFP8_RECIPE_MXFP4_1X32_E8M0
  * split_sizes  as bsfp8_dispatch_plan writes them
+ * capacity_rows + 127 must stay below 2^24 - 128, as for bsfp8_grouped_gemm_wgrad, here and in the two calls below that
+ * quantize activations (the kernels address a group's channels with 32-bit offsets); BSFP8_ERR_SHAPE otherwise.
  */
 int bsfp8_dispatch_quantize(const void* x_bf16, int64_t tokens, int64_t cols, const int32_t* choices, int32_t top_k,
                             const float* weights, int64_t capacity_rows, const int32_t* split_sizes,
@@ -596,6 +598,7 @@ int bsfp8_combine_grad(const void* dout, int dtype, int64_t tokens, int64_t cols
  * input h, kept for the gradient in 8 bits: the bytes that bsfp8_grouped_quantize writes for h with
  * BSFP8_RECIPE_MX_1X32_E8M0 and BSFP8_ROWWISE.
  * kept_q, kept_s  those of [capacity_rows][cols] (SReLU) or [capacity_rows][2 cols] (SwiGLU)
+ * cols is at most 2^21.
  */
 int bsfp8_grouped_act_checkpoint(int activation, const void* h_bf16, const float* probs, int64_t capacity_rows,
                                  int64_t cols, const int32_t* split_sizes, int32_t num_groups, int recipe, int which,

@@ -91,8 +91,8 @@ def quantize(x=P, tokens=4, cols=64, choices=P, k=2, weights=P, cap=8, splits=P,
 
 
 LAYOUTS = [(dict(recipe=9), RECIPE), (dict(recipe=bs.RECIPE_PC), LAYOUT), (dict(recipe=bs.RECIPE_MX | bs.GEMM_FP8_MFMA), RECIPE),
-           (dict(which=4), ARG), (dict(cols=48), SHAPE), (dict(cols=0), SHAPE), (dict(cap=-1), SHAPE), (dict(E=0), GROUPS),
-           (dict(E=1025), GROUPS), (dict(splits=None), NULL), (dict(rq=None), NULL), (dict(rs=None), NULL),
+           (dict(which=4), ARG), (dict(cols=48), SHAPE), (dict(cols=0), SHAPE), (dict(cap=-1), SHAPE), (dict(cap=(1 << 24) - 254), SHAPE),
+           (dict(E=0), GROUPS), (dict(E=1025), GROUPS), (dict(splits=None), NULL), (dict(rq=None), NULL), (dict(rs=None), NULL),
            (dict(cq=None), NULL), (dict(cs=None), NULL), (dict(rq=P + 8), ALIGN), (dict(cs=P + 8), ALIGN),
            (dict(splits=P + 2), ALIGN), (dict(status=P + 1), ALIGN)]
 
@@ -118,7 +118,7 @@ def keep_grad(act=bs.ACT_SRELU, kq=P, ks=P, probs=P, dy=P, cap=8, cols=64, split
 
 
 KEEP = LAYOUTS + [(dict(act=0), ARG), (dict(act=bs.ACT_SRELU_GRAD), ARG), (dict(act=bs.ACT_SWIGLU_GRAD), ARG),
-                  (dict(cap=(1 << 31) + 1), SHAPE), (dict(cols=(1 << 21) + 32), SHAPE), (dict(kq=None), NULL),
+                  (dict(cols=(1 << 21) + 32), SHAPE), (dict(kq=None), NULL),
                   (dict(ks=None), NULL), (dict(kq=P + 4), ALIGN), (dict(ks=P + 4), ALIGN), (dict(probs=P + 2), ALIGN),
                   (dict(cap=0, kq=None, rq=None), OK)]
 
