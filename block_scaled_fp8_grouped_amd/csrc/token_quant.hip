@@ -2,12 +2,14 @@
 // activation between two projections with its input kept in 8 bits, and its gradient from what was kept.
 // include/bsfp8.h states the formulas, group_layout.hpp the layouts.
 //
-// A wave owns 32 rows of a group (a block of the colwise layout) and walks along their columns, 16 * CH at a time: lane
-// l has CH consecutive channels (l % 16) of 8 consecutive rows (l / 16).  So both layouts' blocks are reduced by moves
-// between lanes (4 or 8 neighbours along a row; the 4 lanes of a column), a lane's 8 rows of a channel are 8 consecutive
-// colwise codes, and nothing goes through LDS: no barrier, and as many waves as registers allow hide the loads of each
-// other.  The 4 waves of a workgroup have the 128 rows that share a channel's 128-byte line of codes.  What belongs to a
-// row (the choice that it stands for, its probability, its part of dprobs) is held while the wave walks.
+// A wave owns 32 rows of a group (a block of the colwise layout) and walks along their columns, 128 at a time: lane l has
+// 8 consecutive channels (l % 16) of 8 consecutive rows (l / 16).  So both layouts' blocks are reduced by moves between
+// lanes (4 neighbours along a row; the 4 lanes of a column), and a row's codes are stored from registers, 128 bytes of a
+// row at a time.  A lane's 8 rows of a channel are 8 consecutive colwise codes; those of the 4 waves of a workgroup meet in
+// LDS, whence a channel's 128 leave as one line.  What belongs to a row (the choice that it stands for, its probability,
+// its part of dprobs) is held while the wave walks.
+#include <math.h>
+
 #include <type_traits>
 
 #include "act_math.hpp"
@@ -18,15 +20,16 @@
 
 namespace bsfp8 {
 
+// Codes go past the caches (a line's 128 bytes leave together, and none is read again here): 181 -> 170 us on 65536 gathered rows of
+// 4096.
+constexpr int kPastCaches = 2;
 constexpr int kTThreads = 256;
 
-// What a launch does: the rows of tokens (as they are, or weighted), or an activation's forward or gradient.
-constexpr int kModeRows = 0, kModeWeighted = 1, kModeSrelu = 2, kModeSwiglu = 3, kModeSreluGrad = 4, kModeSwigluGrad = 5;
-constexpr bool mode_rows(int m) { return m <= kModeWeighted; }
+// An activation's forward or gradient.
+constexpr int kModeSrelu = 0, kModeSwiglu = 1, kModeSreluGrad = 2, kModeSwigluGrad = 3;
 constexpr bool mode_grad(int m) { return m >= kModeSreluGrad; }
 constexpr bool mode_glu(int m) { return m == kModeSwiglu || m == kModeSwigluGrad; }
-// channels a lane holds: 4 where three arrays of values (da, db and the activation) have to stay in registers
-constexpr int mode_channels(int m) { return mode_grad(m) ? 4 : 8; }
+constexpr int kTCols = 128;  // channels of a tile: 16 lanes of 8
 
 struct TokenQuantArgs {
   const uint16_t* in;      // rows of tokens, or h (forward), or dy (gradient)
@@ -50,24 +53,17 @@ template <int CTRL>
 __device__ __forceinline__ uint32_t lane_move(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
 }
-constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141;  // lane moves within a quad; of 8 lanes, the order reversed
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E;  // lane moves within a quad
 
-// From each lane's 8 row maxima m the blocks' (over the 4 neighbours of a quad, and with CH == 4 the next quad): lane q of
-// its quad gets those of rows q and 4 + q.  Each step halves the values a lane carries, so that a scale is worked out once
-// and not by every lane of its block.
-template <int CH>
+// From each lane's 8 row maxima m those of the 4 lanes of its quad, which have a block of 32 channels: lane q gets those of rows
+// q and 4 + q.  Each step halves the values a lane carries, so that a scale is worked out once and not by every lane of
+// its block.
 __device__ __forceinline__ void row_block_max(const uint32_t (&m)[8], int ch, uint32_t (&out)[2]) {
   const bool odd = ch & 1, high = ch & 2;
   uint32_t t[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    uint32_t a = m[2 * k], b = m[2 * k + 1];
-    if constexpr (CH == 4) {
-      a = max(a, lane_move<kHalfMirror>(a));
-      b = max(b, lane_move<kHalfMirror>(b));
-    }
-    t[k] = max(odd ? b : a, lane_move<kXor1>(odd ? a : b));
-  }
+  for (int k = 0; k < 4; ++k)
+    t[k] = max(odd ? m[2 * k + 1] : m[2 * k], lane_move<kXor1>(odd ? m[2 * k] : m[2 * k + 1]));
 #pragma unroll
   for (int k = 0; k < 2; ++k)
     out[k] = max(high ? t[2 * k + 1] : t[2 * k], lane_move<kXor2>(high ? t[2 * k] : t[2 * k + 1]));
@@ -107,45 +103,44 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t m) {
   // (e8m0_byte's steps, its lower end by a saturating subtraction)
   return __builtin_elementwise_sub_sat((m + 0x1fffffu) >> 23, 8u);
 }
-// N (4 or 8) values' codes: 4 to a word, or with F4 8 to a word (N == 4: in its low half).
-template <bool F4, int N>
+// 8 values' codes: 4 to a word, with F4 8 to a word.
+template <bool F4>
 struct Codes {
-  uint32_t w[F4 ? 1 : N / 4];
+  uint32_t w[F4 ? 1 : 2];
 };
-template <bool F4, int N>
-__device__ __forceinline__ Codes<F4, N> codes_of(const float (&v)[N], uint32_t byte) {
-  Codes<F4, N> q;
+template <bool F4>
+__device__ __forceinline__ Codes<F4> codes_of(const float (&v)[8], uint32_t byte) {
   if constexpr (F4) {
     const float s = exp2_neg((int)byte - 127);
-    if constexpr (N == 8)
-      q.w[0] = e2m1x8(v[0] * s, v[1] * s, v[2] * s, v[3] * s, v[4] * s, v[5] * s, v[6] * s, v[7] * s);
-    else
-      q.w[0] = e2m1x8(v[0] * s, v[1] * s, v[2] * s, v[3] * s, 0.0f, 0.0f, 0.0f, 0.0f);
+    return {{e2m1x8(v[0] * s, v[1] * s, v[2] * s, v[3] * s, v[4] * s, v[5] * s, v[6] * s, v[7] * s)}};
   } else {
     const float s = __uint_as_float(byte << 23);
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) q.w[i] = e4m3x4_scaled(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], s);
+    return {{e4m3x4_scaled(v[0], v[1], v[2], v[3], s), e4m3x4_scaled(v[4], v[5], v[6], v[7], s)}};
   }
-  return q;
 }
 
-// A lane's 8 rows x CH channels: as fp32, or (bf16 inputs as they are) pairs of channels.  Largest magnitudes are those of
-// bit patterns where the bytes have to be grouped_quantize's (a NaN block has an infinity's scale there), and otherwise
-// (CH == 4, gradients) fp32 maxima, which pass over a NaN and take the magnitude for nothing.
-template <int CH>
+// A lane's 8 rows x 8 channels: as fp32, or (bf16 inputs as they are) pairs of channels.  Largest magnitudes are those of
+// bit patterns where the bytes have to be grouped_quantize's (a NaN block has an infinity's scale there), or (FLOAT:
+// gradients) fp32 maxima, which pass over a NaN and take the magnitude for nothing.
+template <bool FLOAT>
 struct Values {
-  float v[8][CH];
+  float v[8][8];
   __device__ __forceinline__ uint32_t row_max(int i) const {
-    if constexpr (CH == 4) return __float_as_uint(max3_abs(max3_abs(0.0f, v[i][0], v[i][1]), v[i][2], v[i][3]));
+    if constexpr (FLOAT) {
+      float f = 0.0f;
+#pragma unroll
+      for (int c = 0; c < 8; c += 2) f = max3_abs(f, v[i][c], v[i][c + 1]);
+      return __float_as_uint(f);
+    }
     uint32_t m = 0;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) m = max(m, magnitude(v[i][c]));
+    for (int c = 0; c < 8; ++c) m = max(m, magnitude(v[i][c]));
     return m;
   }
-  __device__ __forceinline__ void col_max(uint32_t (&m)[CH]) {
+  __device__ __forceinline__ void col_max(uint32_t (&m)[8]) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      if constexpr (CH == 4) {
+    for (int c = 0; c < 8; ++c) {
+      if constexpr (FLOAT) {
         float f = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; i += 2) f = max3_abs(f, v[i][c], v[i + 1][c]);
@@ -161,13 +156,13 @@ struct Values {
     }
   }
   template <bool F4>
-  __device__ __forceinline__ Codes<F4, CH> row_codes(int i, uint32_t byte) const {
-    return codes_of<F4, CH>(v[i], byte);
+  __device__ __forceinline__ Codes<F4> row_codes(int i, uint32_t byte) const {
+    return codes_of<F4>(v[i], byte);
   }
   template <bool F4>
-  __device__ __forceinline__ Codes<F4, 8> col_codes(int c, uint32_t byte) const {
+  __device__ __forceinline__ Codes<F4> col_codes(int c, uint32_t byte) const {
     const float x[8] = {v[0][c], v[1][c], v[2][c], v[3][c], v[4][c], v[5][c], v[6][c], v[7][c]};
-    return codes_of<F4, 8>(x, byte);
+    return codes_of<F4>(x, byte);
   }
 };
 
@@ -209,7 +204,7 @@ struct Pairs {
     }
   }
   template <bool F4>
-  __device__ __forceinline__ Codes<F4, 8> row_codes(int i, uint32_t byte) const {
+  __device__ __forceinline__ Codes<F4> row_codes(int i, uint32_t byte) const {
     if constexpr (F4) {
       float x[8];
 #pragma unroll
@@ -217,19 +212,19 @@ struct Pairs {
         x[2 * c] = bf16_lo(w[i][c]);
         x[2 * c + 1] = bf16_hi(w[i][c]);
       }
-      return codes_of<F4, 8>(x, byte);
+      return codes_of<F4>(x, byte);
     } else {
       const float s = __uint_as_float(byte << 23);
       return {{e4m3x4_bf16(w[i][0], w[i][1], s), e4m3x4_bf16(w[i][2], w[i][3], s)}};
     }
   }
   template <bool F4>
-  __device__ __forceinline__ Codes<F4, 8> col_codes(int c, uint32_t byte) const {
+  __device__ __forceinline__ Codes<F4> col_codes(int c, uint32_t byte) const {
     if constexpr (F4) {
       float x[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = c & 1 ? bf16_hi(w[i][c / 2]) : bf16_lo(w[i][c / 2]);
-      return codes_of<F4, 8>(x, byte);
+      return codes_of<F4>(x, byte);
     } else {
       const float s = __uint_as_float(byte << 23);
       uint32_t p[4];  // the channel's rows in pairs
@@ -266,33 +261,32 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
   const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32));
   return (int64_t)((uint64_t)hi << 32 | lo);
 }
-template <bool F4, int N>
-__device__ __forceinline__ void store_codes(__amdgpu_buffer_rsrc_t rs, uint32_t off, const Codes<F4, N>& q) {
-  if constexpr (F4 && N == 4) __builtin_amdgcn_raw_buffer_store_b16((short)q.w[0], rs, (int)off, 0, 0);
-  else if constexpr (F4 || N == 4) __builtin_amdgcn_raw_buffer_store_b32((int)q.w[0], rs, (int)off, 0, 0);
-  else __builtin_amdgcn_raw_buffer_store_b64(v2i{(int)q.w[0], (int)q.w[1]}, rs, (int)off, 0, 0);
+template <bool F4>
+__device__ __forceinline__ void store_codes(__amdgpu_buffer_rsrc_t rs, uint32_t off, const Codes<F4>& q) {
+  if constexpr (F4) __builtin_amdgcn_raw_buffer_store_b32((int)q.w[0], rs, (int)off, 0, kPastCaches);
+  else __builtin_amdgcn_raw_buffer_store_b64(v2i{(int)q.w[0], (int)q.w[1]}, rs, (int)off, 0, kPastCaches);
 }
 
 // The values along their rows: codes into q [R][width] from channel c0 on, scales into s [width / 32][R].
-template <bool F4, int CH, class V>
+template <bool F4, class V>
 __device__ __forceinline__ void put_rows(const LanePlace& l, uint8_t* q, uint8_t* s, uint32_t width, int64_t c0, const V& x) {
   constexpr int PER = F4 ? 2 : 1;
   uint32_t m[8], top[2];
 #pragma unroll
   for (int i = 0; i < 8; ++i) m[i] = x.row_max(i);
-  row_block_max<CH>(m, l.ch, top);
+  row_block_max(m, l.ch, top);
   const uint32_t byte[2] = {scale_byte<F4>(top[0]), scale_byte<F4>(top[1])};
   const uint8_t* at = q + (l.row0 * width + c0) / PER;
-  const uint32_t off = l.live_col ? (8 * (uint32_t)l.rl * width + (uint32_t)(l.ch * CH)) / PER : kNowhere;
+  const uint32_t off = l.live_col ? (8 * (uint32_t)l.rl * width + (uint32_t)(l.ch * 8)) / PER : kNowhere;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t b = byte[i >> 2], of = i % 4 == 0 ? quad_lane<0>(b) : i % 4 == 1 ? quad_lane<1>(b) : i % 4 == 2 ? quad_lane<2>(b) : quad_lane<3>(b);
-    store_codes<F4, CH>(row_buffer(at, i, width / PER, l.live), off, x.template row_codes<F4>(i, of));
+    store_codes<F4>(row_buffer(at, i, width / PER, l.live), off, x.template row_codes<F4>(i, of));
   }
-  // a block's first quad has its 8 scales, two a lane
+  // the quad has its block's 8 scales, two a lane
   const int r = l.ch & 3;
   const __amdgpu_buffer_rsrc_t rs = buffer_at(s + c0 / 32 * l.R + l.row0);
-  const uint32_t to = (CH == 8 || (l.ch & 4) == 0) && l.live_col ? (uint32_t)(l.ch * CH / 32) * (uint32_t)l.R + 8 * l.rl + r : kNowhere;
+  const uint32_t to = l.live_col ? (uint32_t)(l.ch / 4) * (uint32_t)l.R + 8 * l.rl + r : kNowhere;
   __builtin_amdgcn_raw_buffer_store_b8((char)byte[0], rs, (int)(r < l.nl ? to : kNowhere), 0, 0);
   __builtin_amdgcn_raw_buffer_store_b8((char)byte[1], rs, (int)(4 + r < l.nl ? to : kNowhere), 4, 0);
   __builtin_amdgcn_sched_barrier(0);
@@ -308,108 +302,315 @@ struct ColTile {
   static __device__ __forceinline__ int swizzle(int channel) { return (channel >> 3) & (GRANULES - 1); }
 };
 
-// The values along their columns: codes into a tile's [16 * CH] channels in LDS, scales into the colwise layout of `width`
+// The values along their columns: codes into a tile's 128 channels in LDS, scales into the colwise layout of `width`
 // channels.
-template <bool F4, int CH, class V>
+template <bool F4, class V>
 __device__ __forceinline__ void put_cols(const LanePlace& l, int wave, uint8_t* codes, uint8_t* s, int64_t width, int64_t c0,
                                          V& x) {
   typedef ColTile<F4> T;
-  uint32_t m[CH];
+  uint32_t m[8];
   x.col_max(m);
   const __amdgpu_buffer_rsrc_t rs = buffer_at(s + col_e8m0(width, l.p, l.block, c0));
   const int at = (32 * wave + 8 * l.rl) / (F4 ? 2 : 1);  // first of the lane's 8 codes in a channel's run
 #pragma unroll
-  for (int k = 0; k < CH / 4; ++k) {
+  for (int k = 0; k < 2; ++k) {
     const uint32_t mine = scale_byte<F4>(col_block_max(m[4 * k], m[4 * k + 1], m[4 * k + 2], m[4 * k + 3]));
     uint32_t byte[4];
     col_broadcast(mine, byte);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int channel = l.ch * CH + 4 * k + i;
-      const Codes<F4, 8> q = x.template col_codes<F4>(4 * k + i, byte[i]);
+      const int channel = l.ch * 8 + 4 * k + i;
+      const Codes<F4> q = x.template col_codes<F4>(4 * k + i, byte[i]);
       __builtin_memcpy(codes + channel * T::RUN + (((at >> 4) ^ T::swizzle(channel)) << 4 | (at & 15)), q.w, sizeof(q.w));
     }
-    __builtin_amdgcn_raw_buffer_store_b8((char)mine, rs, (int)(l.live_col ? l.ch * CH + l.rl : (int)kNowhere), 4 * k, 0);
+    __builtin_amdgcn_raw_buffer_store_b8((char)mine, rs, (int)(l.live_col ? l.ch * 8 + l.rl : (int)kNowhere), 4 * k, 0);
   }
   __builtin_amdgcn_sched_barrier(0);
 }
 
 // A tile's codes from LDS to the layout, 16 bytes a lane; `wave0`: the workgroup's first block of 32 rows.
-template <bool F4, int W>
+template <bool F4>
 __device__ __forceinline__ void flush_cols(const LanePlace& l, int64_t block0, const uint8_t* codes, uint8_t* q, int64_t width,
                                            int64_t c0, int ncols) {
   typedef ColTile<F4> T;
   const __amdgpu_buffer_rsrc_t rs = buffer_at(q + col_elem(width, l.p, l.kp, c0, 32 * block0) / (F4 ? 2 : 1));
   const uint32_t run = (uint32_t)l.kp / (F4 ? 2 : 1);
 #pragma unroll
-  for (int i = 0; i < W * T::GRANULES / kTThreads; ++i) {
+  for (int i = 0; i < kTCols * T::GRANULES / kTThreads; ++i) {
     const int g = i * kTThreads + (int)threadIdx.x, channel = g / T::GRANULES, k = g % T::GRANULES;
     const v4i w = *(const v4i*)(codes + channel * T::RUN + 16 * (k ^ T::swizzle(channel)));
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, w), rs,
-                                           (int)(channel < ncols ? (uint32_t)channel * run + 16u * (uint32_t)k : kNowhere), 0, 0);
+                                           (int)(channel < ncols ? (uint32_t)channel * run + 16u * (uint32_t)k : kNowhere), 0, kPastCaches);
   }
 }
 
-// A lane's 4 e4m3 codes times their block's power of two, 2^(byte - 127).
-__device__ __forceinline__ void unpack_codes(uint32_t w, uint32_t byte, float (&v)[4]) {
+// 8 e4m3 codes times their block's power of two, 2^(byte - 127).
+__device__ __forceinline__ void unpack_codes(const v2i& w, uint32_t byte, float (&v)[8]) {
   const float scale = __uint_as_float(byte << 23);  // (the conversion takes its exponent field alone: 0 stands for 2^-127)
-  const auto lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, scale, false), hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, scale, true);
-  v[0] = lo[0];
-  v[1] = lo[1];
-  v[2] = hi[0];
-  v[3] = hi[1];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const auto lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((uint32_t)w[i], scale, false);
+    const auto hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((uint32_t)w[i], scale, true);
+    v[4 * i] = lo[0];
+    v[4 * i + 1] = lo[1];
+    v[4 * i + 2] = hi[0];
+    v[4 * i + 3] = hi[1];
+  }
 }
 
 // The value is worked out here and now: the compiler would move its last steps to the branch that stores it and hold their
 // operands instead, which are more.
-__device__ __forceinline__ void keep(float& v) { asm volatile("" : "+v"(v)); }
+template <class T>
+__device__ __forceinline__ void keep(T& v) {
+  asm volatile("" : "+v"(v));
+}
 
 // 8 consecutive scale bytes of a column of blocks, of which n are there.
-__device__ __forceinline__ uint64_t load_bytes(const uint8_t* p, int n) {
-  uint64_t b = 0;
+__device__ __forceinline__ void load_bytes(const uint8_t* p, int n, uint32_t (&out)[2]) {
+  out[0] = out[1] = 0;
   if (n == 8) {
-    __builtin_memcpy(&b, p, 8);
+    __builtin_memcpy(out, p, 8);
   } else {
+    uint64_t b = 0;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) b |= (uint64_t)p[i] << (8 * i);
+    out[0] = (uint32_t)b;
+    out[1] = (uint32_t)(b >> 32);
   }
-  return b;
 }
 
 // A lane's inputs of one column tile as they lie in memory.
 template <int MODE>
 struct TokenInputs;
 template <>
-struct TokenInputs<kModeRows> {
+struct TokenInputs<kModeSrelu> {
   Pairs h;
 };
 template <>
-struct TokenInputs<kModeWeighted> : TokenInputs<kModeRows> {};
-template <>
-struct TokenInputs<kModeSrelu> : TokenInputs<kModeRows> {};
-template <>
-struct TokenInputs<kModeSwiglu> : TokenInputs<kModeRows> {
+struct TokenInputs<kModeSwiglu> : TokenInputs<kModeSrelu> {
   Pairs b;
 };
 template <>
 struct TokenInputs<kModeSreluGrad> {
-  uint32_t k0[8];
-  v2i dy[8];
-  uint64_t s0;
+  v2i k0[8];
+  v4i dy[8];
+  uint32_t s0[2];
 };
 template <>
 struct TokenInputs<kModeSwigluGrad> : TokenInputs<kModeSreluGrad> {
-  uint32_t k1[8];
-  uint64_t s1;
+  v2i k1[8];
+  uint32_t s1[2];
 };
 
+// Inclusive sum over a wave, with data-parallel lane moves.
+__device__ __forceinline__ int wave_scan32(int v) {
+  auto add = [&](auto ctrl, auto rows) {
+    v += __builtin_amdgcn_update_dpp(0, v, decltype(ctrl)::value, decltype(rows)::value, 0xf, false);
+  };
+  using std::integral_constant;
+  add(integral_constant<int, 0x111>(), integral_constant<int, 0xf>());  // 1, 2, 4, 8 lanes below in the row of 16
+  add(integral_constant<int, 0x112>(), integral_constant<int, 0xf>());
+  add(integral_constant<int, 0x114>(), integral_constant<int, 0xf>());
+  add(integral_constant<int, 0x118>(), integral_constant<int, 0xf>());
+  add(integral_constant<int, 0x142>(), integral_constant<int, 0xa>());  // row 0's total to row 1, 2's to 3
+  add(integral_constant<int, 0x143>(), integral_constant<int, 0xc>());  // the first half's total to the second
+  return v;
+}
+__device__ __forceinline__ int wave_total(int v) { return __builtin_amdgcn_readlane(wave_scan32(v), 63); }
+
+// Row tiles (of 128 rows) in an order in which the groups advance side by side, each in proportion to its size: with S tiles
+// in the largest group, a group of T has given floor(j T / S) of them by the end of step j, at most one a step.  A token's rows
+// lie in several groups, at about the same fraction of each (the plan keeps the tokens' order), so that the tiles in
+// flight at a time read the same tokens and find them in the caches.  Every wave works the order out by itself; lane l has
+// groups V l .. V l + V - 1.
+template <int V>
+struct Turns {
+  int k[V];         // rows
+  uint32_t rate[V]; // tiles a step, in units of 2^-32, rounded up (0: one)
+  int off, packed;  // rows before the lane's first group, and padded to 128 (valid sizes: below 2^24 and 2^25)
+  int most;         // (uniform) tiles of the largest group
+
+  __device__ __forceinline__ static int tiles(int rows) { return (rows + 127) >> 7; }
+  // the sizes, and what is wrong with them
+  __device__ __forceinline__ uint32_t read(const int32_t* __restrict__ splits, int E, int64_t capacity) {
+    const int lane = threadIdx.x & 63;
+    bool negative = false, large = false;
+    off = packed = most = 0;
+    int64_t rows = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = lane * V + i, v = e < E ? splits[e] : 0;
+      negative |= v < 0;
+      large |= (int64_t)v > capacity;
+      k[i] = v < 0 || (int64_t)v > capacity ? 0 : v;  // below 2^24: a lane's and a wave's sums are below 2^34
+      rows += k[i];
+      packed += tiles(k[i]);
+      most = max(most, tiles(k[i]));
+    }
+    uint32_t flags = __ballot(negative) != 0 ? BSFP8_STATUS_NEGATIVE_SPLIT : 0u;
+    // (in units of 256 rows, rounded down and up, where 32 bits would not do)
+    large |= rows > capacity;
+    const int low = wave_total((int)(rows >> 8)), part = wave_total((int)(rows & 255));
+    if (__ballot(large) != 0 || ((int64_t)low << 8) + part > capacity) flags |= BSFP8_STATUS_EXCEEDS_CAPACITY;
+    if (flags) return flags;
+    off = wave_scan32((int)rows) - (int)rows;
+    packed = 128 * (wave_scan32(packed) - packed);
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) most = max(most, __shfl_xor(most, d, 64));
+    most = __builtin_amdgcn_readfirstlane(most);
+    // T 2^32 / S is a multiple of 1 / S, at least 2^-17, and double is off by less: rounded up rightly.  S times it is T and
+    // less than S / 2^32 more, so that the last step ends at T.
+#pragma unroll
+    for (int i = 0; i < V; ++i) rate[i] = tiles(k[i]) == most ? 0u : (uint32_t)ceil((double)tiles(k[i]) * 0x1p32 / (double)most);
+    return 0;
+  }
+  // tiles of the lane's group i, and of all, in the first j steps
+  __device__ __forceinline__ int given(int i, int j) const {
+    return k[i] == 0 ? 0 : rate[i] == 0u ? j : (int)__umulhi((uint32_t)j, rate[i]);
+  }
+  __device__ __forceinline__ int until(int j) const {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) n += given(i, j);
+    return wave_total(n);
+  }
+  // tile m: its group's rows, their first, the packed offset, and which of the group's tiles it is; false past the last
+  __device__ __forceinline__ bool find(int m, int& rows, int& first, int& p, int& tile) const {
+    int lo = 0, hi = most;  // the step with until(lo) <= m < until(lo + 1)
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (m < until(mid + 1)) hi = mid;
+      else lo = mid + 1;
+    }
+    if (lo == most) return false;
+    const int left = m - until(lo);
+    int has = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) has += given(i, lo + 1) > given(i, lo);
+    const int seen = wave_scan32(has) - has;  // groups of this step before the lane's
+    const int who = __builtin_ctzll(__ballot(left >= seen && left < seen + has));
+    int n = left - seen, o = off, q = packed, size = 0, at = 0;
+    bool done = false;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const bool in = given(i, lo + 1) > given(i, lo);
+      if (!done && in && n == 0) {
+        size = k[i];
+        at = given(i, lo);
+        done = true;
+      }
+      n -= in;
+      if (!done) {
+        o += k[i];
+        q += 128 * tiles(k[i]);
+      }
+    }
+    rows = __builtin_amdgcn_readlane(size, who);
+    first = __builtin_amdgcn_readlane(o, who);
+    p = __builtin_amdgcn_readlane(q, who);
+    tile = __builtin_amdgcn_readlane(at, who);
+    return true;
+  }
+};
+
+// Rows of tokens: a row tile's column segment, the row tiles in the order of Turns (V > 0), or as they lie (V == 0: rowwise
+// only, few rows, no need of the groups).
+template <bool WEIGHTED, bool F4, int V>
+__global__ __launch_bounds__(kTThreads) void dispatch_quantize_kernel(TokenQuantArgs a) {
+  constexpr int W = kTCols;
+  __shared__ __attribute__((aligned(16))) uint8_t codes[2][W * ColTile<F4>::RUN];
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const bool row_out = a.row_q != nullptr, col_out = V > 0 && a.col_q != nullptr;
+  const uint32_t F = (uint32_t)a.F;
+  const int64_t seg = blockIdx.x % (uint32_t)a.segments, m = blockIdx.x / (uint32_t)a.segments;
+  LanePlace l;
+  l.ch = lane & 15;
+  l.rl = lane >> 4;
+  l.R = a.R;
+  Turns<V ? V : 1> turns;
+  if constexpr (V > 0) {
+    const uint32_t flags = turns.read(a.splits, a.E, a.R);
+    report_status(a.status, flags);
+    if (flags) return;
+  }
+  int64_t left;
+  if constexpr (V > 0) {
+    int rows, first, p, tile;
+    if (!turns.find((int)m, rows, first, p, tile)) return;
+    const int in_group = 128 * tile + 32 * wave;
+    l.row0 = first + in_group;
+    l.p = p;
+    l.kp = (rows + 127) & ~127;
+    l.block = in_group / 32;
+    left = rows - in_group;
+  } else {
+    l.row0 = m * 128 + 32 * wave;
+    l.p = l.kp = l.block = 0;
+    left = a.R - l.row0;
+  }
+  l.live = (int)(left < 0 ? 0 : left < 32 ? left : 32);
+  left -= 8 * l.rl;
+  l.nl = (int)(left < 0 ? 0 : left < 8 ? left : 8);
+  const uint16_t* src[8];
+  float weight[8];
+  int there = 0;  // rows up to the first without a choice
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t c = i < l.nl ? (int64_t)a.choices[l.row0 + 8 * l.rl + i] : -1;
+    const bool ok = c >= 0 && c < a.tokens * a.K;
+    there = ok && there == i ? i + 1 : there;
+    src[i] = ok ? a.in + (int64_t)((uint32_t)c / (uint32_t)a.K) * F + l.ch * 8 : nullptr;
+    weight[i] = WEIGHTED && ok ? a.probs[c] : 1.0f;
+  }
+  if constexpr (V == 0) {  // rows without a choice are not stored
+    l.nl = there;
+    l.live = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int n = __builtin_amdgcn_readlane(there, 16 * k);
+      l.live = l.live == 8 * k ? 8 * k + n : l.live;
+    }
+  }
+  int turn = 0;
+  const int64_t begin = seg * a.tiles * W, stop = begin + (int64_t)a.tiles * W, end = stop < F ? stop : F;
+  for (int64_t c0 = begin; c0 < end; c0 += W) {
+    l.live_col = c0 + l.ch * 8 < F;
+    Pairs x;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v4i w = {0, 0, 0, 0};
+      if (src[i] != nullptr && l.live_col) w = *(const v4i*)(src[i] + c0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x.w[i][k] = (uint32_t)w[k];
+    }
+    auto put = [&](auto& values) {
+      if (row_out) put_rows<F4>(l, a.row_q, a.row_s, F, c0, values);
+      if (!col_out) return;
+      put_cols<F4>(l, wave, codes[turn], a.col_s, F, c0, values);
+      __syncthreads();  // (two buffers, as below)
+      flush_cols<F4>(l, l.block - wave, codes[turn], a.col_q, F, c0, F - c0 < W ? (int)(F - c0) : W);
+      turn ^= 1;
+    };
+    if constexpr (WEIGHTED) {
+      Values<false> y;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y.v[i][k] = (k & 1 ? bf16_hi(x.w[i][k / 2]) : bf16_lo(x.w[i][k / 2])) * weight[i];
+      __builtin_amdgcn_sched_barrier(0);
+      put(y);
+    } else {
+      put(x);
+    }
+  }
+}
+
 template <int MODE, bool F4>
-__global__ __launch_bounds__(kTThreads) void token_quant_kernel(TokenQuantArgs a) {
-  constexpr bool GRAD = mode_grad(MODE), GLU = mode_glu(MODE), ROWS = mode_rows(MODE);
-  constexpr int CH = mode_channels(MODE), W = 16 * CH, HALVES = GLU ? 2 : 1, OUTS = GRAD ? HALVES : 1;
-  constexpr int ARRAYS = GRAD ? HALVES + 1 : 1;  // of colwise codes: the output's halves, the activation
+__global__ __launch_bounds__(kTThreads, mode_grad(MODE) ? 2 : 1) void act_checkpoint_kernel(TokenQuantArgs a) {
+  constexpr bool GRAD = mode_grad(MODE), GLU = mode_glu(MODE);
+  constexpr int W = kTCols, HALVES = GLU ? 2 : 1, OUTS = GRAD ? HALVES : 1;
   __shared__ GroupScanSmem<kTThreads> gsm;
-  __shared__ __attribute__((aligned(16))) uint8_t codes[2][ARRAYS][W * ColTile<F4>::RUN];
+  __shared__ __attribute__((aligned(16))) uint8_t codes[2][W * ColTile<F4>::RUN];
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int64_t rt = blockIdx.x / (uint32_t)a.segments, seg = blockIdx.x % (uint32_t)a.segments;
   const bool row_out = a.row_q != nullptr, col_out = a.col_q != nullptr;
@@ -420,72 +621,31 @@ __global__ __launch_bounds__(kTThreads) void token_quant_kernel(TokenQuantArgs a
   l.rl = lane >> 4;
   l.R = a.R;
   int64_t left;  // rows from the wave's first on
-  // rows of tokens without the colwise layout need no groups: theirs are the rows that have a choice
-  if (!ROWS || col_out) {
-    GroupInfo g{};
-    const uint32_t flags = group_scan<kTThreads>(a.splits, a.E, a.R, 128, rt, 0, gsm, g);
-    report_status(a.status, flags);
-    if (g.e < 0) return;
-    const int64_t in_group = uniform64(128 * (rt - g.tile) + 32 * wave);
-    left = uniform64(g.k) - in_group;
-    l.row0 = uniform64(g.off) + in_group;
-    l.p = uniform64(g.p);
-    l.kp = uniform64(g.kp);
-    l.block = in_group / 32;
-  } else {
-    l.row0 = 128 * rt + 32 * wave;
-    left = a.R - l.row0;
-    l.p = l.kp = l.block = 0;
-  }
+  GroupInfo g{};
+  const uint32_t flags = group_scan<kTThreads>(a.splits, a.E, a.R, 128, rt, 0, gsm, g);
+  report_status(a.status, flags);
+  if (g.e < 0) return;
+  const int64_t in_group = uniform64(128 * (rt - g.tile) + 32 * wave);
+  left = uniform64(g.k) - in_group;
+  l.row0 = uniform64(g.off) + in_group;
+  l.p = uniform64(g.p);
+  l.kp = uniform64(g.kp);
+  l.block = in_group / 32;
   l.live = (int)(left < 0 ? 0 : left < 32 ? left : 32);
   left -= 8 * l.rl;
   l.nl = (int)(left < 0 ? 0 : left < 8 ? left : 8);
 
-  // the source rows and probabilities of a lane's 8 rows
-  int64_t src[ROWS ? 8 : 1];
   float prob[8], part[GRAD ? 8 : 1];
-  bool ok[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    ok[i] = i < l.nl;
-    prob[i] = 1.0f;
-    if constexpr (ROWS) {
-      const int64_t c = ok[i] ? (int64_t)a.choices[l.row0 + 8 * l.rl + i] : -1;
-      ok[i] = c >= 0 && c < a.tokens * a.K;
-      src[i] = ok[i] ? (int64_t)((uint32_t)c / (uint32_t)a.K) * F : 0;
-      if (MODE == kModeWeighted && ok[i]) prob[i] = a.probs[c];
-    } else if (ok[i] && a.probs != nullptr) {
-      prob[i] = a.probs[l.row0 + 8 * l.rl + i];
-    }
+    prob[i] = i < l.nl && a.probs != nullptr ? a.probs[l.row0 + 8 * l.rl + i] : 1.0f;
     if constexpr (GRAD) part[i] = 0.0f;
-  }
-  if constexpr (ROWS) {
-    if (!col_out) {  // rows are stored up to the first without a choice
-      int n = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) n = ok[i] && n == i ? i + 1 : n;
-      l.nl = n;
-      l.live = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int m = __builtin_amdgcn_readlane(n, 16 * k);
-        l.live = l.live == 8 * k ? 8 * k + m : l.live;
-      }
-    }
   }
 
   auto load = [&](int64_t c0, TokenInputs<MODE>& x) {
-    const bool live_col = c0 + l.ch * CH < F;
-    if constexpr (ROWS) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v4i w = {0, 0, 0, 0};
-        if (ok[i] && live_col) w = *(const v4i*)(a.in + src[i] + c0 + l.ch * CH);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x.h.w[i][k] = (uint32_t)w[k];
-      }
-    } else if constexpr (!GRAD) {
-      const uint32_t off = live_col ? 2 * (8 * (uint32_t)l.rl * wide + (uint32_t)(l.ch * CH)) : kNowhere;
+    const bool live_col = c0 + l.ch * 8 < F;
+    if constexpr (!GRAD) {
+      const uint32_t off = live_col ? 2 * (8 * (uint32_t)l.rl * wide + (uint32_t)(l.ch * 8)) : kNowhere;
 #pragma unroll
       for (int half = 0; half < HALVES; ++half) {
         const uint16_t* at = a.in + l.row0 * wide + half * (int64_t)F + c0;
@@ -501,107 +661,134 @@ __global__ __launch_bounds__(kTThreads) void token_quant_kernel(TokenQuantArgs a
         }
       }
     } else {
-      const uint32_t off = live_col ? 8 * (uint32_t)l.rl * wide + (uint32_t)(l.ch * CH) : kNowhere;
-      const uint32_t dyo = live_col ? 2 * (8 * (uint32_t)l.rl * F + (uint32_t)(l.ch * CH)) : kNowhere;
+      const uint32_t off = live_col ? 8 * (uint32_t)l.rl * wide + (uint32_t)(l.ch * 8) : kNowhere;
+      const uint32_t dyo = live_col ? 2 * (8 * (uint32_t)l.rl * F + (uint32_t)(l.ch * 8)) : kNowhere;
       const uint8_t* q = a.kq + l.row0 * wide + c0;
       const uint16_t* dy = a.in + l.row0 * F + c0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        x.k0[i] = __builtin_amdgcn_raw_buffer_load_b32(row_buffer(q, i, wide, l.live), (int)off, 0, 0);
-        if constexpr (GLU) x.k1[i] = __builtin_amdgcn_raw_buffer_load_b32(row_buffer(q + F, i, wide, l.live), (int)off, 0, 0);
+        x.k0[i] = __builtin_bit_cast(
+            v2i, __builtin_amdgcn_raw_buffer_load_b64(row_buffer(q, i, wide, l.live), (int)off, 0, 0));
+        if constexpr (GLU)
+          x.k1[i] = __builtin_bit_cast(
+              v2i, __builtin_amdgcn_raw_buffer_load_b64(row_buffer(q + F, i, wide, l.live), (int)off, 0, 0));
         x.dy[i] = __builtin_bit_cast(
-            v2i, __builtin_amdgcn_raw_buffer_load_b64(row_buffer(dy, i, 2 * F, l.live), (int)dyo, 0, 0));
+            v4i, __builtin_amdgcn_raw_buffer_load_b128(row_buffer(dy, i, 2 * F, l.live), (int)dyo, 0, 0));
       }
       const int nl = live_col ? l.nl : 0;
-      const uint8_t* s = a.ks + c0 / 32 * a.R + l.row0 + ((uint64_t)(l.ch * CH / 32) * (uint64_t)a.R + 8 * l.rl);
-      x.s0 = load_bytes(s, nl);
-      if constexpr (GLU) x.s1 = load_bytes(s + (int64_t)(F / 32) * a.R, nl);
+      const uint8_t* s = a.ks + c0 / 32 * a.R + l.row0 + ((uint64_t)(l.ch * 8 / 32) * (uint64_t)a.R + 8 * l.rl);
+      load_bytes(s, nl, x.s0);
+      if constexpr (GLU) load_bytes(s + (int64_t)(F / 32) * a.R, nl, x.s1);
     }
   };
 
   // (loading a tile ahead costs more waves than it hides: 368 us against 400 on 65536 x 2048 of the SwiGLU's gradient)
   TokenInputs<MODE> x;
-  const int64_t begin = seg * a.tiles * W, stop = begin + (int64_t)a.tiles * W, end = stop < F ? stop : F;
   int turn = 0;
+  const int64_t begin = seg * a.tiles * W, stop = begin + (int64_t)a.tiles * W, end = stop < F ? stop : F;
+  // the colwise layout of a tile's values: `half` of the `width` channels from c0 on
+  auto cols = [&](uint8_t* q, uint8_t* s, uint32_t width, int64_t c0, int64_t half, auto& values) {
+    put_cols<F4>(l, wave, codes[turn], s, width, half + c0, values);
+    // (two buffers: a wave that fills the one of the array after next has passed the next one's barrier, which every wave
+    // reaches with its part of this one read)
+    __syncthreads();
+    flush_cols<F4>(l, l.block - wave, codes[turn], q, width, half + c0, F - c0 < W ? (int)(F - c0) : W);
+    turn ^= 1;
+  };
   for (int64_t c0 = begin; c0 < end; c0 += W) {
-    l.live_col = c0 + l.ch * CH < F;
+    l.live_col = c0 + l.ch * 8 < F;
     load(c0, x);
-    if constexpr (MODE == kModeRows) {
-            if (row_out) put_rows<F4, 8>(l, a.row_q, a.row_s, C, c0, x.h);
-      if (col_out) put_cols<F4, 8>(l, wave, codes[turn][0], a.col_s, C, c0, x.h);
-    } else if constexpr (!GRAD) {
-      if constexpr (!ROWS) {
-        put_rows<false, 8>(l, a.kept_q, a.kept_s, wide, c0, x.h);
-        if constexpr (GLU) put_rows<false, 8>(l, a.kept_q, a.kept_s, wide, F + c0, x.b);
-      }
-      Values<8> y;
+    if constexpr (!GRAD) {
+      put_rows<false>(l, a.kept_q, a.kept_s, wide, c0, x.h);
+      if constexpr (GLU) put_rows<false>(l, a.kept_q, a.kept_s, wide, F + c0, x.b);
+      Values<false> y;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float p = prob[i];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const float h = k & 1 ? bf16_hi(x.h.w[i][k / 2]) : bf16_lo(x.h.w[i][k / 2]);
-          if constexpr (ROWS) y.v[i][k] = h * p;
-          else if constexpr (!GLU) y.v[i][k] = act_value<1>(h, 0.0f, p, 0.0f);
+          if constexpr (!GLU) y.v[i][k] = act_value<1>(h, 0.0f, p, 0.0f);
           else y.v[i][k] = act_value<3>(h, k & 1 ? bf16_hi(x.b.w[i][k / 2]) : bf16_lo(x.b.w[i][k / 2]), p, 0.0f);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
-      if (row_out) put_rows<F4, 8>(l, a.row_q, a.row_s, C, c0, y);
-      if (col_out) put_cols<F4, 8>(l, wave, codes[turn][0], a.col_s, C, c0, y);
+      if (row_out) put_rows<F4>(l, a.row_q, a.row_s, C, c0, y);
+      if (col_out) cols(a.col_q, a.col_s, C, c0, 0, y);
     } else {
-      Values<4> y, z, v;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float h[4], b[4];
-        unpack_codes(x.k0[i], (uint32_t)(x.s0 >> (8 * i)) & 255u, h);
-        if constexpr (GLU) unpack_codes(x.k1[i], (uint32_t)(x.s1 >> (8 * i)) & 255u, b);
-        const float p = prob[i];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t w = (uint32_t)x.dy[i][k / 2];
-          const float d = k & 1 ? bf16_hi(w) : bf16_lo(w);
-          if constexpr (!GLU) {
-            const float r = h[k] > 0.0f ? h[k] : 0.0f, r2 = r * r;
-            y.v[i][k] = 2.0f * r * p * d;
-            v.v[i][k] = r2 * p;
-            part[i] = __builtin_fmaf(d, r2, part[i]);
-          } else {
-            float dp = 0.0f;
-            swiglu_grad(h[k], b[k], p, d, y.v[i][k], z.v[i][k], dp);
-            v.v[i][k] = swiglu(h[k], b[k], p);
-            part[i] += dp;
-            keep(z.v[i][k]);
-          }
-          keep(y.v[i][k]);
-          keep(v.v[i][k]);
+      // one array of values at a time, worked out from the inputs and the sigmoids, which stay
+      Values<true> y, sg;
+      float d[8], h[8], b[8];
+      auto inputs = [&](int i) {
+        keep(x.k0[i]);
+        keep(x.s0[i >> 2]);
+        unpack_codes(x.k0[i], x.s0[i >> 2] >> (8 * (i & 3)) & 255u, h);
+        if constexpr (GLU) {
+          keep(x.k1[i]);
+          keep(x.s1[i >> 2]);
+          unpack_codes(x.k1[i], x.s1[i >> 2] >> (8 * (i & 3)) & 255u, b);
         }
+        keep(x.dy[i]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) d[k] = k & 1 ? bf16_hi((uint32_t)x.dy[i][k / 2]) : bf16_lo((uint32_t)x.dy[i][k / 2]);
+      };
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {  // the activation, its part of dprobs
+        inputs(i);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float val;
+          if constexpr (!GLU) {
+            const float r = h[k] > 0.0f ? h[k] : 0.0f;
+            val = r * r;
+          } else {
+            sg.v[i][k] = sigmoid_fast(h[k]);
+            keep(sg.v[i][k]);
+            val = h[k] * sg.v[i][k] * b[k];
+          }
+          part[i] = __builtin_fmaf(d[k], val, part[i]);
+          y.v[i][k] = val * prob[i];
+          keep(y.v[i][k]);
+        }
+        keep(part[i]);
       }
       __builtin_amdgcn_sched_barrier(0);
-      if (row_out) {
-        put_rows<F4, 4>(l, a.row_q, a.row_s, C, c0, y);
-        if constexpr (GLU) put_rows<F4, 4>(l, a.row_q, a.row_s, C, F + c0, z);
+      if (a.ycol_q != nullptr) cols(a.ycol_q, a.ycol_s, F, c0, 0, y);
+      if (row_out || col_out) {
+        if constexpr (GLU) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            inputs(i);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              
+              y.v[i][k] = d[k] * prob[i] * (h[k] * sg.v[i][k]);
+              keep(y.v[i][k]);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          if (row_out) put_rows<F4>(l, a.row_q, a.row_s, C, F + c0, y);
+          if (col_out) cols(a.col_q, a.col_s, C, c0, F, y);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          inputs(i);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            if constexpr (!GLU) {
+              const float r = h[k] > 0.0f ? h[k] : 0.0f;
+              y.v[i][k] = 2.0f * r * prob[i] * d[k];
+            } else {
+              const float s = sg.v[i][k], sl = h[k] * s;
+              y.v[i][k] = d[k] * prob[i] * b[k] * (s + __builtin_fmaf(-sl, s, sl));
+            }
+            keep(y.v[i][k]);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (row_out) put_rows<F4>(l, a.row_q, a.row_s, C, c0, y);
+        if (col_out) cols(a.col_q, a.col_s, C, c0, 0, y);
       }
-      if (col_out) {
-        put_cols<F4, 4>(l, wave, codes[turn][0], a.col_s, C, c0, y);
-        if constexpr (GLU) put_cols<F4, 4>(l, wave, codes[turn][HALVES - 1], a.col_s, C, F + c0, z);
-      }
-      if (a.ycol_q != nullptr) put_cols<F4, 4>(l, wave, codes[turn][ARRAYS - 1], a.ycol_s, F, c0, v);
-    }
-    // (two buffers: a wave that fills the one of the tile after next has passed the next tile's barrier, which every wave
-    // reaches with its part of this one read)
-    if (col_out || (GRAD && a.ycol_q != nullptr)) {
-      __syncthreads();
-      const int ncols = F - c0 < W ? (int)(F - c0) : W;
-      const int64_t block0 = l.block - wave;
-      if (col_out) {
-        flush_cols<F4, W>(l, block0, codes[turn][0], a.col_q, C, c0, ncols);
-        if constexpr (GRAD && GLU) flush_cols<F4, W>(l, block0, codes[turn][1], a.col_q, C, F + c0, ncols);
-      }
-      if constexpr (GRAD) {
-        if (a.ycol_q != nullptr) flush_cols<F4, W>(l, block0, codes[turn][ARRAYS - 1], a.ycol_q, F, c0, ncols);
-      }
-      turn ^= 1;
     }
   }
   if constexpr (GRAD) {
@@ -642,12 +829,15 @@ __global__ __launch_bounds__(256) void token_dprobs_kernel(const float* partial,
   dprobs[r] = s;
 }
 
-// Column segments of a launch over `rows` row tiles and `cols` column tiles: as many as give 4096 workgroups (16 per CU).
+// Column segments of a launch over `rows` row tiles and `cols` column tiles: as many as give kTFill workgroups, or twice that for
+// an activation's forward (2048 / 4096 / 8192 workgroups: SReLU of 65536 x 4096 300 / 278 / 264 us, its gradient
+// 352 / 335 / 328, SwiGLU's of 65536 x 2048 288 / 281 / 306, 65536 gathered rows of 4096 170 / 170 / 181).
 struct TokenSegments {
   int64_t count, tiles;
 };
-static TokenSegments token_segments(int64_t rows, int64_t cols) {
-  int64_t n = (4096 + rows - 1) / (rows < 1 ? 1 : rows);
+constexpr int64_t kTFill = 4096;
+static TokenSegments token_segments(int64_t rows, int64_t cols, int64_t fill = kTFill) {
+  int64_t n = (fill + rows - 1) / (rows < 1 ? 1 : rows);
   n = n < 1 ? 1 : n > cols ? cols : n;
   const int64_t per = (cols + n - 1) / n;
   return {(cols + per - 1) / per, per};
@@ -659,22 +849,20 @@ static int64_t token_row_tiles(int64_t R, int E) {
 
 size_t act_checkpoint_grad_workspace_bytes(int64_t R, int64_t F) {
   // (at least as many segments as with any number of groups)
-  return (size_t)token_segments(token_row_tiles(R, 0), (F + 63) / 64).count * (size_t)R * sizeof(float);
+  return (size_t)token_segments(token_row_tiles(R, 0), (F + kTCols - 1) / kTCols).count * (size_t)R * sizeof(float);
 }
 
 template <int MODE>
 static int launch_mode(const TokenQuantArgs& given, bool f4, hipStream_t stream) {
   TokenQuantArgs a = given;
-  constexpr int W = 16 * mode_channels(MODE);
-  const bool grouped = !mode_rows(MODE) || a.col_q != nullptr;
-  const int64_t rows = token_row_tiles(a.R, grouped ? a.E : 0);
-  const TokenSegments s = token_segments(rows, (a.F + W - 1) / W);
+  const int64_t rows = token_row_tiles(a.R, a.E);
+  const TokenSegments s = token_segments(rows, (a.F + kTCols - 1) / kTCols, mode_grad(MODE) ? kTFill : 2 * kTFill);
   const int64_t blocks = rows * s.count;
   if (blocks > 0x7fffffff) return BSFP8_ERR_SHAPE;
   a.segments = (int)s.count;
   a.tiles = (int)s.tiles;
-  if (f4) hipLaunchKernelGGL((token_quant_kernel<MODE, true>), dim3((unsigned)blocks), dim3(kTThreads), 0, stream, a);
-  else hipLaunchKernelGGL((token_quant_kernel<MODE, false>), dim3((unsigned)blocks), dim3(kTThreads), 0, stream, a);
+  if (f4) hipLaunchKernelGGL((act_checkpoint_kernel<MODE, true>), dim3((unsigned)blocks), dim3(kTThreads), 0, stream, a);
+  else hipLaunchKernelGGL((act_checkpoint_kernel<MODE, false>), dim3((unsigned)blocks), dim3(kTThreads), 0, stream, a);
   return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
 }
 
@@ -696,8 +884,29 @@ int launch_dispatch_quantize(const void* x, int64_t T, int64_t C, const int32_t*
   a.col_q = col_q;
   a.col_s = col_s;
   a.status = status;
+  // few rows that need no groups are taken as they lie
+  const bool turns = col_q != nullptr || R >= 4096;
+  const int64_t rows = token_row_tiles(R, turns ? E : 0);
+  const TokenSegments seg = token_segments(rows, (C + kTCols - 1) / kTCols);
+  if (rows * seg.count > 0x7fffffff) return BSFP8_ERR_SHAPE;
+  a.segments = (int)seg.count;
+  a.tiles = (int)seg.tiles;
+  const dim3 grid((unsigned)(rows * seg.count)), block(kTThreads);
+  auto go = [&](auto weighted, auto f4) {
+    constexpr bool W = decltype(weighted)::value, F4 = decltype(f4)::value;
+    if (!turns) hipLaunchKernelGGL((dispatch_quantize_kernel<W, F4, 0>), grid, block, 0, stream, a);
+    else if (E <= 64) hipLaunchKernelGGL((dispatch_quantize_kernel<W, F4, 1>), grid, block, 0, stream, a);
+    else if (E <= 256) hipLaunchKernelGGL((dispatch_quantize_kernel<W, F4, 4>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((dispatch_quantize_kernel<W, F4, 16>), grid, block, 0, stream, a);
+  };
+  const std::integral_constant<bool, true> yes;
+  const std::integral_constant<bool, false> no;
   const bool f4 = recipe == BSFP8_RECIPE_MXFP4_1X32_E8M0;
-  return weights != nullptr ? launch_mode<kModeWeighted>(a, f4, stream) : launch_mode<kModeRows>(a, f4, stream);
+  if (weights != nullptr && f4) go(yes, yes);
+  else if (weights != nullptr) go(yes, no);
+  else if (f4) go(no, yes);
+  else go(no, no);
+  return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
 }
 
 int launch_act_checkpoint(int act, const void* h, const float* probs, int64_t R, int64_t F, const int32_t* splits, int E,
@@ -746,7 +955,7 @@ int launch_act_checkpoint_grad(int act, const uint8_t* kept_q, const uint8_t* ke
   const int rc = act == BSFP8_ACT_SRELU ? launch_mode<kModeSreluGrad>(a, f4, stream)
                                         : launch_mode<kModeSwigluGrad>(a, f4, stream);
   if (rc != BSFP8_OK || dprobs == nullptr) return rc;
-  const int64_t parts = token_segments(token_row_tiles(R, E), (F + 63) / 64).count;
+  const int64_t parts = token_segments(token_row_tiles(R, E), (F + kTCols - 1) / kTCols).count;
   hipLaunchKernelGGL(token_dprobs_kernel, dim3((unsigned)((R + 255) / 256)), dim3(256), 0, stream, workspace, R, parts,
                      splits, E, dprobs);
   return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
