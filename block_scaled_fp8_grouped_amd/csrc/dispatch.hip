@@ -169,7 +169,11 @@ struct MoveArgs {
   void* out;
   const void* y;
   float* dweights;
+  bool past;  // the output goes past the caches
 };
+// Outputs that no cache holds until they are read go past it (gradient of 65536 rows of 4096 265 -> 247 us, 16384 tokens' sums
+// of 2050 fp32 188 -> 173); smaller ones are left for what reads them next.
+static bool move_past(int64_t rows, int64_t cols, bool f32) { return rows * cols * (f32 ? 4 : 2) >= int64_t(64) << 20; }
 
 // Threads over (token, chunk of 8 columns): a workgroup takes 256 chunks of one token, or several whole tokens where
 // their rows are shorter; `shift`: log2 of the threads that a token takes in a workgroup.
@@ -192,18 +196,22 @@ __device__ __forceinline__ bool move_place(const MoveArgs& a, int shift, int64_t
 }
 
 // 8 elements as they were loaded, bit for bit.
-__device__ __forceinline__ void copy8(float* p, int n, const Raw8<float>& v) {
+__device__ __forceinline__ void copy8(float* p, int n, const Raw8<float>& v, bool past) {
   if (n >= 8) {
-    __builtin_memcpy(p, v.t, sizeof(v.t));
+    if (past) stream8(p, v.t);
+    else __builtin_memcpy(p, v.t, sizeof(v.t));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i < n) p[i] = v.t[i];
   }
 }
-__device__ __forceinline__ void copy8(uint16_t* p, int n, const Raw8<uint16_t>& v) {
+__device__ __forceinline__ void copy8(uint16_t* p, int n, const Raw8<uint16_t>& v, bool past) {
   if (n >= 8) {
-    __builtin_memcpy(p, v.w, sizeof(v.w));
+    uint16_t t[8];
+    __builtin_memcpy(t, v.w, sizeof(t));
+    if (past) stream8(p, t);
+    else __builtin_memcpy(p, t, sizeof(t));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -223,18 +231,36 @@ __global__ __launch_bounds__(256) void dispatch_kernel(MoveArgs a, int shift, in
     if (r < 0 || r >= a.cap) continue;
     T* out = (T*)a.out + r * a.C + c;
     if (a.weights == nullptr) {
-      copy8(out, n, v);
+      copy8(out, n, v, a.past);
       continue;
     }
     float o[8];
     const float w = a.weights[t * a.K + j];
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = v[i] * w;
-    store8(out, n, o);
+    store8(out, n, o, a.past);
   }
 }
 
-template <class T>
+// The rows of KB of a token's choices from j0 on (-1: none), and their weights.
+template <int KB>
+struct TokenRows {
+  int32_t r[KB];
+  float w[KB];
+  __device__ __forceinline__ TokenRows(const MoveArgs& a, int64_t t, int j0) {
+#pragma unroll
+    for (int j = 0; j < KB; ++j) {
+      const bool in = j0 + j < a.K;
+      r[j] = in ? a.rows[t * a.K + j0 + j] : -1;
+      w[j] = in && a.weights != nullptr ? a.weights[t * a.K + j0 + j] : 1.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < KB; ++j) r[j] = r[j] >= 0 && r[j] < a.cap ? r[j] : -1;
+  }
+};
+
+// KB rows are in flight at a time.
+template <class T, int KB>
 __global__ __launch_bounds__(256) void combine_kernel(MoveArgs a, int shift, int64_t segments) {
   int64_t t, c;
   if (!move_place(a, shift, segments, t, c)) return;
@@ -242,14 +268,17 @@ __global__ __launch_bounds__(256) void combine_kernel(MoveArgs a, int shift, int
   float sum[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
-  for (int j = 0; j < a.K; ++j) {
-    const int64_t r = a.rows[t * a.K + j];
-    if (r < 0 || r >= a.cap) continue;
-    const float w = a.weights != nullptr ? a.weights[t * a.K + j] : 1.0f;
-    float v[8];
-    load8((const T*)a.in + r * a.C + c, n, v);
+  for (int j0 = 0; j0 < a.K; j0 += KB) {
+    const TokenRows<KB> rows(a, t, j0);
+    Raw8<T> v[KB];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum[i] = __builtin_fmaf(w, v[i], sum[i]);
+    for (int j = 0; j < KB; ++j)
+      if (rows.r[j] >= 0) v[j].load((const T*)a.in + rows.r[j] * a.C + c, n);
+#pragma unroll
+    for (int j = 0; j < KB; ++j)
+      if (rows.r[j] >= 0)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] = __builtin_fmaf(rows.w[j], v[j][i], sum[i]);
   }
   if (a.add != nullptr) {
     float v[8];
@@ -257,60 +286,62 @@ __global__ __launch_bounds__(256) void combine_kernel(MoveArgs a, int shift, int
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum[i] += v[i];
   }
-  store8((T*)a.out + t * a.C + c, n, sum);
+  store8((T*)a.out + t * a.C + c, n, sum, a.past);
 }
 
-// A token per wave (W == 1) or per workgroup of W waves; its K dot products in sets of 8.
-template <class T, int W>
+// A token per wave (W == 1) or per workgroup of W waves, KB of its choices at a time; Y: with the dot products, O: with the
+// rows' gradients.
+template <class T, int W, int KB, bool Y, bool O>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void combine_grad_kernel(MoveArgs a) {
-  __shared__ float sums[W][8];
+  __shared__ float sums[W][KB];
   const int lane = threadIdx.x & 63, wave = W == 1 ? 0 : threadIdx.x >> 6;
-  const int64_t t = W == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  const int64_t t = W == 1 ? (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) : blockIdx.x;
   if (t >= a.T) return;
   const T* dout = (const T*)a.in + t * a.C;
-  for (int j0 = 0; j0 < a.K; j0 += 8) {
-    const int nj = a.K - j0 < 8 ? a.K - j0 : 8;
-    float dot[8];
+  for (int j0 = 0; j0 < a.K; j0 += KB) {
+    const TokenRows<KB> rows(a, t, j0);
+    float dot[KB];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dot[j] = 0.0f;
+    for (int j = 0; j < KB; ++j) dot[j] = 0.0f;
     for (int64_t c = 8 * (wave * 64 + lane); c < a.C; c += 512 * W) {
       const int n = a.C - c < 8 ? (int)(a.C - c) : 8;
-      float d[8];
-      load8(dout + c, n, d);
+      Raw8<T> d, y[Y ? KB : 1];
+      d.load(dout + c, n);
+      // (every row of the set is asked for before the first is used, and before any gradient is stored: dy may be y)
+      if constexpr (Y) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (j >= nj) break;
-        const int64_t r = a.rows[t * a.K + j0 + j];
-        if (r < 0 || r >= a.cap) continue;
-        if (a.dweights != nullptr) {
-          float y[8];
-          load8((const T*)a.y + r * a.C + c, n, y);
+        for (int j = 0; j < KB; ++j)
+          if (rows.r[j] >= 0) y[j].load((const T*)a.y + rows.r[j] * a.C + c, n);
+      }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dot[j] = __builtin_fmaf(d[i], y[i], dot[j]);
+      for (int j = 0; j < KB; ++j) {
+        if (rows.r[j] < 0) continue;
+        if constexpr (Y) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot[j] = __builtin_fmaf(d[i], y[j][i], dot[j]);
         }
-        if (a.out != nullptr) {
-          const float w = a.weights != nullptr ? a.weights[t * a.K + j0 + j] : 1.0f;
+        if constexpr (O) {
           float o[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = d[i] * w;
-          store8((T*)a.out + r * a.C + c, n, o);
+          for (int i = 0; i < 8; ++i) o[i] = d[i] * rows.w[j];
+          store8((T*)a.out + rows.r[j] * a.C + c, n, o, a.past);
         }
       }
     }
-    if (a.dweights == nullptr) continue;
+    if constexpr (!Y) continue;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dot[j] = wave_sum(dot[j]);
+    for (int j = 0; j < KB; ++j) dot[j] = wave_sum(dot[j]);
     if constexpr (W == 1) {
       if (lane == 63)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < nj) a.dweights[t * a.K + j0 + j] = dot[j];
+        for (int j = 0; j < KB; ++j)
+          if (j0 + j < a.K) a.dweights[t * a.K + j0 + j] = dot[j];
     } else {
       if (lane == 63)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sums[wave][j] = dot[j];
+        for (int j = 0; j < KB; ++j) sums[wave][j] = dot[j];
       __syncthreads();
-      if ((int)threadIdx.x < nj) {
+      if ((int)threadIdx.x < KB && j0 + (int)threadIdx.x < a.K) {
         float s = 0.0f;
         for (int w = 0; w < W; ++w) s += sums[w][threadIdx.x];
         a.dweights[t * a.K + j0 + threadIdx.x] = s;
@@ -320,11 +351,19 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void combine_grad_kernel(Mov
   }
 }
 
+// f with how many of top_k choices are taken at a time: all of up to 4, sets of 8 above (4 of fp32, to stay within registers).
+template <class F>
+static void for_top_k(int K, bool f32, F f) {
+  if (K <= 2) f(std::integral_constant<int, 2>());
+  else if (K <= 4 || f32) f(std::integral_constant<int, 4>());
+  else f(std::integral_constant<int, 8>());
+}
+
 int launch_dispatch(const void* x, bool f32, int64_t T, int64_t C, const int32_t* rows, int K, const float* weights,
                     void* out, int64_t cap, hipStream_t stream) {
   const MoveShape s = move_shape(T, C);
   if (s.blocks > 0x7fffffff) return BSFP8_ERR_SHAPE;
-  const MoveArgs a{T, C, cap, K, rows, weights, x, nullptr, out, nullptr, nullptr};
+  const MoveArgs a{T, C, cap, K, rows, weights, x, nullptr, out, nullptr, nullptr, move_past(cap, C, f32)};
   const dim3 grid((unsigned)s.blocks), block(256);
   if (f32) hipLaunchKernelGGL(dispatch_kernel<float>, grid, block, 0, stream, a, s.shift, s.segments);
   else hipLaunchKernelGGL(dispatch_kernel<uint16_t>, grid, block, 0, stream, a, s.shift, s.segments);
@@ -335,29 +374,43 @@ int launch_combine(const void* y, bool f32, int64_t cap, int64_t C, const int32_
                    const float* weights, const void* add, void* out, hipStream_t stream) {
   const MoveShape s = move_shape(T, C);
   if (s.blocks > 0x7fffffff) return BSFP8_ERR_SHAPE;
-  const MoveArgs a{T, C, cap, K, rows, weights, y, add, out, nullptr, nullptr};
+  const MoveArgs a{T, C, cap, K, rows, weights, y, add, out, nullptr, nullptr, move_past(T, C, f32)};
   const dim3 grid((unsigned)s.blocks), block(256);
-  if (f32) hipLaunchKernelGGL(combine_kernel<float>, grid, block, 0, stream, a, s.shift, s.segments);
-  else hipLaunchKernelGGL(combine_kernel<uint16_t>, grid, block, 0, stream, a, s.shift, s.segments);
+  for_top_k(K, f32, [&](auto kb) {
+    constexpr int KB = decltype(kb)::value;
+    if (f32) hipLaunchKernelGGL((combine_kernel<float, KB>), grid, block, 0, stream, a, s.shift, s.segments);
+    else hipLaunchKernelGGL((combine_kernel<uint16_t, KB>), grid, block, 0, stream, a, s.shift, s.segments);
+  });
   return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
 }
 
 int launch_combine_grad(const void* dout, bool f32, int64_t T, int64_t C, const void* y, int64_t cap,
                         const int32_t* rows, int K, const float* weights, void* dy, float* dweights,
                         hipStream_t stream) {
-  const MoveArgs a{T, C, cap, K, rows, weights, dout, nullptr, dy, y, dweights};
+  const MoveArgs a{T, C, cap, K, rows, weights, dout, nullptr, dy, y, dweights, move_past(cap, C, f32)};
   // a token per wave where they fill the chip by themselves
   const bool wave = T >= 4096 || C <= 512;
   const int64_t blocks = wave ? (T + 3) / 4 : T;
   if (blocks > 0x7fffffff) return BSFP8_ERR_SHAPE;
   const dim3 grid((unsigned)blocks);
-  if (wave) {
-    if (f32) hipLaunchKernelGGL((combine_grad_kernel<float, 1>), grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((combine_grad_kernel<uint16_t, 1>), grid, dim3(256), 0, stream, a);
-  } else {
-    if (f32) hipLaunchKernelGGL((combine_grad_kernel<float, 8>), grid, dim3(512), 0, stream, a);
-    else hipLaunchKernelGGL((combine_grad_kernel<uint16_t, 8>), grid, dim3(512), 0, stream, a);
-  }
+  auto go = [&](auto kb, auto y, auto o) {
+    constexpr int KB = decltype(kb)::value;
+    constexpr bool Y = decltype(y)::value, O = decltype(o)::value;
+    if (wave) {
+      if (f32) hipLaunchKernelGGL((combine_grad_kernel<float, 1, KB, Y, O>), grid, dim3(256), 0, stream, a);
+      else hipLaunchKernelGGL((combine_grad_kernel<uint16_t, 1, KB, Y, O>), grid, dim3(256), 0, stream, a);
+    } else {
+      if (f32) hipLaunchKernelGGL((combine_grad_kernel<float, 8, KB, Y, O>), grid, dim3(512), 0, stream, a);
+      else hipLaunchKernelGGL((combine_grad_kernel<uint16_t, 8, KB, Y, O>), grid, dim3(512), 0, stream, a);
+    }
+  };
+  const std::integral_constant<bool, true> yes;
+  const std::integral_constant<bool, false> no;
+  for_top_k(K, f32, [&](auto kb) {
+    if (dweights != nullptr && dy != nullptr) go(kb, yes, yes);
+    else if (dweights != nullptr) go(kb, yes, no);
+    else go(kb, no, yes);
+  });
   return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
 }
 
