@@ -865,6 +865,13 @@ def _arg(t, what, dtypes, shape=None):
     return p
 
 
+def _here():
+    """What the native calls below begin with: the current device and its stream."""
+    if _raw_device is None:
+        return torch.cuda.current_device(), _stream(None)
+    return _raw_device(), _stream(None)
+
+
 def _matrix(t, what, dtypes):
     """Pointer and shape of a [rows, cols] tensor, which has to be given."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
@@ -894,6 +901,14 @@ def route_topk(logits, top_k, scoring=ROUTE_SOFTMAX, bias=None, renormalize=True
     if _elsewhere(stream):
         with _on(stream):
             return route_topk(logits, top_k, scoring, bias, renormalize, scale, probs, experts, score_sum, workspace)
+    if _use_native():
+        got = _native.route_topk(*_here(), logits, top_k, scoring, bias, renormalize, scale, probs, experts, score_sum,
+                                 workspace)
+        if _native_done(got, "route_topk"):
+            out = {"probs": got[0], "experts": got[1]}
+            if score_sum is not None:
+                out["score_sum"] = score_sum
+            return out
     pl, (T, E) = _matrix(logits, "logits", _STREAM)
     pb, ps = _arg(bias, "bias", _F32, (E,)), _arg(score_sum, "score_sum", _F32, (E,))
     if probs is None:
@@ -919,6 +934,10 @@ def route_topk_grad(dprobs, logits, experts, scoring=ROUTE_SOFTMAX, renormalize=
     if _elsewhere(stream):
         with _on(stream):
             return route_topk_grad(dprobs, logits, experts, scoring, renormalize, scale, dscore_sum, dlogits)
+    if _use_native():
+        got = _native.route_topk_grad(*_here(), dprobs, logits, experts, scoring, renormalize, scale, dscore_sum, dlogits)
+        if _native_done(got, "route_topk_grad"):
+            return got[0]
     pl, (T, E) = _matrix(logits, "logits", _STREAM)
     pe, (_, K) = _matrix(experts, "experts", _I32)
     _like(experts, (T, K), "experts")
@@ -945,10 +964,18 @@ def dispatch_plan(experts, num_experts, probs=None, out=None, workspace=None, st
     if _elsewhere(stream):
         with _on(stream):
             return dispatch_plan(experts, num_experts, probs, out, workspace)
+    given = out or {}
+    if _use_native():
+        got = _native.dispatch_plan(*_here(), experts, num_experts, probs, given.get("splits"), given.get("rows"),
+                                    given.get("choices"), None if probs is None else given.get("probs"), workspace)
+        if _native_done(got, "dispatch_plan"):
+            out = {"splits": got[0], "rows": got[1], "choices": got[2]}
+            if probs is not None:
+                out["probs"] = got[3]
+            return out
     pe, (T, K) = _matrix(experts, "experts", _I32)
     pp, N = _arg(probs, "probs", _F32, (T, K)), T * K
-    given, out = out or {}, {}
-    ptrs = []
+    ptrs, out = [], {}
     for name, shape, dtype in (("splits", (num_experts,), torch.int32), ("rows", (T, K), torch.int32),
                                ("choices", (N,), torch.int32), ("probs", (N,), torch.float32)):
         if name == "probs" and probs is None:
@@ -977,6 +1004,10 @@ def dispatch(x, plan, weights=None, out=None, stream=None):
     if _elsewhere(stream):
         with _on(stream):
             return dispatch(x, plan, weights, out)
+    if _use_native():
+        got = _native.dispatch(*_here(), x, plan["rows"], weights, out)
+        if _native_done(got, "dispatch"):
+            return got[0]
     pr, T, K, N = _plan_rows(plan)
     px, (_, C) = _matrix(x, "x", _STREAM)
     _like(x, (T, C), "x")
@@ -995,6 +1026,10 @@ def dispatch_quantize(x, plan, recipe, which, out, weights=None, status=None, st
     if _elsewhere(stream):
         with _on(stream):
             return dispatch_quantize(x, plan, recipe, which, out, weights, status)
+    if _use_native() and _native_done(_native.dispatch_quantize(
+            *_here(), x, plan["rows"], plan["choices"], plan["splits"], recipe, which, out.get("row_q"), out.get("row_s"),
+            out.get("col_q"), out.get("col_s"), weights, status), "dispatch_quantize"):
+        return out
     _, T, K, N = _plan_rows(plan)
     px, (_, C) = _matrix(x, "x", _BF16)
     _like(x, (T, C), "x")
@@ -1015,6 +1050,10 @@ def combine(y, plan, weights=None, add=None, out=None, stream=None):
     if _elsewhere(stream):
         with _on(stream):
             return combine(y, plan, weights, add, out)
+    if _use_native():
+        got = _native.combine(*_here(), y, plan["rows"], weights, add, out)
+        if _native_done(got, "combine"):
+            return got[0]
     pr, T, K, N = _plan_rows(plan)
     py, (_, C) = _matrix(y, "y", _STREAM)
     _like(y, (N, C), "y")
@@ -1034,6 +1073,14 @@ def combine_grad(dout, plan, y=None, weights=None, dy=None, dweights=None, strea
     if _elsewhere(stream):
         with _on(stream):
             return combine_grad(dout, plan, y, weights, dy, dweights)
+    if _use_native():
+        got = _native.combine_grad(*_here(), dout, plan["rows"], y, weights, None if dy is False else dy, dy is not False,
+                                   dweights)
+        if _native_done(got, "combine_grad"):
+            out = {"dy": got[0]} if got[0] is not None else {}
+            if got[1] is not None:
+                out["dweights"] = got[1]
+            return out
     pr, T, K, N = _plan_rows(plan)
     pd, (_, C) = _matrix(dout, "dout", _STREAM)
     _like(dout, (T, C), "dout")
@@ -1064,6 +1111,13 @@ def grouped_act_checkpoint(activation, h, split_sizes, recipe, which, out, kept,
     """bsfp8_grouped_act_checkpoint: as grouped_act_quantize with ACT_SRELU (h [R, C] bf16) or ACT_SWIGLU (h [R, 2F]), and
     in the same pass h itself in 8 bits into ``kept`` (alloc_quantized for h's shape, RECIPE_MX, ROWWISE), which is what
     grouped_act_checkpoint_grad needs of it."""
+    if _elsewhere(stream):
+        with _on(stream):
+            return grouped_act_checkpoint(activation, h, split_sizes, recipe, which, out, kept, probs, status)
+    if _use_native() and _native_done(_native.act_checkpoint(
+            *_here(), activation, h, probs, split_sizes, recipe, which, out.get("row_q"), out.get("row_s"), out.get("col_q"),
+            out.get("col_s"), kept.get("row_q"), kept.get("row_s"), status), "grouped_act_checkpoint"):
+        return out
     ph, (R, wide) = _matrix(h, "h", _BF16)
     if activation == ACT_SWIGLU and wide % 2:
         raise ValueError("grouped_act_checkpoint: a GLU input has an even number of columns")
@@ -1090,14 +1144,19 @@ def grouped_act_checkpoint_grad(activation, kept, dy, split_sizes, recipe, which
     ACT_SRELU, [R, 2F] with ACT_SWIGLU).  y: a dict with col_q and col_s (alloc_quantized for [R, F], COLWISE) that
     receives the activation again, for the second projection's weight gradient.  dprobs: fp32 [R], receives the
     gradient of the probabilities.  Returns a dict of out's tensors, y and dprobs, where given."""
-    if dprobs is not None and workspace is None and _elsewhere(stream):
+    if _elsewhere(stream):
         with _on(stream):
             return grouped_act_checkpoint_grad(activation, kept, dy, split_sizes, recipe, which, out, probs, y, dprobs,
-                                               None, status)
+                                               workspace, status)
+    out, q = dict(out or {}), y or {}
+    if _use_native() and _native_done(_native.act_checkpoint_grad(
+            *_here(), activation, kept.get("row_q"), kept.get("row_s"), dy, probs, split_sizes, recipe, which,
+            out.get("row_q"), out.get("row_s"), out.get("col_q"), out.get("col_s"), q.get("col_q"), q.get("col_s"), dprobs,
+            workspace, status), "grouped_act_checkpoint_grad"):
+        return _glu_result(out, y=y, dprobs=dprobs)
     pd, (R, F) = _matrix(dy, "dy", _BF16)
     wide = 2 * F if activation == ACT_SWIGLU else F
     E = int(split_sizes.numel())
-    out, q = dict(out or {}), y or {}
     args = (activation, _quant(kept, "row_q", "kept"), _quant(kept, "row_s", "kept"), _arg(probs, "probs", _F32, (R,)), pd,
             R, F, _arg(split_sizes, "split_sizes", _I32), E, recipe, which, _quant(out, "row_q", "out"),
             _quant(out, "row_s", "out"), _quant(out, "col_q", "out"), _quant(out, "col_s", "out"),
@@ -1111,7 +1170,4 @@ def grouped_act_checkpoint_grad(activation, kept, dy, split_sizes, recipe, which
     rc = lib().bsfp8_grouped_act_checkpoint_grad(*args, _ptr(workspace) if dprobs is not None else None,
                                                  _dev(status, "status", _I32), _stream(stream))
     _check(rc, "grouped_act_checkpoint_grad")
-    for name, value in (("y", y), ("dprobs", dprobs)):
-        if value is not None:
-            out[name] = value
-    return out
+    return _glu_result(out, y=y, dprobs=dprobs)

@@ -23,6 +23,7 @@ namespace bsfp8 {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / 64;
+constexpr int kPlanSteps = kPlanUnit / kPlanThreads;  // choices a thread takes at a time
 
 struct PlanArgs {
   const int32_t* experts;
@@ -41,9 +42,19 @@ __device__ __forceinline__ int plan_bin(int32_t e, int E) { return e < 0 || e >=
 __global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(PlanArgs a) {
   __shared__ int32_t count[kMaxGroups + 1];
   for (int b = threadIdx.x; b <= a.E; b += kPlanThreads) count[b] = 0;
-  __syncthreads();
   const int64_t begin = a.chunk * blockIdx.x, end = begin + a.chunk < a.N ? begin + a.chunk : a.N;
-  for (int64_t c = begin + threadIdx.x; c < end; c += kPlanThreads) atomicAdd(&count[plan_bin(a.experts[c], a.E)], 1);
+  int32_t e[kPlanSteps];
+  for (int64_t c0 = begin; c0 < end; c0 += kPlanUnit) {
+#pragma unroll
+    for (int i = 0; i < kPlanSteps; ++i) {
+      const int64_t c = c0 + i * kPlanThreads + threadIdx.x;
+      e[i] = c < end ? a.experts[c] : -1;
+    }
+    if (c0 == begin) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPlanSteps; ++i)
+      if (c0 + i * kPlanThreads + threadIdx.x < end) atomicAdd(&count[plan_bin(e[i], a.E)], 1);
+  }
   __syncthreads();
   for (int b = threadIdx.x; b <= a.E; b += kPlanThreads) a.hist[(int64_t)blockIdx.x * (a.E + 1) + b] = count[b];
 }
@@ -70,71 +81,102 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanArgs a) {
   __shared__ int32_t at[kPlanWaves * (kMaxGroups + 1)];
   __shared__ int32_t total[kMaxGroups + 1], before[kMaxGroups + 1], wave_total[kPlanWaves];
   const int bins = a.E + 1, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  // a wave's part of the chunk, kPlanSteps times 64 choices at a time; all of it stays in registers where that is the part
+  const int64_t part = a.chunk / kPlanWaves, begin = a.chunk * blockIdx.x + part * wave;
+  const int64_t end = begin + part < a.N ? begin + part : a.N;
+  int32_t bin[kPlanSteps];
+  auto load = [&](int64_t c0) {
+#pragma unroll
+    for (int i = 0; i < kPlanSteps; ++i) {
+      const int64_t c = c0 + 64 * i + lane;
+      bin[i] = c < end ? plan_bin(a.experts[c], a.E) : bins;  // (a bin of their own for the lanes past the end)
+    }
+  };
+  load(begin);
   for (int i = threadIdx.x; i < kPlanWaves * bins; i += kPlanThreads) at[i] = 0;
   for (int b = threadIdx.x; b < bins; b += kPlanThreads) total[b] = before[b] = 0;
   __syncthreads();
-  const int64_t begin = a.chunk * blockIdx.x + a.chunk / kPlanWaves * wave;
-  const int64_t stop = begin + a.chunk / kPlanWaves, end = stop < a.N ? stop : a.N;
-  for (int64_t c = begin + lane; c < end; c += 64) atomicAdd(&at[wave * bins + plan_bin(a.experts[c], a.E)], 1);
+  for (int64_t c0 = begin; c0 < end; c0 += 64 * kPlanSteps) {
+    if (c0 != begin) load(c0);
+#pragma unroll
+    for (int i = 0; i < kPlanSteps; ++i)
+      if (bin[i] < bins) atomicAdd(&at[wave * bins + bin[i]], 1);
+  }
   if (a.hist != nullptr) {
+    // the other chunks' counts, every 16th a wave's; 8 loads in flight
     for (int b = lane; b < bins; b += 64) {
       int32_t all = 0, mine = 0;
-      for (int c = wave; c < a.chunks; c += kPlanWaves) {
-        const int32_t n = a.hist[(int64_t)c * bins + b];
-        all += n;
-        mine += c < (int)blockIdx.x ? n : 0;
+      for (int c0 = wave; c0 < a.chunks; c0 += 8 * kPlanWaves) {
+        int32_t n[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int c = c0 + u * kPlanWaves;
+          n[u] = c < a.chunks ? a.hist[(int64_t)c * bins + b] : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          all += n[u];
+          mine += c0 + u * kPlanWaves < (int)blockIdx.x ? n[u] : 0;
+        }
       }
       atomicAdd(&total[b], all);  // (whole numbers: the order does not matter)
       atomicAdd(&before[b], mine);
     }
   }
   __syncthreads();
-  if (a.hist == nullptr)
-    for (int b = threadIdx.x; b < bins; b += kPlanThreads)
-      for (int w = 0; w < kPlanWaves; ++w) total[b] += at[w * bins + b];
-  if (a.hist == nullptr) __syncthreads();
-  // at most two bins a thread: consecutive ones, so that one prefix over the threads serves them
+  // a bin's counts of the 16 waves, before each
+  for (int b = threadIdx.x; b < bins; b += kPlanThreads) {
+    int32_t n[kPlanWaves], sum = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanWaves; ++w) n[w] = at[w * bins + b];
+#pragma unroll
+    for (int w = 0; w < kPlanWaves; ++w) {
+      at[w * bins + b] = sum;
+      sum += n[w];
+    }
+    if (a.hist == nullptr) total[b] = sum;
+  }
+  __syncthreads();
+  // where the bins begin: at most two bins a thread, consecutive ones, so that one prefix over the threads serves them
   const int b0 = 2 * threadIdx.x;
   const int32_t n0 = b0 < bins ? total[b0] : 0, n1 = b0 + 1 < bins ? total[b0 + 1] : 0;
   const int32_t first = plan_scan(n0 + n1, wave_total);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int b = b0 + i;
-    if (b < bins) {
-      if (blockIdx.x == 0 && b < a.E) a.splits[b] = i ? n1 : n0;
-      int32_t next = first + (i ? n0 : 0) + before[b];
-      for (int w = 0; w < kPlanWaves; ++w) {
-        const int32_t n = at[w * bins + b];
-        at[w * bins + b] = next;
-        next += n;
-      }
-    }
+    if (b >= bins) break;
+    if (blockIdx.x == 0 && b < a.E) a.splits[b] = i ? n1 : n0;
+    before[b] += first + (i ? n0 : 0);
   }
   __syncthreads();
   int32_t* next = at + wave * bins;
   const uint64_t below = (uint64_t(1) << lane) - 1;
-  for (int64_t c0 = begin; c0 < end; c0 += 64) {
-    const int64_t c = c0 + lane;
-    const bool live = c < end;
-    const int b = live ? plan_bin(a.experts[c], a.E) : bins;  // (a bin of their own for the lanes past the end)
-    // the lanes of the same bin
-    uint64_t same = ~uint64_t(0);
-    for (int bit = 0; (bins >> bit) != 0; ++bit) {
-      const bool set = (b >> bit) & 1;
-      const uint64_t m = __ballot(set);
-      same &= set ? m : ~m;
-    }
-    const int rank = __popcll(same & below);
-    if (live) {
-      const int32_t row = next[b] + rank;
+  const int bits = 32 - __builtin_clz(bins);
+  for (int64_t c0 = begin; c0 < end; c0 += 64 * kPlanSteps) {
+    if (part > 64 * kPlanSteps) load(c0);
+#pragma unroll
+    for (int i = 0; i < kPlanSteps; ++i) {
+      const int64_t c = c0 + 64 * i + lane;
+      const int b = bin[i];
+      // the lanes of the same bin
+      uint64_t same = ~uint64_t(0);
+      for (int bit = 0; bit < bits; ++bit) {
+        const bool set = (b >> bit) & 1;
+        const uint64_t m = __ballot(set);
+        same &= set ? m : ~m;
+      }
+      const int rank = __popcll(same & below);
+      if (b < bins) {
+        const int32_t mine = next[b], row = before[b] + mine + rank;
+        __builtin_amdgcn_wave_barrier();
+        if (rank == 0) next[b] = mine + __popcll(same);  // (a wave's LDS accesses are done in order)
+        const bool dropped = b == a.E;
+        a.rows[c] = dropped ? -1 : row;
+        a.choices[row] = dropped ? -1 : (int32_t)c;
+        if (a.row_probs != nullptr) a.row_probs[row] = dropped ? 0.0f : a.probs[c];
+      }
       __builtin_amdgcn_wave_barrier();
-      if (rank == 0) next[b] = row + __popcll(same);  // (a wave's LDS accesses are done in order)
-      const bool dropped = b == a.E;
-      a.rows[c] = dropped ? -1 : row;
-      a.choices[row] = dropped ? -1 : (int32_t)c;
-      if (a.row_probs != nullptr) a.row_probs[row] = dropped ? 0.0f : a.probs[c];
     }
-    __builtin_amdgcn_wave_barrier();
   }
 }
 
