@@ -574,7 +574,7 @@ int bsfp8_route_topk_grad(const float* dprobs, const void* logits, int logits_dt
 size_t bsfp8_dispatch_plan_workspace_bytes(int64_t tokens, int32_t top_k, int32_t num_experts) {
   if (!valid_groups(num_experts) || !valid_route(tokens, num_experts, top_k)) return 0;
   const int64_t chunks = bsfp8::plan_chunks(tokens * top_k);
-  return chunks > 1 ? (size_t)chunks * (size_t)(num_experts + 1) * sizeof(int32_t) : 0;
+  return chunks > 1 ? (size_t)chunks * (size_t)bsfp8::plan_hist_row(num_experts) * sizeof(int32_t) : 0;
 }
 
 int bsfp8_dispatch_plan(const int32_t* experts, const float* probs, int64_t tokens, int32_t top_k, int32_t num_experts,

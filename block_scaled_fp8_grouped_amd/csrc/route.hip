@@ -78,6 +78,16 @@ __device__ __forceinline__ float sigmoid_stated(float l, float* other = nullptr)
   return s;
 }
 
+// exp(x) for x <= 0 from the hardware's 2^x: the product's rounding is an error of |x| 2^-24 of the result, which below 2^-126 is 0.
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+
+// Orders a wave's LDS accesses before its own later ones (no other wave is involved).
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // V values of a row from e0 on; past its end: -infinity.
 template <int V, class T>
 __device__ __forceinline__ void load_logits(const T* row, int e0, int E, float (&l)[V]) {
@@ -113,7 +123,7 @@ __device__ __forceinline__ void scores_of(const float (&l)[V], int sigmoid, floa
   float sum = 0.0f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    s[v] = expf(l[v] - m);
+    s[v] = exp_fast(l[v] - m);
     sum += s[v];
   }
   sum = sum_over<G>(sum);
@@ -157,6 +167,7 @@ template <class T, int G, int V>
 __global__ __launch_bounds__(256) void route_topk_kernel(RouteArgs a) {
   constexpr int P = kPerLane<G>;
   __shared__ float sums[256 / G][G * V + 1];
+  __shared__ int taken[256 / G][BSFP8_MAX_TOP_K];
   const int lane = threadIdx.x & (G - 1), group = threadIdx.x / G, e0 = lane * V;
   float total[V];
 #pragma unroll
@@ -168,7 +179,7 @@ __global__ __launch_bounds__(256) void route_topk_kernel(RouteArgs a) {
     const T* row = (const T*)a.logits + t * a.E;
     float l[V], s[V];
     load_logits<V>(row, e0, a.E, l);
-    if (a.sigmoid || a.partial != nullptr || !a.renormalize) scores_of<G, V>(l, a.sigmoid, s);
+    if (a.sigmoid || a.partial != nullptr) scores_of<G, V>(l, a.sigmoid, s);
     if (a.partial != nullptr && live) {
 #pragma unroll
       for (int v = 0; v < V; ++v) total[v] += e0 + v < a.E ? s[v] : 0.0f;
@@ -180,24 +191,46 @@ __global__ __launch_bounds__(256) void route_topk_kernel(RouteArgs a) {
       if (a.bias != nullptr && e0 + v < a.E) key += a.bias[e0 + v];
       u[v] = l[v] == -INFINITY || key == -INFINITY ? 0u : ordered(key);
     }
-    int mine[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) mine[i] = -1;
+    for (int i = 0; i < P; ++i)
+      if (lane + i * G < a.K) taken[group][lane + i * G] = -1;
     for (int j = 0; j < a.K; ++j) {
       uint32_t best = u[0];
 #pragma unroll
       for (int v = 1; v < V; ++v) best = u[v] > best ? u[v] : best;
       best = max_over<G>(best);
-      uint32_t at = 0xffffffffu;
+      const bool open_ = best != 0u;
+      const uint32_t key = open_ ? best : 0xfffffffeu;  // (a number that no key has)
+      // one of a token's keys is the largest, unless two are equal: then the lowest expert's is taken
+      int found = 0, at = 0;
+      uint64_t lanes = 0;
 #pragma unroll
-      for (int v = V - 1; v >= 0; --v) at = u[v] == best ? (uint32_t)(e0 + v) : at;
-      at = min_over<G>(at);
+      for (int v = 0; v < V; ++v) {
+        const bool equal = u[v] == key;
+        const uint64_t m = __ballot(equal);
+        found += __popcll(m);
+        lanes |= m;
+        at = equal ? v : at;
+      }
+      if (found * G == __popcll(__ballot(open_))) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) u[v] = at == (uint32_t)(e0 + v) ? 0u : u[v];
+        for (int v = 0; v < V; ++v) u[v] = u[v] == key ? 0u : u[v];
+        if (lanes >> (threadIdx.x & 63) & 1) taken[group][j] = e0 + at;
+      } else {
+        uint32_t e = 0xffffffffu;
 #pragma unroll
-      for (int i = 0; i < P; ++i)
-        if (j == lane + i * G) mine[i] = best == 0u ? -1 : (int)at;
+        for (int v = V - 1; v >= 0; --v) e = u[v] == key ? (uint32_t)(e0 + v) : e;
+        e = min_over<G>(e);
+#pragma unroll
+        for (int v = 0; v < V; ++v) u[v] = e == (uint32_t)(e0 + v) ? 0u : u[v];
+        if (lane == 0 && open_) taken[group][j] = (int)e;
+      }
     }
+    wave_order();
+    int mine[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) mine[i] = lane + i * G < a.K ? taken[group][lane + i * G] : -1;
+    wave_order();
     float p[P], other[P];
     if (a.renormalize) {
       chosen_scores<G>(row, mine, a.sigmoid, p, other);
@@ -210,13 +243,13 @@ __global__ __launch_bounds__(256) void route_topk_kernel(RouteArgs a) {
         m = fmax_over<G>(m);
         if (m == -INFINITY) m = 0.0f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) sum += expf(l[v] - m);
+        for (int v = 0; v < V; ++v) sum += exp_fast(l[v] - m);
         sum = sum_over<G>(sum);
       }
 #pragma unroll
       for (int i = 0; i < P; ++i) {
         const float x = mine[i] >= 0 ? to_f32(row[mine[i]]) : -INFINITY;
-        p[i] = mine[i] < 0 ? 0.0f : a.sigmoid ? sigmoid_stated(x) : expf(x - m) * (1.0f / sum);
+        p[i] = mine[i] < 0 ? 0.0f : a.sigmoid ? sigmoid_stated(x) : exp_fast(x - m) * (1.0f / sum);
       }
     }
 #pragma unroll
@@ -240,17 +273,28 @@ __global__ __launch_bounds__(256) void route_topk_kernel(RouteArgs a) {
   }
 }
 
-// The partial sums of 64 experts added in the order of the workgroups: 16 waves each every 16th, then the waves'.
+// The partial sums of 16 experts added in a fixed order: a workgroup's 64 rows of 16 lanes have every 64th each, 8 loads in
+// flight; then the 4 rows of a wave, then the waves.
 __global__ __launch_bounds__(1024) void route_sum_kernel(const float* partial, int blocks, int E, float* out) {
-  __shared__ float sums[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e = blockIdx.x * 64 + lane;
+  __shared__ float sums[16][16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e = blockIdx.x * 16 + (lane & 15);
   float s = 0.0f;
-  if (e < E)
-    for (int b = wave; b < blocks; b += 16) s += partial[(int64_t)b * E + e];
-  sums[wave][lane] = s;
+  if (e < E) {
+    for (int b0 = wave * 4 + (lane >> 4); b0 < blocks; b0 += 8 * 64) {
+      float n[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) n[u] = b0 + 64 * u < blocks ? partial[(int64_t)(b0 + 64 * u) * E + e] : 0.0f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += n[u];
+    }
+  }
+  s += __shfl_xor(s, 16, 64);
+  s += __shfl_xor(s, 32, 64);
+  if (lane < 16) sums[wave][lane] = s;
   __syncthreads();
-  if (wave == 0 && e < E) {
-    for (int w = 1; w < 16; ++w) s += sums[w][lane];
+  if (threadIdx.x < 16 && e < E) {
+    s = 0.0f;
+    for (int w = 0; w < 16; ++w) s += sums[w][lane];
     out[e] = s;
   }
 }
@@ -261,6 +305,7 @@ __global__ __launch_bounds__(256) void route_topk_grad_kernel(RouteArgs a) {
   constexpr int P = kPerLane<G>;
   __shared__ int at_sm[256 / G][BSFP8_MAX_TOP_K];
   __shared__ float part_sm[256 / G][BSFP8_MAX_TOP_K];
+  __shared__ __attribute__((aligned(16))) float row_sm[256 / G][G * V];
   const int lane = threadIdx.x & (G - 1), group = threadIdx.x / G, e0 = lane * V;
   for (int64_t t0 = (int64_t)blockIdx.x * (256 / G); t0 < a.T; t0 += (int64_t)gridDim.x * (256 / G)) {
     const bool live = t0 + group < a.T;
@@ -299,27 +344,49 @@ __global__ __launch_bounds__(256) void route_topk_grad_kernel(RouteArgs a) {
         g[i] = x == -INFINITY ? 0.0f : g[i] * sc * rest;
       }
     }
-    // the choices, seen by all lanes of the token (a wave's LDS accesses are done in order)
+    // the choices' parts at their experts' places.  Each choice writes its number there first: one that finds another's
+    // shares its expert, and the parts are then added choice by choice, in order
+    float d[V];
+    float* to = &row_sm[group][e0];
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int j = lane + i * G;
-      if (j < a.K) {
-        at_sm[group][j] = e[i];
-        part_sm[group][j] = g[i];
+    for (int v = 0; v < V; ++v) to[v] = 0.0f;
+    wave_order();
+    bool alone = true;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (e[i] >= 0) row_sm[group][e[i]] = __int_as_float(lane + i * G);
+    wave_order();
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (e[i] >= 0) alone &= __float_as_int(row_sm[group][e[i]]) == lane + i * G;
+    wave_order();
+    if (__ballot(!alone) == 0) {
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (e[i] >= 0) row_sm[group][e[i]] = g[i];
+      wave_order();
+#pragma unroll
+      for (int v = 0; v < V; ++v) d[v] = to[v];
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const int j = lane + i * G;
+        if (j < a.K) {
+          at_sm[group][j] = e[i];
+          part_sm[group][j] = g[i];
+        }
+      }
+      wave_order();
+#pragma unroll
+      for (int v = 0; v < V; ++v) d[v] = 0.0f;
+      for (int j = 0; j < a.K; ++j) {
+        const int x = at_sm[group][j] - e0;
+        const float y = part_sm[group][j];
+#pragma unroll
+        for (int v = 0; v < V; ++v) d[v] += x == v ? y : 0.0f;
       }
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    float d[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) d[v] = 0.0f;
-    for (int j = 0; j < a.K; ++j) {
-      const int x = at_sm[group][j] - e0;
-      const float y = part_sm[group][j];
-#pragma unroll
-      for (int v = 0; v < V; ++v) d[v] += x == v ? y : 0.0f;
-    }
+    wave_order();
     if constexpr (FULL) {
       float back[V], mean = 0.0f;
 #pragma unroll
@@ -353,8 +420,6 @@ __global__ __launch_bounds__(256) void route_topk_grad_kernel(RouteArgs a) {
           if (e0 + v < a.E) out[v] = o[v];
       }
     }
-    // (the next token's choices are written after this one's were read: the same wave's accesses stay in order)
-    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -389,7 +454,7 @@ int launch_route_topk(const void* logits, bool f32, int64_t T, int E, int K, boo
     if (hipGetLastError() != hipSuccess) return BSFP8_ERR_LAUNCH;
   }
   if (score_sum == nullptr) return BSFP8_OK;
-  hipLaunchKernelGGL(route_sum_kernel, dim3((unsigned)((E + 63) / 64)), dim3(1024), 0, stream, workspace, (int)blocks, E,
+  hipLaunchKernelGGL(route_sum_kernel, dim3((unsigned)((E + 15) / 16)), dim3(1024), 0, stream, workspace, (int)blocks, E,
                      score_sum);
   return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
 }

@@ -23,4 +23,10 @@ inline int64_t plan_chunks(int64_t choices) {
   return choices == 0 ? 0 : (choices + plan_chunk(choices) - 1) / plan_chunk(choices);
 }
 
+// Counts of a chunk in the workspace: one per expert and one of the dropped choices, in whole vectors of 4.
+#if defined(__HIPCC__)
+__host__ __device__
+#endif
+constexpr int plan_hist_row(int experts) { return (experts + 4) / 4 * 4; }
+
 }  // namespace bsfp8
