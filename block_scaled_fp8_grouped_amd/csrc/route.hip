@@ -21,7 +21,7 @@ struct RouteArgs {
   int64_t T;
   int E, K;
   const float* bias;
-  int sigmoid, renormalize;
+  int renormalize;
   float scale;
   float* probs;        // forward out; gradient: dprobs in
   int32_t* experts;
@@ -64,7 +64,9 @@ __device__ __forceinline__ float fmax_over(float v) {
   }));
 }
 
-// A key as an unsigned number of the same order: 0 below every number, +0 where it was -0, NaN above all.
+// A key as an unsigned number of the same order: +0 where it was -0, NaN above all; -infinity, the key of the masked, is
+// kMasked and the lowest, so that 0 stands for the taken.
+constexpr uint32_t kMasked = 0x007fffffu;
 __device__ __forceinline__ uint32_t ordered(float key) {
   const uint32_t b = __float_as_uint(key + 0.0f);
   return key != key ? 0xffffffffu : b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
@@ -103,9 +105,9 @@ __device__ __forceinline__ void load_logits(const T* row, int e0, int E, float (
 }
 
 // The scores of a token's V logits a lane: s, and for the sigmoid 1 - s (FULL gradients).
-template <int G, int V>
-__device__ __forceinline__ void scores_of(const float (&l)[V], int sigmoid, float (&s)[V], float* other = nullptr) {
-  if (sigmoid) {
+template <int G, int V, bool SIGMOID>
+__device__ __forceinline__ void scores_of(const float (&l)[V], float (&s)[V], float* other = nullptr) {
+  if constexpr (SIGMOID) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float o;
@@ -127,45 +129,36 @@ __device__ __forceinline__ void scores_of(const float (&l)[V], int sigmoid, floa
     sum += s[v];
   }
   sum = sum_over<G>(sum);
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const float inv = sum == 0.0f ? 0.0f : recip_rn(sum);  // (the largest counts 1 in it)
 #pragma unroll
   for (int v = 0; v < V; ++v) s[v] *= inv;
 }
 
-// A lane's choices j = lane, lane + G, ... of a token: up to kMaxPerLane.
-template <int G>
-constexpr int kPerLane = (BSFP8_MAX_TOP_K + G - 1) / G;
-
-// The scores of the chosen over what they are divided by: ph, and for the sigmoid 1 - s.
-template <int G, class T>
-__device__ __forceinline__ void chosen_scores(const T* row, const int (&e)[kPerLane<G>], int sigmoid,
-                                              float (&ph)[kPerLane<G>], float (&other)[kPerLane<G>]) {
-  constexpr int P = kPerLane<G>;
-  float l[P], m = -INFINITY, sum = 0.0f;
+// The scores of a lane's P chosen over what they are divided by: ph, and for the sigmoid 1 - s.
+template <int G, int P, bool SIGMOID>
+__device__ __forceinline__ void chosen_scores(const float (&l)[P], const int (&e)[P], float (&ph)[P], float (&other)[P]) {
+  float m = -INFINITY, sum = 0.0f;
+  if constexpr (!SIGMOID) {
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    l[i] = e[i] >= 0 ? to_f32(row[e[i]]) : -INFINITY;
-    m = fmaxf(m, l[i]);
-  }
-  if (!sigmoid) {
+    for (int i = 0; i < P; ++i) m = fmaxf(m, l[i]);
     m = fmax_over<G>(m);
     if (m == -INFINITY) m = 0.0f;
   }
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    ph[i] = sigmoid ? sigmoid_stated(l[i], &other[i]) : expf(l[i] - m);
+    ph[i] = SIGMOID ? sigmoid_stated(l[i], &other[i]) : expf(l[i] - m);
     if (e[i] < 0 || l[i] == -INFINITY) ph[i] = 0.0f;
     sum += ph[i];
   }
   sum = sum_over<G>(sum);
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const float inv = sum == 0.0f ? 0.0f : SIGMOID ? 1.0f / sum : recip_rn(sum);
 #pragma unroll
   for (int i = 0; i < P; ++i) ph[i] *= inv;
 }
 
-template <class T, int G, int V>
+// P: a lane's choices j = lane, lane + G, ... of a token.
+template <class T, int G, int V, int P, bool SIGMOID>
 __global__ __launch_bounds__(256) void route_topk_kernel(RouteArgs a) {
-  constexpr int P = kPerLane<G>;
   __shared__ float sums[256 / G][G * V + 1];
   __shared__ int taken[256 / G][BSFP8_MAX_TOP_K];
   const int lane = threadIdx.x & (G - 1), group = threadIdx.x / G, e0 = lane * V;
@@ -179,17 +172,18 @@ __global__ __launch_bounds__(256) void route_topk_kernel(RouteArgs a) {
     const T* row = (const T*)a.logits + t * a.E;
     float l[V], s[V];
     load_logits<V>(row, e0, a.E, l);
-    if (a.sigmoid || a.partial != nullptr) scores_of<G, V>(l, a.sigmoid, s);
+    if (SIGMOID || a.partial != nullptr) scores_of<G, V, SIGMOID>(l, s);
     if (a.partial != nullptr && live) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) total[v] += e0 + v < a.E ? s[v] : 0.0f;
+      for (int v = 0; v < V; ++v) total[v] += s[v];
     }
     uint32_t u[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float key = a.sigmoid ? s[v] : l[v];
+      float key = SIGMOID ? s[v] : l[v];
       if (a.bias != nullptr && e0 + v < a.E) key += a.bias[e0 + v];
-      u[v] = l[v] == -INFINITY || key == -INFINITY ? 0u : ordered(key);
+      if (SIGMOID || a.bias != nullptr) key = l[v] == -INFINITY ? -INFINITY : key;
+      u[v] = ordered(key);
     }
 #pragma unroll
     for (int i = 0; i < P; ++i)
@@ -199,45 +193,38 @@ __global__ __launch_bounds__(256) void route_topk_kernel(RouteArgs a) {
 #pragma unroll
       for (int v = 1; v < V; ++v) best = u[v] > best ? u[v] : best;
       best = max_over<G>(best);
-      const bool open_ = best != 0u;
+      const bool open_ = best > kMasked;
       const uint32_t key = open_ ? best : 0xfffffffeu;  // (a number that no key has)
       // one of a token's keys is the largest, unless two are equal: then the lowest expert's is taken
-      int found = 0, at = 0;
-      uint64_t lanes = 0;
+      int at = -1, found = 0;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
+      for (int v = V - 1; v >= 0; --v) {
         const bool equal = u[v] == key;
-        const uint64_t m = __ballot(equal);
-        found += __popcll(m);
-        lanes |= m;
+        found += __popcll(__ballot(equal));
         at = equal ? v : at;
       }
-      if (found * G == __popcll(__ballot(open_))) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) u[v] = u[v] == key ? 0u : u[v];
-        if (lanes >> (threadIdx.x & 63) & 1) taken[group][j] = e0 + at;
-      } else {
-        uint32_t e = 0xffffffffu;
-#pragma unroll
-        for (int v = V - 1; v >= 0; --v) e = u[v] == key ? (uint32_t)(e0 + v) : e;
-        e = min_over<G>(e);
-#pragma unroll
-        for (int v = 0; v < V; ++v) u[v] = e == (uint32_t)(e0 + v) ? 0u : u[v];
-        if (lane == 0 && open_) taken[group][j] = (int)e;
+      if (found * G != __popcll(__ballot(open_))) {
+        const uint32_t e = min_over<G>(at < 0 ? 0xffffffffu : (uint32_t)(e0 + at));
+        at = e == (uint32_t)(e0 + at) ? at : -1;
       }
+#pragma unroll
+      for (int v = 0; v < V; ++v) u[v] = at == v ? 0u : u[v];
+      if (at >= 0) taken[group][j] = e0 + at;
     }
     wave_order();
     int mine[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) mine[i] = lane + i * G < a.K ? taken[group][lane + i * G] : -1;
     wave_order();
-    float p[P], other[P];
+    float p[P], other[P], x[P];
+    // (the chosen logits are read again: a lane holds other experts' than those it writes)
+#pragma unroll
+    for (int i = 0; i < P; ++i) x[i] = mine[i] >= 0 ? to_f32(row[mine[i]]) : -INFINITY;
     if (a.renormalize) {
-      chosen_scores<G>(row, mine, a.sigmoid, p, other);
+      chosen_scores<G, P, SIGMOID>(x, mine, p, other);
     } else {
-      // (the chosen logits are read again: a lane holds other experts' than those it writes)
       float m = l[0], sum = 0.0f;
-      if (!a.sigmoid) {
+      if constexpr (!SIGMOID) {
 #pragma unroll
         for (int v = 1; v < V; ++v) m = fmaxf(m, l[v]);
         m = fmax_over<G>(m);
@@ -247,10 +234,8 @@ __global__ __launch_bounds__(256) void route_topk_kernel(RouteArgs a) {
         sum = sum_over<G>(sum);
       }
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const float x = mine[i] >= 0 ? to_f32(row[mine[i]]) : -INFINITY;
-        p[i] = mine[i] < 0 ? 0.0f : a.sigmoid ? sigmoid_stated(x) : exp_fast(x - m) * (1.0f / sum);
-      }
+      for (int i = 0; i < P; ++i)
+        p[i] = mine[i] < 0 ? 0.0f : SIGMOID ? sigmoid_stated(x[i]) : exp_fast(x[i] - m) * recip_rn(sum);
     }
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -300,54 +285,83 @@ __global__ __launch_bounds__(1024) void route_sum_kernel(const float* partial, i
 }
 
 // FULL: every score is needed (the scores' sums have a gradient, or the softmax is not renormalized).
-template <class T, int G, int V, bool FULL>
+template <class T, int G, int V, int P, bool SIGMOID, bool FULL>
 __global__ __launch_bounds__(256) void route_topk_grad_kernel(RouteArgs a) {
-  constexpr int P = kPerLane<G>;
   __shared__ int at_sm[256 / G][BSFP8_MAX_TOP_K];
   __shared__ float part_sm[256 / G][BSFP8_MAX_TOP_K];
   __shared__ __attribute__((aligned(16))) float row_sm[256 / G][G * V];
   const int lane = threadIdx.x & (G - 1), group = threadIdx.x / G, e0 = lane * V;
-  for (int64_t t0 = (int64_t)blockIdx.x * (256 / G); t0 < a.T; t0 += (int64_t)gridDim.x * (256 / G)) {
-    const bool live = t0 + group < a.T;
-    const int64_t t = live ? t0 + group : a.T - 1;
-    const T* row = (const T*)a.logits + t * a.E;
-    float l[V], s[V], other[V];
-    if constexpr (FULL) {
-      load_logits<V>(row, e0, a.E, l);
-      scores_of<G, V>(l, a.sigmoid, s, other);
-    }
-    int e[P];
-    float g[P];
+  float dsum[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) dsum[v] = FULL && a.dsum != nullptr && e0 + v < a.E ? a.dsum[e0 + v] : 0.0f;
+  // a token's logits, choices and gradients, asked for before the token before it is worked on
+  float next_l[V], next_g[P];
+  int next_e[P];
+  const int64_t step = (int64_t)gridDim.x * (256 / G);
+  auto ask = [&](int64_t t0) {
+    const int64_t t = t0 + group < a.T ? t0 + group : a.T - 1;
+    if constexpr (FULL) load_logits<V>((const T*)a.logits + t * a.E, e0, a.E, next_l);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const int j = lane + i * G;
-      e[i] = j < a.K ? a.experts[t * a.K + j] : -1;
-      if (e[i] >= a.E) e[i] = -1;
-      g[i] = e[i] >= 0 ? a.probs[t * a.K + j] * a.scale : 0.0f;
+      next_e[i] = j < a.K ? a.experts[t * a.K + j] : -1;
+      next_g[i] = j < a.K ? a.probs[t * a.K + j] : 0.0f;
+    }
+  };
+  ask((int64_t)blockIdx.x * (256 / G));
+  for (int64_t t0 = (int64_t)blockIdx.x * (256 / G); t0 < a.T; t0 += step) {
+    const bool live = t0 + group < a.T;
+    const int64_t t = live ? t0 + group : a.T - 1;
+    const T* row = (const T*)a.logits + t * a.E;
+    float l[V], s[V], other[V], g[P];
+    int e[P];
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = FULL ? next_l[v] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      e[i] = next_e[i] < a.E ? next_e[i] : -1;
+      g[i] = e[i] >= 0 ? next_g[i] * a.scale : 0.0f;
+    }
+    ask(t0 + step);
+    float* to = &row_sm[group][e0];
+    const bool chosen_only = a.renormalize || SIGMOID;
+    // the chosen logits: from LDS where the lanes hold the row anyway
+    float x[P];
+    if constexpr (FULL) {
+      if (chosen_only) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) to[v] = l[v];
+        wave_order();
+#pragma unroll
+        for (int i = 0; i < P; ++i) x[i] = e[i] >= 0 ? row_sm[group][e[i]] : -INFINITY;
+        wave_order();
+      }
+      scores_of<G, V, SIGMOID>(l, s, other);
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; ++i) x[i] = e[i] >= 0 ? to_f32(row[e[i]]) : -INFINITY;
     }
     // what a choice gives to its expert: at the logit, or (softmax without renormalize) at the score
-    const bool at_score = !a.renormalize && !a.sigmoid;
+    const bool at_score = !a.renormalize && !SIGMOID;
     if (a.renormalize) {
       float ph[P], rest[P], mean = 0.0f;
-      chosen_scores<G>(row, e, a.sigmoid, ph, rest);
+      chosen_scores<G, P, SIGMOID>(x, e, ph, rest);
 #pragma unroll
       for (int i = 0; i < P; ++i) mean += g[i] * ph[i];
       mean = sum_over<G>(mean);
 #pragma unroll
-      for (int i = 0; i < P; ++i) g[i] = e[i] < 0 ? 0.0f : ph[i] * (g[i] - mean) * (a.sigmoid ? rest[i] : 1.0f);
-    } else if (a.sigmoid) {
+      for (int i = 0; i < P; ++i) g[i] = e[i] < 0 ? 0.0f : ph[i] * (g[i] - mean) * (SIGMOID ? rest[i] : 1.0f);
+    } else if constexpr (SIGMOID) {
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        const float x = e[i] >= 0 ? to_f32(row[e[i]]) : -INFINITY;
         float rest;
-        const float sc = sigmoid_stated(x, &rest);
-        g[i] = x == -INFINITY ? 0.0f : g[i] * sc * rest;
+        const float sc = sigmoid_stated(x[i], &rest);
+        g[i] = x[i] == -INFINITY ? 0.0f : g[i] * sc * rest;
       }
     }
     // the choices' parts at their experts' places.  Each choice writes its number there first: one that finds another's
     // shares its expert, and the parts are then added choice by choice, in order
     float d[V];
-    float* to = &row_sm[group][e0];
 #pragma unroll
     for (int v = 0; v < V; ++v) to[v] = 0.0f;
     wave_order();
@@ -391,14 +405,14 @@ __global__ __launch_bounds__(256) void route_topk_grad_kernel(RouteArgs a) {
       float back[V], mean = 0.0f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        back[v] = a.dsum != nullptr && e0 + v < a.E ? a.dsum[e0 + v] : 0.0f;
+        back[v] = dsum[v];
         if (at_score) {
           back[v] += d[v];
           d[v] = 0.0f;
         }
         mean += s[v] == 0.0f ? 0.0f : back[v] * s[v];
       }
-      if (a.sigmoid) {
+      if constexpr (SIGMOID) {
 #pragma unroll
         for (int v = 0; v < V; ++v) d[v] += s[v] == 0.0f ? 0.0f : back[v] * s[v] * other[v];
       } else {
@@ -423,17 +437,30 @@ __global__ __launch_bounds__(256) void route_topk_grad_kernel(RouteArgs a) {
   }
 }
 
-// f with the lanes per token and the values per lane that E experts take.
+// f with the lanes per token, the experts and the choices per lane that E and K take, and the scoring.
 template <class F>
-static void for_experts(int E, F f) {
+static void for_shape(int E, int K, bool sigmoid, F f) {
+  auto scoring = [&](auto g, auto v, auto p) {
+    if (sigmoid) f(g, v, p, std::true_type());
+    else f(g, v, p, std::false_type());
+  };
+  auto choices = [&](auto g, auto v) {
+    if constexpr (decltype(g)::value < BSFP8_MAX_TOP_K) {
+      if (K > decltype(g)::value) {
+        scoring(g, v, std::integral_constant<int, BSFP8_MAX_TOP_K / decltype(g)::value>());
+        return;
+      }
+    }
+    scoring(g, v, std::integral_constant<int, 1>());
+  };
   auto with = [&](auto g) {
     constexpr int G = decltype(g)::value;
     const int v = (E + G - 1) / G;
-    if (v <= 1) f(g, std::integral_constant<int, 1>());
-    else if (v <= 2) f(g, std::integral_constant<int, 2>());
-    else if (v <= 4) f(g, std::integral_constant<int, 4>());
-    else if (v <= 8) f(g, std::integral_constant<int, 8>());
-    else f(g, std::integral_constant<int, 16>());
+    if (v <= 1) choices(g, std::integral_constant<int, 1>());
+    else if (v <= 2) choices(g, std::integral_constant<int, 2>());
+    else if (v <= 4) choices(g, std::integral_constant<int, 4>());
+    else if (v <= 8) choices(g, std::integral_constant<int, 8>());
+    else choices(g, std::integral_constant<int, 16>());
   };
   if (route_lanes(E) == 16) with(std::integral_constant<int, 16>());
   else with(std::integral_constant<int, 64>());
@@ -444,12 +471,14 @@ int launch_route_topk(const void* logits, bool f32, int64_t T, int E, int K, boo
                       hipStream_t stream) {
   const int64_t blocks = route_blocks(T, E);
   if (blocks > 0) {
-    const RouteArgs a{logits, T, E, K, bias, sigmoid, renormalize, scale, probs, experts,
+    const RouteArgs a{logits, T, E, K, bias, renormalize, scale, probs, experts,
                       score_sum != nullptr ? workspace : nullptr, nullptr, nullptr};
-    for_experts(E, [&](auto g, auto v) {
-      constexpr int G = decltype(g)::value, V = decltype(v)::value;
-      if (f32) hipLaunchKernelGGL((route_topk_kernel<float, G, V>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
-      else hipLaunchKernelGGL((route_topk_kernel<uint16_t, G, V>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
+    const dim3 grid((unsigned)blocks), block(256);
+    for_shape(E, K, sigmoid, [&](auto g, auto v, auto p, auto sg) {
+      constexpr int G = decltype(g)::value, V = decltype(v)::value, P = decltype(p)::value;
+      constexpr bool S = decltype(sg)::value;
+      if (f32) hipLaunchKernelGGL((route_topk_kernel<float, G, V, P, S>), grid, block, 0, stream, a);
+      else hipLaunchKernelGGL((route_topk_kernel<uint16_t, G, V, P, S>), grid, block, 0, stream, a);
     });
     if (hipGetLastError() != hipSuccess) return BSFP8_ERR_LAUNCH;
   }
@@ -462,16 +491,18 @@ int launch_route_topk(const void* logits, bool f32, int64_t T, int E, int K, boo
 int launch_route_topk_grad(const float* dprobs, const void* logits, bool f32, const int32_t* experts, int64_t T, int E,
                            int K, bool sigmoid, int renormalize, float scale, const float* dsum, void* dlogits,
                            hipStream_t stream) {
-  const RouteArgs a{logits, T, E, K, nullptr, sigmoid, renormalize, scale, const_cast<float*>(dprobs),
+  const RouteArgs a{logits, T, E, K, nullptr, renormalize, scale, const_cast<float*>(dprobs),
                     const_cast<int32_t*>(experts), nullptr, dsum, dlogits};
   const bool full = dsum != nullptr || (!sigmoid && !renormalize);
-  const dim3 grid((unsigned)route_blocks(T, E)), block(256);
-  for_experts(E, [&](auto g, auto v) {
-    constexpr int G = decltype(g)::value, V = decltype(v)::value;
-    if (f32 && full) hipLaunchKernelGGL((route_topk_grad_kernel<float, G, V, true>), grid, block, 0, stream, a);
-    else if (f32) hipLaunchKernelGGL((route_topk_grad_kernel<float, G, V, false>), grid, block, 0, stream, a);
-    else if (full) hipLaunchKernelGGL((route_topk_grad_kernel<uint16_t, G, V, true>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((route_topk_grad_kernel<uint16_t, G, V, false>), grid, block, 0, stream, a);
+  const dim3 grid((unsigned)route_blocks(T, E, true)), block(256);
+  for_shape(E, K, sigmoid, [&](auto g, auto v, auto p, auto sg) {
+    constexpr int G = decltype(g)::value, V = decltype(v)::value, P = decltype(p)::value;
+    constexpr bool S = decltype(sg)::value;
+    auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
+    if (f32 && full) launch(route_topk_grad_kernel<float, G, V, P, S, true>);
+    else if (f32) launch(route_topk_grad_kernel<float, G, V, P, S, false>);
+    else if (full) launch(route_topk_grad_kernel<uint16_t, G, V, P, S, true>);
+    else launch(route_topk_grad_kernel<uint16_t, G, V, P, S, false>);
   });
   return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
 }
