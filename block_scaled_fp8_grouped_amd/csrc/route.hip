@@ -3,8 +3,15 @@
 //
 // A token's logits lie in the registers of 16 lanes (up to 256 experts) or of a wave (up to 1024), V = 1 to 16
 // consecutive experts a lane, so that a lane's logits are one wide load and its reductions over a token are moves within
-// a row of 16 lanes.  Keys are compared as unsigned numbers whose order is that of the keys (NaN highest, 0 for masked
-// and taken ones).  A choice takes one reduction for the largest key and one for the lowest expert that has it.
+// a row of 16 lanes.  Keys are compared as unsigned numbers whose order is that of the keys (NaN highest, the masked
+// lowest, then 0 for the taken).  A choice takes one reduction for the largest key, and where two of a token's keys are
+// equal one more for the lowest expert that has it.
+//
+// What bounds them: 131072 tokens of 128 logits in fp32 are 67 MB, 11 us at 6.2 TB/s.  The choices' comparisons are about
+// 35 vector instructions a choice for 4 tokens, so the forward pass is bound by them: 44 us with the sums of the scores
+// (66 with both reductions at every choice, 49 with the scoring and the choices per lane looked up while running).  The
+// gradient reads and writes 134 MB, 22 us; a token's loads hang on each other (its choices, then their logits), so the
+// next token's are asked for ahead and the chosen logits of a row that the lanes hold come from LDS: 33 us (58 without).
 #include <math.h>
 
 #include <type_traits>
