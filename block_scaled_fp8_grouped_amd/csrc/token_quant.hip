@@ -8,6 +8,11 @@
 // row at a time.  A lane's 8 rows of a channel are 8 consecutive colwise codes; those of the 4 waves of a workgroup meet in
 // LDS, whence a channel's 128 leave as one line.  What belongs to a row (the choice that it stands for, its probability,
 // its part of dprobs) is held while the wave walks.
+//
+// What bounds them: bytes, which come and go at 6.2 TB/s at best, and the instructions that the conversions to codes in two
+// directions take.  65536 gathered rows of 4096 (32 experts, 4 a token) read 134 MB and write 553 MB, 111 us: 169 us.  The
+// SwiGLU's gradient of 65536 x 2048 reads 545 MB and writes 690 MB, 200 us: 281 us, at the 256 registers that leave two
+// waves a SIMD.  Activation and kept input of 4099 x 4128, 85 MB: 14 us of bytes in 27 us, 1320 workgroups at 1024 places.
 #include <math.h>
 
 #include <type_traits>
@@ -20,8 +25,8 @@
 
 namespace bsfp8 {
 
-// Codes go past the caches (a line's 128 bytes leave together, and none is read again here): 181 -> 170 us on 65536 gathered rows of
-// 4096.
+// Codes go past the caches (a line's 128 bytes leave together, and none is read again here): 181 -> 170 us on 65536
+// gathered rows of 4096, whose tokens then stay in them; 288 -> 279 us on the SwiGLU's gradient.
 constexpr int kPastCaches = 2;
 constexpr int kTThreads = 256;
 
@@ -55,8 +60,8 @@ __device__ __forceinline__ uint32_t lane_move(uint32_t v) {
 }
 constexpr int kXor1 = 0xB1, kXor2 = 0x4E;  // lane moves within a quad
 
-// From each lane's 8 row maxima m those of the 4 lanes of its quad, which have a block of 32 channels: lane q gets those of rows
-// q and 4 + q.  Each step halves the values a lane carries, so that a scale is worked out once and not by every lane of
+// From each lane's 8 row maxima m those of the 4 lanes of its quad, which have a block of 32 channels: lane q gets those
+// of rows q and 4 + q.  Each step halves the values a lane carries, so that a scale is worked out once and not by every lane of
 // its block.
 __device__ __forceinline__ void row_block_max(const uint32_t (&m)[8], int ch, uint32_t (&out)[2]) {
   const bool odd = ch & 1, high = ch & 2;
@@ -280,7 +285,9 @@ __device__ __forceinline__ void put_rows(const LanePlace& l, uint8_t* q, uint8_t
   const uint32_t off = l.live_col ? (8 * (uint32_t)l.rl * width + (uint32_t)(l.ch * 8)) / PER : kNowhere;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint32_t b = byte[i >> 2], of = i % 4 == 0 ? quad_lane<0>(b) : i % 4 == 1 ? quad_lane<1>(b) : i % 4 == 2 ? quad_lane<2>(b) : quad_lane<3>(b);
+    const uint32_t b = byte[i >> 2];
+    const uint32_t of = i % 4 == 0 ? quad_lane<0>(b) : i % 4 == 1 ? quad_lane<1>(b) : i % 4 == 2 ? quad_lane<2>(b)
+                                                                                              : quad_lane<3>(b);
     store_codes<F4>(row_buffer(at, i, width / PER, l.live), off, x.template row_codes<F4>(i, of));
   }
   // the quad has its block's 8 scales, two a lane
@@ -328,7 +335,7 @@ __device__ __forceinline__ void put_cols(const LanePlace& l, int wave, uint8_t* 
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// A tile's codes from LDS to the layout, 16 bytes a lane; `wave0`: the workgroup's first block of 32 rows.
+// A tile's codes from LDS to the layout, 16 bytes a lane; `block0`: the workgroup's first block of 32 rows.
 template <bool F4>
 __device__ __forceinline__ void flush_cols(const LanePlace& l, int64_t block0, const uint8_t* codes, uint8_t* q, int64_t width,
                                            int64_t c0, int ncols) {
@@ -587,7 +594,7 @@ __global__ __launch_bounds__(kTThreads) void dispatch_quantize_kernel(TokenQuant
       if (row_out) put_rows<F4>(l, a.row_q, a.row_s, F, c0, values);
       if (!col_out) return;
       put_cols<F4>(l, wave, codes[turn], a.col_s, F, c0, values);
-      __syncthreads();  // (two buffers, as below)
+      __syncthreads();  // (one for two buffers: see the activations' kernel)
       flush_cols<F4>(l, l.block - wave, codes[turn], a.col_q, F, c0, F - c0 < W ? (int)(F - c0) : W);
       turn ^= 1;
     };
@@ -682,7 +689,8 @@ __global__ __launch_bounds__(kTThreads, mode_grad(MODE) ? 2 : 1) void act_checkp
     }
   };
 
-  // (loading a tile ahead costs more waves than it hides: 368 us against 400 on 65536 x 2048 of the SwiGLU's gradient)
+  // (a tile asked for ahead takes registers that are worth more as waves: 400 us against 368 when the SwiGLU's gradient of
+  // 65536 x 2048 took that)
   TokenInputs<MODE> x;
   int turn = 0;
   const int64_t begin = seg * a.tiles * W, stop = begin + (int64_t)a.tiles * W, end = stop < F ? stop : F;
@@ -761,7 +769,6 @@ __global__ __launch_bounds__(kTThreads, mode_grad(MODE) ? 2 : 1) void act_checkp
             inputs(i);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              
               y.v[i][k] = d[k] * prob[i] * (h[k] * sg.v[i][k]);
               keep(y.v[i][k]);
             }

@@ -543,8 +543,9 @@ int bsfp8_dispatch_plan(const int32_t* experts, const float* probs, int64_t toke
  * x        [tokens][cols] of dtype (BSFP8_F32 or BSFP8_BF16); out [capacity_rows][cols] of dtype
  * rows     int32 [tokens][top_k], as bsfp8_dispatch_plan writes them; one outside [0, capacity_rows) is skipped
  * weights  fp32 [tokens][top_k], or NULL (1: the rows are copied bit for bit)
- * Rows of out that no choice has are not written.  1 <= cols <= 2^24, tokens * top_k <= 2^30,
- * capacity_rows <= 2^31 - 1.  This is also the gradient of bsfp8_combine without weights.
+ * Rows of out that no choice has are not written; no two choices have one row.  1 <= cols <= 2^24,
+ * tokens * top_k <= 2^30, capacity_rows <= 2^31 - 1, and x is below 2^35 elements with cols rounded up to 8 2^n (above
+ * 2048: to a multiple of 2048).  This is also the gradient of bsfp8_combine without weights.
  */
 int bsfp8_dispatch(const void* x, int dtype, int64_t tokens, int64_t cols, const int32_t* rows, int32_t top_k,
                    const float* weights, void* out, int64_t capacity_rows, void* stream);
@@ -571,7 +572,7 @@ int bsfp8_dispatch_quantize(const void* x_bf16, int64_t tokens, int64_t cols, co
  * y       [capacity_rows][cols] of dtype; a row outside [0, capacity_rows) counts as zero and is not read
  * weights fp32 [tokens][top_k] or NULL (1: this is the gradient of bsfp8_dispatch without weights)
  * add     [tokens][cols] of dtype or NULL (0); may be out itself
- * out     [tokens][cols] of dtype
+ * out     [tokens][cols] of dtype; its size bounded as x above
  */
 int bsfp8_combine(const void* y, int dtype, int64_t capacity_rows, int64_t cols, const int32_t* rows, int64_t tokens,
                   int32_t top_k, const float* weights, const void* add, void* out, void* stream);
@@ -583,7 +584,8 @@ int bsfp8_combine(const void* y, int dtype, int64_t capacity_rows, int64_t cols,
  * rows' gradient with the same weights.)
  * dout      [tokens][cols] of dtype
  * y         [capacity_rows][cols] of dtype, needed for dweights
- * dy        [capacity_rows][cols] of dtype or NULL; may be y itself.  Rows that no choice has are not written
+ * dy        [capacity_rows][cols] of dtype or NULL; may be y itself.  Rows that no choice has are not written; no two
+ *           choices have one row
  * dweights  fp32 [tokens][top_k] or NULL
  */
 int bsfp8_combine_grad(const void* dout, int dtype, int64_t tokens, int64_t cols, const void* y, int64_t capacity_rows,

@@ -292,3 +292,14 @@ def test_large_checkpoint(act):
             assert torch.equal(got[:, -tail:], want), name
         else:
             assert torch.equal(got[at * c // per:(at + n) * c // per], want[:n * c // per]), name
+
+
+def test_more_tokens_than_a_launch_has_waves():
+    """Rows of one channel: each token's part of the gradient by itself."""
+    tokens = (1 << 26) + 5
+    rows = torch.arange(tokens - 1, -1, -1, dtype=torch.int32, device=DEV).view(tokens, 1)
+    x, y, w = (torch.rand((tokens, 1), device=DEV) for _ in range(3))
+    d = bs.combine_grad(x, {"rows": rows}, y=y, weights=w)
+    assert torch.equal(d["dweights"], x * y.flip(0)) and torch.equal(d["dy"], (x * w).flip(0))
+    assert torch.equal(bs.combine(y, {"rows": rows}, w), y.flip(0) * w)
+    assert torch.equal(bs.dispatch(x, {"rows": rows}), x.flip(0))
