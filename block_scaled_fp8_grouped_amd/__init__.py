@@ -6,7 +6,9 @@ step of the computation runs in the library's kernels.  PyTorch supplies device 
 stream.  If the library has not been built, importing works but every call raises.
 
 Functions keep the C names without the ``bsfp8_`` prefix:
-  grouped_quantize, grouped_gemm_wgrad, grouped_gemm_fprop, the size queries, strerror.
+  grouped_quantize, grouped_gemm_wgrad, grouped_gemm_fprop, the size queries, strerror; and the steps around them:
+  grouped_gemm_swiglu, residual_norm, adamw_step, route_topk, dispatch_plan, dispatch, dispatch_quantize, combine,
+  grouped_act_checkpoint and their gradients.
 ``alloc_quantized`` and ``alloc_*`` helpers size output tensors with the library's own size
 queries.
 """

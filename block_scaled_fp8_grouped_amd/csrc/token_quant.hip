@@ -12,7 +12,7 @@
 // What bounds them: bytes, which come and go at 6.2 TB/s at best, and the instructions that the conversions to codes in two
 // directions take.  65536 gathered rows of 4096 (32 experts, 4 a token) read 134 MB and write 553 MB, 111 us: 169 us.  The
 // SwiGLU's gradient of 65536 x 2048 reads 545 MB and writes 690 MB, 200 us: 281 us, at the 256 registers that leave two
-// waves a SIMD.  Activation and kept input of 4099 x 4128, 85 MB: 14 us of bytes in 27 us, 1320 workgroups at 1024 places.
+// waves a SIMD.  Activation and kept input of 4099 x 4128, 88 MB: 14 us of bytes in 27 us, 1320 workgroups at 1024 places.
 #include <math.h>
 
 #include <type_traits>
