@@ -7,8 +7,9 @@
 // expert; the second adds up the chunks before its own by itself (no third launch, no wait between workgroups) and
 // places.  Up to one chunk of choices takes one launch.
 //
-// What bounds it: 131072 tokens' 8 choices of 128 are 21 MB, 3.4 us, in two launches: 16 us (one workgroup's 4096 choices go
-// through a scan over 128 bins and 16 waves whatever their bytes).
+// What bounds it: 131072 tokens' 8 choices of 128 are 21 MB, 3.4 us, in two launches: 15 us, of which the second's
+// workgroups take 1 for their choices, 3 to add up the chunks' counts, 1 for the bins' begins (2 with all waves in it), 2 to
+// rank 4096 choices and 1 to store them.
 //
 // The row movers walk tokens: a token's row is read once and written (dispatch), or a token's top_k rows are read and
 // summed (combine), each byte moved once in rows of cols elements, 8 elements a thread.  All are bound by HBM: 16384 tokens'
@@ -65,27 +66,24 @@ __global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(PlanArgs a) {
     a.hist[(int64_t)blockIdx.x * plan_hist_row(a.E) + b] = b <= a.E ? count[b] : 0;
 }
 
-// Exclusive prefix over the workgroup of one value a thread.
-__device__ __forceinline__ int32_t plan_scan(int32_t v, int32_t* wave_total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int32_t s = v;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int32_t u = __shfl_up(s, d, 64);
-    if (lane >= d) s += u;
+// A wave turns the counts of n bins into where each begins; `out` (or NULL) gets the counts of the first n - 1.
+__device__ __forceinline__ void plan_begins(int32_t* count, int n, int32_t* out) {
+  const int lane = threadIdx.x & 63, per = (n + 63) / 64, b0 = lane * per;
+  int sum = 0;
+  for (int b = b0; b < b0 + per; ++b) sum += b < n ? count[b] : 0;
+  int begin = wave_scan32(sum) - sum;
+  for (int b = b0; b < b0 + per && b < n; ++b) {
+    const int32_t v = count[b];
+    if (out != nullptr && b < n - 1) out[b] = v;
+    count[b] = begin;
+    begin += v;
   }
-  if (lane == 63) wave_total[wave] = s;
-  __syncthreads();
-  int32_t before = 0;
-  for (int w = 0; w < wave; ++w) before += wave_total[w];
-  __syncthreads();
-  return before + s - v;
 }
 
 __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanArgs a) {
   // at[w * bins + b]: first the choices of wave w in bin b, then where its next one goes
   __shared__ int32_t at[kPlanWaves * (kMaxGroups + 1)];
-  __shared__ int32_t total[kMaxGroups + 1], before[kMaxGroups + 1], own[kMaxGroups + 1], wave_total[kPlanWaves];
+  __shared__ int32_t total[kMaxGroups + 1], before[kMaxGroups + 1], own[kMaxGroups + 1];
   __shared__ int32_t sorted_row[kPlanUnit], sorted_choice[kPlanUnit];
   __shared__ float sorted_prob[kPlanUnit];
   const int bins = a.E + 1, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -104,12 +102,6 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanArgs a) {
   for (int i = threadIdx.x; i < kPlanWaves * bins; i += kPlanThreads) at[i] = 0;
   for (int b = threadIdx.x; b < bins; b += kPlanThreads) total[b] = before[b] = 0;
   __syncthreads();
-  for (int64_t c0 = begin; c0 < end; c0 += 64 * kPlanSteps) {
-    if (c0 != begin) load(c0);
-#pragma unroll
-    for (int i = 0; i < kPlanSteps; ++i)
-      if (bin[i] < bins) atomicAdd(&at[wave * bins + bin[i]], 1);
-  }
   if (a.hist != nullptr) {
     // the chunks' counts: every 16th a wave's, 4 bins a lane, 8 loads in flight
     const int row = plan_hist_row(a.E);
@@ -137,6 +129,12 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanArgs a) {
       }
     }
   }
+  for (int64_t c0 = begin; c0 < end; c0 += 64 * kPlanSteps) {
+    if (c0 != begin) load(c0);
+#pragma unroll
+    for (int i = 0; i < kPlanSteps; ++i)
+      if (bin[i] < bins) atomicAdd(&at[wave * bins + bin[i]], 1);
+  }
   __syncthreads();
   // a bin's counts of the 16 waves, before each
   for (int b = threadIdx.x; b < bins; b += kPlanThreads) {
@@ -152,20 +150,9 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanArgs a) {
     own[b] = sum;
   }
   __syncthreads();
-  // where the bins begin: at most two bins a thread, consecutive ones, so that one prefix over the threads serves them
-  const int b0 = 2 * threadIdx.x;
-  const int32_t n0 = b0 < bins ? total[b0] : 0, n1 = b0 + 1 < bins ? total[b0 + 1] : 0;
-  const int32_t first = plan_scan(n0 + n1, wave_total);
-  const int32_t o0 = b0 < bins ? own[b0] : 0, o1 = b0 + 1 < bins ? own[b0 + 1] : 0;
-  const int32_t own_first = a.hist != nullptr ? plan_scan(o0 + o1, wave_total) : first;  // (one chunk: its own are all)
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int b = b0 + i;
-    if (b >= bins) break;
-    if (blockIdx.x == 0 && b < a.E) a.splits[b] = i ? n1 : n0;
-    before[b] += first + (i ? n0 : 0);
-    own[b] = own_first + (i ? o0 : 0);
-  }
+  // where the bins begin, in the rows and in the chunk
+  if (wave == 0) plan_begins(total, bins, blockIdx.x == 0 ? a.splits : nullptr);
+  if (wave == 1) plan_begins(own, bins, nullptr);
   __syncthreads();
   int32_t* next = at + wave * bins;
   const uint64_t below = (uint64_t(1) << lane) - 1;
@@ -190,7 +177,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanArgs a) {
       const uint64_t same = (uint64_t)hi << 32 | lo;
       const int rank = __popcll(same & below);
       if (b < bins) {
-        const int32_t mine = next[b] + rank, row = before[b] + mine;
+        const int32_t mine = next[b] + rank, row = total[b] + before[b] + mine;
         __builtin_amdgcn_wave_barrier();
         if (rank == 0) next[b] = mine + __popcll(same);  // (a wave's LDS accesses are done in order)
         const bool dropped = b == a.E;

@@ -97,4 +97,19 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
+// Inclusive sum over a wave, with data-parallel lane moves.
+__device__ __forceinline__ int wave_scan32(int v) {
+  auto add = [&](auto ctrl, auto rows) {
+    v += __builtin_amdgcn_update_dpp(0, v, decltype(ctrl)::value, decltype(rows)::value, 0xf, false);
+  };
+  using std::integral_constant;
+  add(integral_constant<int, 0x111>(), integral_constant<int, 0xf>());  // 1, 2, 4, 8 lanes below in the row of 16
+  add(integral_constant<int, 0x112>(), integral_constant<int, 0xf>());
+  add(integral_constant<int, 0x114>(), integral_constant<int, 0xf>());
+  add(integral_constant<int, 0x118>(), integral_constant<int, 0xf>());
+  add(integral_constant<int, 0x142>(), integral_constant<int, 0xa>());  // row 0's total to row 1, 2's to 3
+  add(integral_constant<int, 0x143>(), integral_constant<int, 0xc>());  // the first half's total to the second
+  return v;
+}
+
 }  // namespace bsfp8
