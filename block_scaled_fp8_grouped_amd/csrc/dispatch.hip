@@ -14,7 +14,7 @@
 // The row movers walk tokens: a token's row is read once and written (dispatch), or a token's top_k rows are read and
 // summed (combine), each byte moved once in rows of cols elements, 8 elements a thread.  All are bound by HBM: 16384 tokens'
 // sums of 4 rows of 4096 bf16 with the residual stream 142 us, 130 us of bytes at 6.2 TB/s; the gradient of 16411 tokens' 3
-// rows of 2050, whose rows begin at odd multiples of 4 bytes, 101 us (69 us of bytes).
+// rows of 2050, whose rows begin at odd multiples of 4 bytes, 92 us (69 us of bytes).
 #include <type_traits>
 
 #include "common.hpp"
@@ -463,20 +463,25 @@ int launch_combine_grad(const void* dout, bool f32, int64_t T, int64_t C, const 
                         const int32_t* rows, int K, const float* weights, void* dy, float* dweights,
                         hipStream_t stream) {
   const MoveArgs a{T, C, cap, K, rows, weights, dout, nullptr, dy, y, dweights, move_past(cap, C, f32)};
-  // a token per wave where they fill the chip by themselves
-  const bool wave = T >= 4096 || C <= 512;
-  const int64_t blocks = wave ? (T + 3) / 4 : T;
-  const dim3 grid((unsigned)(blocks < kMostBlocks ? blocks : kMostBlocks));
-  auto go = [&](auto kb, auto y, auto o) {
-    constexpr int KB = decltype(kb)::value;
+  // A token's row is a workgroup's, with a wave for each KB of it up to 8, or a wave's: few tokens in flight at a time, whose
+  // rows are read and written as a whole (waves a token 1 / 2 / 4 / 8: 16384 x 4 rows of 4096 bf16 246 / 236 / 227 / 223 us,
+  // of 2050 101 / 94 / 92 / 118, 32768 x 4 of 1024 114 / 111 / 120 / 188, 65536 x 4 of 512 112 / 122 / 189 / 327; 16384 x 4
+  // of 2048 fp32 277 / 256 / 241 / 225, of 1024 137 / 125 / 119 / 134, 65536 x 4 of 256 123 / 157 / 232 / 363).  Up to an
+  // eighth more goes without waves of its own.
+  auto launch = [&](auto w, auto kb, auto y, auto o) {
+    constexpr int W = decltype(w)::value, KB = decltype(kb)::value, THREADS = W == 1 ? 256 : 64 * W;
     constexpr bool Y = decltype(y)::value, O = decltype(o)::value;
-    if (wave) {
-      if (f32) hipLaunchKernelGGL((combine_grad_kernel<float, 1, KB, Y, O>), grid, dim3(256), 0, stream, a);
-      else hipLaunchKernelGGL((combine_grad_kernel<uint16_t, 1, KB, Y, O>), grid, dim3(256), 0, stream, a);
-    } else {
-      if (f32) hipLaunchKernelGGL((combine_grad_kernel<float, 8, KB, Y, O>), grid, dim3(512), 0, stream, a);
-      else hipLaunchKernelGGL((combine_grad_kernel<uint16_t, 8, KB, Y, O>), grid, dim3(512), 0, stream, a);
-    }
+    const int64_t blocks = W == 1 ? (T + 3) / 4 : T, most = kMostBlocks / 2;
+    const dim3 grid((unsigned)(blocks < most ? blocks : most)), block(THREADS);
+    if (f32) hipLaunchKernelGGL((combine_grad_kernel<float, W, KB, Y, O>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((combine_grad_kernel<uint16_t, W, KB, Y, O>), grid, block, 0, stream, a);
+  };
+  auto go = [&](auto kb, auto y, auto o) {
+    const int64_t bytes = C * (f32 ? 4 : 2);
+    if (bytes <= 1152) launch(std::integral_constant<int, 1>(), kb, y, o);
+    else if (bytes <= 2304) launch(std::integral_constant<int, 2>(), kb, y, o);
+    else if (bytes <= 4608) launch(std::integral_constant<int, 4>(), kb, y, o);
+    else launch(std::integral_constant<int, 8>(), kb, y, o);
   };
   const std::integral_constant<bool, true> yes;
   const std::integral_constant<bool, false> no;

@@ -240,7 +240,7 @@ def test_large_dispatch():
     a = bs.combine_grad(x, plan, rows, w, dy=rows)  # (dy over y)
     b = bs.combine_grad(small, part, None, w[-tail:].clone())
     assert torch.equal(a["dy"][-tail:], b["dy"])
-    # the order of a sum goes by the number of tokens: chains of at most cols / 64 products a lane, 6 steps and 8 waves
+    # (a sum of cols products: chains of at most cols / 64 a lane, 6 steps and 8 waves)
     terms = small.double() * want.double()
     off = (a["dweights"][-tail:, 0].double() - terms.sum(1)).abs()
     assert (off <= (cols / 64 + 16) * 2.0 ** -24 * terms.abs().sum(1)).all() and bool(a["dweights"][-tail:].any())
