@@ -13,8 +13,8 @@
 //
 // The row movers walk tokens: a token's row is read once and written (dispatch), or a token's top_k rows are read and
 // summed (combine), each byte moved once in rows of cols elements, 8 elements a thread.  All are bound by HBM: 16384 tokens'
-// sums of 4 rows of 4096 bf16 with the residual stream 142 us, 130 us of bytes at 6.2 TB/s; the gradient of 16411 tokens' 3
-// rows of 2050, whose rows begin at odd multiples of 4 bytes, 92 us (69 us of bytes).
+// sums of 4 rows of 4096 bf16 with the residual stream 138 us, 130 us of bytes at 6.2 TB/s; the gradient of 16411 tokens' 3
+// rows of 2050, whose rows begin at odd multiples of 4 bytes, 91 us (69 us of bytes).
 #include <type_traits>
 
 #include "common.hpp"
@@ -241,15 +241,18 @@ struct MoveArgs {
   float* dweights;
   bool past;  // the output goes past the caches
 };
-// Outputs that no cache holds until they are read go past it (gradient of 65536 rows of 4096 265 -> 247 us, 16384 tokens' sums
-// of 2050 fp32 188 -> 173); smaller ones are left for what reads them next.
+// Outputs that no cache holds until they are read go past it (16384 tokens' sums of 4 rows of 4096 bf16 149 -> 141 us, their
+// gradient 229 -> 224); smaller ones are left for what reads them next.
 static bool move_past(int64_t rows, int64_t cols, bool f32) { return rows * cols * (f32 ? 4 : 2) >= int64_t(64) << 20; }
 
 // A launch has fewer than 2^32 threads.
-constexpr int64_t kMostBlocks = (int64_t(1) << 24) - 1;  // of 256
+constexpr int64_t kMostThreads = (int64_t(1) << 32) - 1;
 
-// Threads over (token, chunk of 8 columns): a workgroup takes 256 chunks of one token, or several whole tokens where
-// their rows are shorter; `shift`: log2 of the threads that a token takes in a workgroup.
+// Threads over (token, chunk of 8 columns): a workgroup takes 128 chunks of one token, or several whole tokens where
+// their rows are shorter; `shift`: log2 of the threads that a token takes in a workgroup.  (Workgroups of 64 / 128 / 256 /
+// 512 threads: sums of 4 rows of 4096 bf16 139 / 137 / 141 / 140 us, of 2050 fp32 135 / 135 / 171 / 133, rows out 113 /
+// 113 / 117 / 122.)
+constexpr int kMoveShift = 7, kMoveThreads = 1 << kMoveShift;
 struct MoveShape {
   int shift;
   int64_t segments, blocks;
@@ -257,14 +260,14 @@ struct MoveShape {
 static MoveShape move_shape(int64_t T, int64_t C) {
   const int64_t chunks = (C + 7) / 8;
   int shift = 0;
-  while (shift < 8 && (int64_t(1) << shift) < chunks) ++shift;
-  const int64_t seg = (chunks + (int64_t(1) << shift) - 1) >> shift, per = 256 >> shift;
+  while (shift < kMoveShift && (int64_t(1) << shift) < chunks) ++shift;
+  const int64_t seg = (chunks + (int64_t(1) << shift) - 1) >> shift, per = kMoveThreads >> shift;
   return {shift, seg, (T + per - 1) / per * seg};
 }
 __device__ __forceinline__ bool move_place(const MoveArgs& a, int shift, int64_t segments, int64_t& t, int64_t& c) {
   const int64_t seg = (int64_t)blockIdx.x % segments, set = (int64_t)blockIdx.x / segments;
-  t = set * (256 >> shift) + (threadIdx.x >> shift);
-  c = 8 * (seg * 256 + (threadIdx.x & ((1 << shift) - 1)));
+  t = set * (kMoveThreads >> shift) + (threadIdx.x >> shift);
+  c = 8 * (seg * kMoveThreads + (threadIdx.x & ((1 << shift) - 1)));
   return t < a.T && c < a.C;
 }
 
@@ -293,7 +296,7 @@ __device__ __forceinline__ void copy8(uint16_t* p, int n, const Raw8<uint16_t>& 
 }
 
 template <class T>
-__global__ __launch_bounds__(256) void dispatch_kernel(MoveArgs a, int shift, int64_t segments) {
+__global__ __launch_bounds__(kMoveThreads) void dispatch_kernel(MoveArgs a, int shift, int64_t segments) {
   int64_t t, c;
   if (!move_place(a, shift, segments, t, c)) return;
   const int n = a.C - c < 8 ? (int)(a.C - c) : 8;
@@ -334,7 +337,7 @@ struct TokenRows {
 
 // KB rows are in flight at a time.
 template <class T, int KB>
-__global__ __launch_bounds__(256) void combine_kernel(MoveArgs a, int shift, int64_t segments) {
+__global__ __launch_bounds__(kMoveThreads) void combine_kernel(MoveArgs a, int shift, int64_t segments) {
   int64_t t, c;
   if (!move_place(a, shift, segments, t, c)) return;
   const int n = a.C - c < 8 ? (int)(a.C - c) : 8;
@@ -437,9 +440,9 @@ static void for_top_k(int K, bool f32, F f) {
 int launch_dispatch(const void* x, bool f32, int64_t T, int64_t C, const int32_t* rows, int K, const float* weights,
                     void* out, int64_t cap, hipStream_t stream) {
   const MoveShape s = move_shape(T, C);
-  if (s.blocks > kMostBlocks) return BSFP8_ERR_SHAPE;
+  if (s.blocks > kMostThreads / kMoveThreads) return BSFP8_ERR_SHAPE;
   const MoveArgs a{T, C, cap, K, rows, weights, x, nullptr, out, nullptr, nullptr, move_past(cap, C, f32)};
-  const dim3 grid((unsigned)s.blocks), block(256);
+  const dim3 grid((unsigned)s.blocks), block(kMoveThreads);
   if (f32) hipLaunchKernelGGL(dispatch_kernel<float>, grid, block, 0, stream, a, s.shift, s.segments);
   else hipLaunchKernelGGL(dispatch_kernel<uint16_t>, grid, block, 0, stream, a, s.shift, s.segments);
   return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
@@ -448,9 +451,9 @@ int launch_dispatch(const void* x, bool f32, int64_t T, int64_t C, const int32_t
 int launch_combine(const void* y, bool f32, int64_t cap, int64_t C, const int32_t* rows, int64_t T, int K,
                    const float* weights, const void* add, void* out, hipStream_t stream) {
   const MoveShape s = move_shape(T, C);
-  if (s.blocks > kMostBlocks) return BSFP8_ERR_SHAPE;
+  if (s.blocks > kMostThreads / kMoveThreads) return BSFP8_ERR_SHAPE;
   const MoveArgs a{T, C, cap, K, rows, weights, y, add, out, nullptr, nullptr, move_past(T, C, f32)};
-  const dim3 grid((unsigned)s.blocks), block(256);
+  const dim3 grid((unsigned)s.blocks), block(kMoveThreads);
   for_top_k(K, f32, [&](auto kb) {
     constexpr int KB = decltype(kb)::value;
     if (f32) hipLaunchKernelGGL((combine_kernel<float, KB>), grid, block, 0, stream, a, s.shift, s.segments);
@@ -471,7 +474,7 @@ int launch_combine_grad(const void* dout, bool f32, int64_t T, int64_t C, const 
   auto launch = [&](auto w, auto kb, auto y, auto o) {
     constexpr int W = decltype(w)::value, KB = decltype(kb)::value, THREADS = W == 1 ? 256 : 64 * W;
     constexpr bool Y = decltype(y)::value, O = decltype(o)::value;
-    const int64_t blocks = W == 1 ? (T + 3) / 4 : T, most = kMostBlocks / 2;
+    const int64_t blocks = W == 1 ? (T + 3) / 4 : T, most = kMostThreads / THREADS;
     const dim3 grid((unsigned)(blocks < most ? blocks : most)), block(THREADS);
     if (f32) hipLaunchKernelGGL((combine_grad_kernel<float, W, KB, Y, O>), grid, block, 0, stream, a);
     else hipLaunchKernelGGL((combine_grad_kernel<uint16_t, W, KB, Y, O>), grid, block, 0, stream, a);

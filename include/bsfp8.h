@@ -545,7 +545,7 @@ int bsfp8_dispatch_plan(const int32_t* experts, const float* probs, int64_t toke
  * weights  fp32 [tokens][top_k], or NULL (1: the rows are copied bit for bit)
  * Rows of out that no choice has are not written; no two choices have one row.  1 <= cols <= 2^24,
  * tokens * top_k <= 2^30, capacity_rows <= 2^31 - 1, and x is below 2^35 elements with cols rounded up to 8 2^n (above
- * 2048: to a multiple of 2048).  This is also the gradient of bsfp8_combine without weights.
+ * 1024: to a multiple of 1024).  This is also the gradient of bsfp8_combine without weights.
  */
 int bsfp8_dispatch(const void* x, int dtype, int64_t tokens, int64_t cols, const int32_t* rows, int32_t top_k,
                    const float* weights, void* out, int64_t capacity_rows, void* stream);
