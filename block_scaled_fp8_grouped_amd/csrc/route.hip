@@ -8,10 +8,11 @@
 // equal one more for the lowest expert that has it.
 //
 // What bounds them: 131072 tokens of 128 logits in fp32 are 67 MB, 11 us at 6.2 TB/s.  The choices' comparisons are about
-// 35 vector instructions a choice for 4 tokens, so the forward pass is bound by them: 44 us with the sums of the scores
-// (66 with both reductions at every choice, 49 with the scoring and the choices per lane looked up while running).  The
-// gradient reads and writes 134 MB, 22 us; a token's loads hang on each other (its choices, then their logits), so the
-// next token's are asked for ahead and the chosen logits of a row that the lanes hold come from LDS: 33 us (58 without).
+// 35 vector instructions a choice for 4 tokens, so the forward pass is bound by them: 39 us with the sums of the scores
+// (66 with both reductions at every choice; 49 with the scoring and the choices per lane looked up while running, 44 with
+// what is taken compared again and not kept as lane masks).  The gradient reads and writes 134 MB, 22 us; a token's
+// loads hang on each other (its choices, then their logits), so the next token's are asked for ahead and the chosen
+// logits of a row that the lanes hold come from LDS: 33 us (58 without).
 #include <math.h>
 
 #include <type_traits>
@@ -203,20 +204,31 @@ __global__ __launch_bounds__(256) void route_topk_kernel(RouteArgs a) {
       const bool open_ = best > kMasked;
       const uint32_t key = open_ ? best : 0xfffffffeu;  // (a number that no key has)
       // one of a token's keys is the largest, unless two are equal: then the lowest expert's is taken
-      int at = -1, found = 0;
+      uint64_t hit[V];
+      int found = 0;
 #pragma unroll
-      for (int v = V - 1; v >= 0; --v) {
-        const bool equal = u[v] == key;
-        found += __popcll(__ballot(equal));
-        at = equal ? v : at;
+      for (int v = 0; v < V; ++v) {
+        hit[v] = __ballot(u[v] == key);
+        found += __popcll(hit[v]);
       }
       if (found * G != __popcll(__ballot(open_))) {
-        const uint32_t e = min_over<G>(at < 0 ? 0xffffffffu : (uint32_t)(e0 + at));
-        at = e == (uint32_t)(e0 + at) ? at : -1;
+        uint32_t e = 0xffffffffu;
+#pragma unroll
+        for (int v = V - 1; v >= 0; --v) e = u[v] == key ? (uint32_t)(e0 + v) : e;
+        e = min_over<G>(e);
+#pragma unroll
+        for (int v = 0; v < V; ++v) hit[v] = __ballot(e == (uint32_t)(e0 + v));
+      }
+      uint64_t lanes = hit[0];
+      int at = e0;
+#pragma unroll
+      for (int v = 1; v < V; ++v) {
+        lanes |= hit[v];
+        at = __builtin_amdgcn_inverse_ballot_w64(hit[v]) ? e0 + v : at;
       }
 #pragma unroll
-      for (int v = 0; v < V; ++v) u[v] = at == v ? 0u : u[v];
-      if (at >= 0) taken[group][j] = e0 + at;
+      for (int v = 0; v < V; ++v) u[v] = __builtin_amdgcn_inverse_ballot_w64(hit[v]) ? 0u : u[v];
+      if (__builtin_amdgcn_inverse_ballot_w64(lanes)) taken[group][j] = at;
     }
     wave_order();
     int mine[P];

@@ -7,7 +7,7 @@ namespace bsfp8 {
 
 // Router: lanes per token (a row of 16 where 16 values a lane hold all experts, a wave above) and the workgroups of 4
 // waves, each walking every gridDim-th set of tokens: at most 8 per CU, as many as partial sums of the scores (131072
-// tokens, 128 experts: 44 us, with 4 per CU 47).  The gradient asks for its next tokens ahead and takes 4 per CU (33 us,
+// tokens, 128 experts: 44 us then, with 4 per CU 47).  The gradient asks for its next tokens ahead and takes 4 per CU (33 us,
 // with 8 per CU 35).
 inline int route_lanes(int experts) { return experts <= 256 ? 16 : 64; }
 inline int64_t route_blocks(int64_t tokens, int experts, bool grad = false) {
