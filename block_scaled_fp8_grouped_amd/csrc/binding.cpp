@@ -5,9 +5,9 @@
 // Every function answers None where an argument is not what the kernels take (another type, host memory, a wrong
 // shape, a size too small, an argument that the library refuses): the caller then takes its own path, which names
 // the argument in its error.  Nothing has been launched in that case.  A failed launch is answered with the
-// library's code instead: a kernel may have been queued before it, so the call must not be made again.  Four tokens of 7168 columns: 12.4 us per call of the
-// norms with the checks and the allocations in Python; four tokens' choices sorted 16.8 us there, 7.7 here, their rows' sum
-// 10.1 and 4.9.
+// library's code instead: a kernel may have been queued before it, so the call must not be made again.  Four tokens of
+// 7168 columns: 12.4 us per call of the norms with the checks and the allocations in Python; four tokens' choices sorted
+// 16.8 us there, 7.7 here, their rows' sum 10.1 and 4.9.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -403,7 +403,8 @@ PyObject* dispatch(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   if (!a.ok) Py_RETURN_NONE;
   Out out{a.tensor(x->scalar_type()), {}, true};
   const int64_t T = rows->size(0), K = rows->size(1), C = x->size(1), N = T * K;
-  if (!a.done() || K > BSFP8_MAX_TOP_K || !shaped(x, T, C) || !shaped(weights, T, K) || !shaped(out.given, N, C)) Py_RETURN_NONE;
+  if (!a.done() || K > BSFP8_MAX_TOP_K || !shaped(x, T, C) || !shaped(weights, T, K) || !shaped(out.given, N, C))
+    Py_RETURN_NONE;
   void* po = out.get([&] { return at::empty({N, C}, x->options()); });
   const int rc = bsfp8_dispatch(ptr(x), dtype_of(x), T, C, (const int32_t*)ptr(rows), (int32_t)K, (const float*)ptr(weights),
                                 po, N, (void*)a.stream);
@@ -429,7 +430,8 @@ struct MxBuffers {
 // (.., x, rows, choices, splits, recipe, which, four outputs, weights, status) -> True
 PyObject* dispatch_quantize(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   Call a(argv, argc);
-  const at::Tensor *x = a.matrix(BF16, at::kShort), *rows = a.matrix(I32, I32), *choices = a.tensor(I32), *splits = a.tensor(I32);
+  const at::Tensor *x = a.matrix(BF16, at::kShort), *rows = a.matrix(I32, I32);
+  const at::Tensor *choices = a.tensor(I32), *splits = a.tensor(I32);
   const int64_t recipe = a.integer(), which = a.integer();
   if (!a.ok || choices == nullptr || splits == nullptr) Py_RETURN_NONE;
   const int64_t T = rows->size(0), K = rows->size(1), C = x->size(1), N = T * K, E = splits->numel();
@@ -452,7 +454,8 @@ PyObject* combine(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   const at::Tensor* add = a.tensor(y->scalar_type());
   Out out{a.tensor(y->scalar_type()), {}, true};
   const int64_t T = rows->size(0), K = rows->size(1), C = y->size(1), N = T * K;
-  if (!a.done() || K > BSFP8_MAX_TOP_K || !shaped(y, N, C) || !shaped(weights, T, K) || !shaped(add, T, C) || !shaped(out.given, T, C))
+  if (!a.done() || K > BSFP8_MAX_TOP_K || !shaped(y, N, C) || !shaped(weights, T, K) || !shaped(add, T, C) ||
+      !shaped(out.given, T, C))
     Py_RETURN_NONE;
   void* po = out.get([&] { return at::empty({T, C}, y->options()); });
   const int rc = bsfp8_combine(ptr(y), dtype_of(y), N, C, (const int32_t*)ptr(rows), T, (int32_t)K,
@@ -472,8 +475,8 @@ PyObject* combine_grad(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   dy.wanted = a.truth();
   Out dw{a.tensor(F32), {}, weights != nullptr && y != nullptr};
   const int64_t T = rows->size(0), K = rows->size(1), C = dout->size(1), N = T * K;
-  if (!a.done() || K > BSFP8_MAX_TOP_K || !shaped(dout, T, C) || !shaped(y, N, C) || !shaped(weights, T, K) || !shaped(dy.given, N, C) ||
-      !shaped(dw.given, T, K) || (dw.given != nullptr && y == nullptr))
+  if (!a.done() || K > BSFP8_MAX_TOP_K || !shaped(dout, T, C) || !shaped(y, N, C) || !shaped(weights, T, K) ||
+      !shaped(dy.given, N, C) || !shaped(dw.given, T, K) || (dw.given != nullptr && y == nullptr))
     Py_RETURN_NONE;
   void* pd = dy.get([&] { return at::empty({N, C}, dout->options()); });
   float* pw = (float*)dw.get([&] { return at::empty({T, K}, weights->options()); });

@@ -157,8 +157,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanArgs a) {
   int32_t* next = at + wave * bins;
   const uint64_t below = (uint64_t(1) << lane) - 1;
   const int bits = 32 - __builtin_clz(bins);
-  // a chunk of one unit is put in order in LDS first, so that an expert's run leaves as whole lines (4 bytes each to where they go:
-  // 21.2 us for 1048576 choices, 17.4 with the order left out)
+  // a chunk of one unit is put in order in LDS first, so that an expert's run leaves as whole lines (4 bytes each to where
+  // they go: 20 us for 1048576 choices where this took 16)
   const bool whole = a.chunk == kPlanUnit;
   for (int64_t c0 = begin; c0 < end; c0 += 64 * kPlanSteps) {
     if (!whole) load(c0);

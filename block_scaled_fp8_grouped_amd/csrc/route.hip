@@ -88,7 +88,8 @@ __device__ __forceinline__ float sigmoid_stated(float l, float* other = nullptr)
   return s;
 }
 
-// exp(x) for x <= 0 from the hardware's 2^x: the product's rounding is an error of |x| 2^-24 of the result, which below 2^-126 is 0.
+// exp(x) for x <= 0 from the hardware's 2^x: the product's rounding is an error of |x| 2^-24 of the result, which below
+// 2^-126 is 0.
 __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 
 // Orders a wave's LDS accesses before its own later ones (no other wave is involved).

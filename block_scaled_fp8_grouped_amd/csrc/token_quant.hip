@@ -347,8 +347,8 @@ __device__ __forceinline__ void flush_cols(const LanePlace& l, int64_t block0, c
   for (int i = 0; i < kTCols * T::GRANULES / kTThreads; ++i) {
     const int g = i * kTThreads + (int)threadIdx.x, channel = g / T::GRANULES, k = g % T::GRANULES;
     const v4i w = *(const v4i*)(codes + channel * T::RUN + 16 * (k ^ T::swizzle(channel)));
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, w), rs,
-                                           (int)(channel < ncols ? (uint32_t)channel * run + 16u * (uint32_t)k : kNowhere), 0, kPastCaches);
+    const uint32_t to = channel < ncols ? (uint32_t)channel * run + 16u * (uint32_t)k : kNowhere;
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, w), rs, (int)to, 0, kPastCaches);
   }
 }
 
@@ -455,7 +455,8 @@ struct Turns {
     // T 2^32 / S is a multiple of 1 / S, at least 2^-17, and double is off by less: rounded up rightly.  S times it is T and
     // less than S / 2^32 more, so that the last step ends at T.
 #pragma unroll
-    for (int i = 0; i < V; ++i) rate[i] = tiles(k[i]) == most ? 0u : (uint32_t)ceil((double)tiles(k[i]) * 0x1p32 / (double)most);
+    for (int i = 0; i < V; ++i)
+      rate[i] = tiles(k[i]) == most ? 0u : (uint32_t)ceil((double)tiles(k[i]) * 0x1p32 / (double)most);
     return 0;
   }
   // tiles of the lane's group i, and of all, in the first j steps
@@ -823,9 +824,9 @@ __global__ __launch_bounds__(256) void token_dprobs_kernel(const float* partial,
   dprobs[r] = s;
 }
 
-// Column segments of a launch over `rows` row tiles and `cols` column tiles: as many as give kTFill workgroups, or twice that for
-// an activation's forward (2048 / 4096 / 8192 workgroups: SReLU of 65536 x 4096 300 / 278 / 264 us, its gradient
-// 352 / 335 / 328, SwiGLU's of 65536 x 2048 288 / 281 / 306, 65536 gathered rows of 4096 170 / 170 / 181).
+// Column segments of a launch over `rows` row tiles and `cols` column tiles: as many as give kTFill workgroups, or
+// twice that for an activation's forward (2048 / 4096 / 8192 workgroups: SReLU of 65536 x 4096 300 / 278 / 264 us, its
+// gradient 352 / 335 / 328, SwiGLU's of 65536 x 2048 288 / 281 / 306, 65536 gathered rows of 4096 170 / 170 / 181).
 struct TokenSegments {
   int64_t count, tiles;
 };

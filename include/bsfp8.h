@@ -502,7 +502,8 @@ int bsfp8_adamw_step_stochastic(const void* device_plan, int32_t num_tensors, in
  * score_sum fp32 [num_experts] or NULL: sum of s[t][e] over the tokens, added in a fixed order
  * workspace bsfp8_route_topk_workspace_bytes() bytes of device memory, needed with score_sum
  * 1 <= num_experts <= BSFP8_MAX_GROUPS, 1 <= top_k <= min(num_experts, BSFP8_MAX_TOP_K), tokens * top_k <= 2^30.  The
- * logits begin at a multiple of 16 bytes, rows of any length follow one another.  tokens == 0 writes nothing but zeros to score_sum.
+ * logits begin at a multiple of 16 bytes, rows of any length follow one another.  tokens == 0 writes nothing but zeros
+ * to score_sum.
  */
 size_t bsfp8_route_topk_workspace_bytes(int64_t tokens, int32_t num_experts);
 int bsfp8_route_topk(const void* logits, int logits_dtype, int64_t tokens, int32_t num_experts, int32_t top_k,
