@@ -12,7 +12,7 @@
 // What bounds them: bytes, which come and go at 6.2 TB/s at best, and the instructions that the conversions to codes in two
 // directions take.  65536 gathered rows of 4096 (32 experts, 4 a token) read 134 MB and write 553 MB, 111 us: 169 us.  The
 // SwiGLU's gradient of 65536 x 2048 reads 545 MB and writes 690 MB, 200 us: 281 us, at the 256 registers that leave two
-// waves a SIMD.  Activation and kept input of 4099 x 4128, 88 MB: 14 us of bytes in 27 us, 1320 workgroups at 1024 places.
+// waves a SIMD.  Activation and kept input of 4099 x 4128, 88 MB: 14 us of bytes in 22 us, 1320 workgroups at 1024 places.
 #include <math.h>
 
 #include <type_traits>
@@ -27,8 +27,9 @@
 namespace bsfp8 {
 
 // Codes go past the caches (a line's 128 bytes leave together, and none is read again here): 181 -> 170 us on 65536
-// gathered rows of 4096, whose tokens then stay in them; 288 -> 279 us on the SwiGLU's gradient.
-constexpr int kPastCaches = 2;
+// gathered rows of 4096, whose tokens then stay in them; 288 -> 279 us on the SwiGLU's gradient.  An activation's rowwise
+// codes, which the next product reads, stay in them (SReLU of 4099 x 4128 26.9 -> 22.2 us, layers the same).
+constexpr int kInCaches = 0, kPastCaches = 2;
 constexpr int kTThreads = 256;
 
 // An activation's forward or gradient.
@@ -267,14 +268,14 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
   const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32));
   return (int64_t)((uint64_t)hi << 32 | lo);
 }
-template <bool F4>
+template <int AUX, bool F4>
 __device__ __forceinline__ void store_codes(__amdgpu_buffer_rsrc_t rs, uint32_t off, const Codes<F4>& q) {
-  if constexpr (F4) __builtin_amdgcn_raw_buffer_store_b32((int)q.w[0], rs, (int)off, 0, kPastCaches);
-  else __builtin_amdgcn_raw_buffer_store_b64(v2i{(int)q.w[0], (int)q.w[1]}, rs, (int)off, 0, kPastCaches);
+  if constexpr (F4) __builtin_amdgcn_raw_buffer_store_b32((int)q.w[0], rs, (int)off, 0, AUX);
+  else __builtin_amdgcn_raw_buffer_store_b64(v2i{(int)q.w[0], (int)q.w[1]}, rs, (int)off, 0, AUX);
 }
 
 // The values along their rows: codes into q [R][width] from channel c0 on, scales into s [width / 32][R].
-template <bool F4, class V>
+template <bool F4, int AUX = kPastCaches, class V>
 __device__ __forceinline__ void put_rows(const LanePlace& l, uint8_t* q, uint8_t* s, uint32_t width, int64_t c0, const V& x) {
   constexpr int PER = F4 ? 2 : 1;
   uint32_t m[8], top[2];
@@ -289,7 +290,7 @@ __device__ __forceinline__ void put_rows(const LanePlace& l, uint8_t* q, uint8_t
     const uint32_t b = byte[i >> 2];
     const uint32_t of = i % 4 == 0 ? quad_lane<0>(b) : i % 4 == 1 ? quad_lane<1>(b) : i % 4 == 2 ? quad_lane<2>(b)
                                                                                               : quad_lane<3>(b);
-    store_codes<F4>(row_buffer(at, i, width / PER, l.live), off, x.template row_codes<F4>(i, of));
+    store_codes<AUX>(row_buffer(at, i, width / PER, l.live), off, x.template row_codes<F4>(i, of));
   }
   // the quad has its block's 8 scales, two a lane
   const int r = l.ch & 3;
@@ -605,7 +606,8 @@ __global__ __launch_bounds__(kTThreads, mode_grad(MODE) ? 2 : 1) void act_checkp
   constexpr bool GRAD = mode_grad(MODE), GLU = mode_glu(MODE);
   constexpr int W = kTCols, HALVES = GLU ? 2 : 1, OUTS = GRAD ? HALVES : 1;
   __shared__ GroupScanSmem<kTThreads> gsm;
-  __shared__ __attribute__((aligned(16))) uint8_t codes[2][W * ColTile<F4>::RUN];
+  constexpr int BUFFERS = GRAD ? 2 : 1;  // (the forward's one array a tile: SwiGLU of 65536 x 2048 226 us with two, 220 with one)
+  __shared__ __attribute__((aligned(16))) uint8_t codes[BUFFERS][W * ColTile<F4>::RUN];
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int64_t rt = blockIdx.x / (uint32_t)a.segments, seg = blockIdx.x % (uint32_t)a.segments;
   const bool row_out = a.row_q != nullptr, col_out = a.col_q != nullptr;
@@ -684,12 +686,13 @@ __global__ __launch_bounds__(kTThreads, mode_grad(MODE) ? 2 : 1) void act_checkp
   const int64_t begin = seg * a.tiles * W, stop = begin + (int64_t)a.tiles * W, end = stop < F ? stop : F;
   // the colwise layout of a tile's values: `half` of the `width` channels from c0 on
   auto cols = [&](uint8_t* q, uint8_t* s, uint32_t width, int64_t c0, int64_t half, auto& values) {
+    if (BUFFERS == 1 && c0 != begin) __syncthreads();  // (the tile before is out)
     put_cols<F4>(l, wave, codes[turn], s, width, half + c0, values);
     // (two buffers: a wave that fills the one of the array after next has passed the next one's barrier, which every wave
     // reaches with its part of this one read)
     __syncthreads();
     flush_cols<F4>(l, l.block - wave, codes[turn], q, width, half + c0, F - c0 < W ? (int)(F - c0) : W);
-    turn ^= 1;
+    turn = (turn + 1) % BUFFERS;
   };
   for (int64_t c0 = begin; c0 < end; c0 += W) {
     l.live_col = c0 + l.ch * 8 < F;
@@ -709,7 +712,7 @@ __global__ __launch_bounds__(kTThreads, mode_grad(MODE) ? 2 : 1) void act_checkp
         }
       }
       __builtin_amdgcn_sched_barrier(0);
-      if (row_out) put_rows<F4>(l, a.row_q, a.row_s, C, c0, y);
+      if (row_out) put_rows<F4, kInCaches>(l, a.row_q, a.row_s, C, c0, y);
       if (col_out) cols(a.col_q, a.col_s, C, c0, 0, y);
     } else {
       // one array of values at a time, worked out from the inputs and the sigmoids, which stay
