@@ -303,3 +303,31 @@ def test_more_tokens_than_a_launch_has_waves():
     assert torch.equal(d["dweights"], x * y.flip(0)) and torch.equal(d["dy"], (x * w).flip(0))
     assert torch.equal(bs.combine(y, {"rows": rows}, w), y.flip(0) * w)
     assert torch.equal(bs.dispatch(x, {"rows": rows}), x.flip(0))
+
+
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+@pytest.mark.parametrize("cols", [1, 8, 513, 576, 577, 1025, 1152, 1153, 2050, 2305, 4097, 8200])
+@pytest.mark.parametrize("tokens,k", [(3, 1), (65, 5)])
+def test_gradient_of_sums_at_every_width(dtype, cols, tokens, k):
+    """Rows of one wave, of several and of several passes.  A product is rounded once (half a step); a weight's gradient is a
+    chain of at most 8 ceil(cols / 512) products a lane, 6 steps and 8 waves in fp32."""
+    g = torch.Generator(device=DEV).manual_seed(cols)
+    rand = lambda *s: torch.randn(s, generator=g, device=DEV)  # noqa: E731
+    rows = torch.randperm(tokens * k, generator=g, device=DEV).to(torch.int32).view(tokens, k)
+    rows[0, 0] = -1
+    x, y, w = rand(tokens, cols).to(dtype), rand(tokens * k, cols).to(dtype), rand(tokens, k)
+    dy = torch.full_like(y, 7.0)
+    d = bs.combine_grad(x, {"rows": rows}, y=y, weights=w, dy=dy)
+    live = rows >= 0
+    at = rows[live].long()
+    want = (x.double()[:, None] * w.double()[..., None])[live]
+    assert ((dy[at].double() - want).abs() <= (torch.finfo(dtype).eps / 2 + 2.0 ** -24) * want.abs()).all()
+    left = torch.ones(tokens * k, dtype=torch.bool, device=DEV)
+    left[at] = False
+    assert int(left.sum()) == 1 and bool((dy[left] == 7).all())
+    terms = (x.double()[:, None] * torch.ones_like(w.double())[..., None])[live] * y[at].double()
+    bound = (8 * ((cols + 511) // 512) + 14) * 2.0 ** -24 * terms.abs().sum(1)
+    assert ((d["dweights"][live].double() - terms.sum(1)).abs() <= bound).all() and float(d["dweights"][0, 0]) == 0
+    assert torch.equal(bs.combine_grad(x, {"rows": rows}, y=y, weights=w, dy=False)["dweights"], d["dweights"])
+    again = bs.combine_grad(x, {"rows": rows}, y=y, weights=w, dy=y)  # (dy over y)
+    assert torch.equal(again["dweights"], d["dweights"]) and torch.equal(y[at], dy[at])
