@@ -9,8 +9,7 @@ namespace bsfp8 {
 // 2^x in fp32 by a stated algorithm every IEEE fp32 machine reproduces bit for bit: x clamped to
 // [-126, 126]; k = floor(x + 1/2), r = x - k (exact); the degree-7 Taylor polynomial of
 // exp(r ln 2) (coefficients (ln 2)^n / n! in fp32, Horner order, no fused multiply-add) times 2^k.
-__device__ __forceinline__ float exp2_stated(float x) {
-  x = x > 126.0f ? 126.0f : (x < -126.0f ? -126.0f : x);
+__device__ __forceinline__ float exp2_clamped(float x) {
   const float kf = floorf(x + 0.5f);  // an integer in [-126, 126]: exact as fp32 and as int
   const int k = (int)kf;
   const float r = x - kf;
@@ -23,6 +22,9 @@ __device__ __forceinline__ float exp2_stated(float x) {
   poly = poly * r + 0.693147182f;
   poly = poly * r + 1.0f;
   return ldexpf(poly, k);
+}
+__device__ __forceinline__ float exp2_stated(float x) {
+  return exp2_clamped(x > 126.0f ? 126.0f : (x < -126.0f ? -126.0f : x));
 }
 
 // The activations between fc1 and fc2 (TE #3484: fc1 -> ScaledSReLU / ScaledSwiGLU -> fc2 with

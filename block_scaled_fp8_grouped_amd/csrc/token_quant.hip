@@ -11,8 +11,9 @@
 //
 // What bounds them: bytes, which come and go at 6.2 TB/s at best, and the instructions that the conversions to codes in two
 // directions take.  65536 gathered rows of 4096 (32 experts, 4 a token) read 134 MB and write 553 MB, 111 us: 169 us.  The
-// SwiGLU's gradient of 65536 x 2048 reads 545 MB and writes 690 MB, 200 us: 281 us, at the 256 registers that leave two
-// waves a SIMD.  Activation and kept input of 4099 x 4128, 88 MB: 14 us of bytes in 22 us, 1320 workgroups at 1024 places.
+// SwiGLU's gradient of 65536 x 2048 reads 545 MB and writes 690 MB, 200 us: 318 us, at the 256 registers that leave two
+// waves a SIMD, and with 25 vector instructions for a sigmoid by the forward's steps (278 us with 4, from the hardware's
+// exponential and reciprocal, which put codes next to a border on its other side: 110 of 268 million).  Activation and kept input of 4099 x 4128, 88 MB: 14 us of bytes in 22 us, 1320 workgroups at 1024 places.
 #include <math.h>
 
 #include <type_traits>
@@ -372,6 +373,12 @@ __device__ __forceinline__ void unpack_codes(const v2i& w, uint32_t byte, float 
 template <class T>
 __device__ __forceinline__ void keep(T& v) {
   asm volatile("" : "+v"(v));
+}
+
+// The sigmoid of act_value's SwiGLU and of glu_grad, step for step, the clamp in one instruction: it takes a bound for a NaN,
+// whose products with a stay NaN.
+__device__ __forceinline__ float act_sigmoid(float a) {
+  return recip_rn(1.0f + exp2_clamped(__builtin_amdgcn_fmed3f(-a * 1.44269502f, -126.0f, 126.0f)));
 }
 
 // 8 consecutive scale bytes of a column of blocks, of which n are there.
@@ -741,7 +748,7 @@ __global__ __launch_bounds__(kTThreads, mode_grad(MODE) ? 2 : 1) void act_checkp
             const float r = h[k] > 0.0f ? h[k] : 0.0f;
             val = r * r;
           } else {
-            sg.v[i][k] = sigmoid_fast(h[k]);
+            sg.v[i][k] = act_sigmoid(h[k]);
             keep(sg.v[i][k]);
             val = h[k] * sg.v[i][k] * b[k];
           }
@@ -777,8 +784,8 @@ __global__ __launch_bounds__(kTThreads, mode_grad(MODE) ? 2 : 1) void act_checkp
               const float r = h[k] > 0.0f ? h[k] : 0.0f;
               y.v[i][k] = 2.0f * r * prob[i] * d[k];
             } else {
-              const float s = sg.v[i][k], sl = h[k] * s;
-              y.v[i][k] = d[k] * prob[i] * b[k] * (s + __builtin_fmaf(-sl, s, sl));
+              const float s = sg.v[i][k];
+              y.v[i][k] = d[k] * prob[i] * b[k] * (s * (1.0f + h[k] * (1.0f - s)));
             }
             keep(y.v[i][k]);
           }

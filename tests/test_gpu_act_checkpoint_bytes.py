@@ -1,0 +1,62 @@
+"""The gradient of an activation kept in 8 bits is that of the values kept, step for step: the bytes that
+grouped_act_quantize writes for its gradient at those values, and for the activation again.  (A kept value has four
+significant bits, so bf16 holds it.)  No tolerance: the same operations in the same order."""
+import pytest
+import torch
+
+import block_scaled_fp8_grouped_amd as bs
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+MX, MX4 = bs.RECIPE_MX, bs.RECIPE_MX4
+ROW, COL, BOTH = bs.ROWWISE, bs.COLWISE, bs.ROWWISE | bs.COLWISE
+GRAD = {bs.ACT_SRELU: bs.ACT_SRELU_GRAD, bs.ACT_SWIGLU: bs.ACT_SWIGLU_GRAD}
+
+
+def zeroed(rows, cols, experts, recipe, which):
+    q = bs.alloc_quantized(rows, cols, experts, recipe, which, DEV)
+    for t in q.values():
+        t.zero_()
+    return q
+
+
+def kept_of(h, live):
+    """h[:live] in 8 bits, and the values that those stand for."""
+    st = torch.tensor([live], dtype=torch.int32, device=DEV)
+    kept = bs.grouped_quantize(h, st, MX, ROW, zeroed(h.shape[0], h.shape[1], 1, MX, ROW))
+    scale = torch.exp2(kept["row_s"].t().float() - 127).repeat_interleave(32, 1)
+    return kept, (kept["row_q"].view(torch.float8_e4m3fn).float() * scale).bfloat16()
+
+
+def draw(splits, cols, act, pad, seed, wide=3.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    live = sum(splits)
+    rows, both = live + pad, cols * (2 if act == bs.ACT_SWIGLU else 1)
+    h = (torch.randn((rows, both), generator=g, device=DEV) * wide).bfloat16()
+    dy = (torch.randn((rows, cols), generator=g, device=DEV) * 0.01).bfloat16()
+    p = torch.rand(rows, generator=g, device=DEV)
+    return h, dy, p, torch.tensor(splits, dtype=torch.int32, device=DEV)
+
+
+def both_ways(act, h, dy, p, st, recipe):
+    """(the gradient's layouts, the activation's again) from what is kept, and from the separate calls."""
+    (rows, wide), cols, experts = h.shape, dy.shape[1], st.numel()
+    kept, values = kept_of(h, int(st.sum()))
+    q, y = zeroed(rows, wide, experts, recipe, BOTH), zeroed(rows, cols, experts, recipe, COL)
+    bs.grouped_act_checkpoint_grad(act, kept, dy, st, recipe, BOTH, q, p, y)
+    want_q = bs.grouped_act_quantize(GRAD[act], values, st, recipe, BOTH, zeroed(rows, wide, experts, recipe, BOTH), p, dy)
+    want_y = bs.grouped_act_quantize(act, values, st, recipe, COL, zeroed(rows, cols, experts, recipe, COL), p)
+    return (q, want_q), (y, want_y)
+
+
+@pytest.mark.parametrize("splits,cols,pad", [([1], 32, 0), ([200, 0, 33, 128, 1], 160, 7), ([3000, 1097], 1056, 3),
+                                             ([0, 4096, 129], 2048, 0)])
+@pytest.mark.parametrize("act", [bs.ACT_SRELU, bs.ACT_SWIGLU])
+@pytest.mark.parametrize("recipe", [MX, MX4])
+@pytest.mark.parametrize("wide", [1.0, 30.0])
+def test_gradient_is_that_of_the_separate_call(splits, cols, pad, act, recipe, wide):
+    """Sigmoids near 1/2 and out to their ends; a code next to the border of two shows any other arithmetic."""
+    h, dy, p, st = draw(splits, cols, act, pad, 1, wide)
+    for got, want in both_ways(act, h, dy, p, st, recipe):
+        for name in want:
+            assert torch.equal(got[name], want[name]), f"{name}: {int((got[name] != want[name]).sum())} bytes"
