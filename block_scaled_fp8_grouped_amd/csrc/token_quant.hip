@@ -516,6 +516,31 @@ struct Turns {
   }
 };
 
+// The sum of the sizes where the groups' places do not matter, and what is wrong with them.  Every wave works it out by
+// itself; capacity below 2^24.
+__device__ __forceinline__ uint32_t live_rows(const int32_t* __restrict__ splits, int E, int capacity, int& total) {
+  const int lane = threadIdx.x & 63;
+  bool negative = false, large = false;
+  int rows = 0;  // a lane's at most 16 sizes, each at most the capacity
+  auto read = [&](auto n) {  // all loads in flight
+    int v[decltype(n)::value];
+#pragma unroll
+    for (int i = 0; i < decltype(n)::value; ++i) v[i] = 64 * i + lane < E ? splits[64 * i + lane] : 0;
+#pragma unroll
+    for (int i = 0; i < decltype(n)::value; ++i) {
+      negative |= v[i] < 0;
+      large |= v[i] > capacity;
+      rows += v[i] < 0 || v[i] > capacity ? 0 : v[i];
+    }
+  };
+  if (E <= 256) read(std::integral_constant<int, 4>());
+  else read(std::integral_constant<int, 16>());
+  large |= rows > capacity;
+  total = wave_total(rows > capacity ? 0 : rows);  // at most 64 times the capacity
+  return (__ballot(negative) != 0 ? BSFP8_STATUS_NEGATIVE_SPLIT : 0u) |
+         (__ballot(large) != 0 || total > capacity ? BSFP8_STATUS_EXCEEDS_CAPACITY : 0u);
+}
+
 // Rows of tokens: a row tile's column segment, the row tiles in the order of Turns (V > 0), or as they lie (V == 0: rowwise
 // only, few rows, no need of the groups).
 template <bool WEIGHTED, bool F4, int V>
@@ -531,11 +556,18 @@ __global__ __launch_bounds__(kTThreads) void dispatch_quantize_kernel(TokenQuant
   l.rl = lane >> 4;
   l.R = a.R;
   Turns<V ? V : 1> turns;
-  if constexpr (V > 0) {
-    const uint32_t flags = turns.read(a.splits, a.E, a.R);
-    report_status(a.status, flags);
-    if (flags) return;
+  int32_t near[8];  // (V == 0: the lane's choices, asked for beside the sizes)
+  if constexpr (V == 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t r = m * 128 + 32 * wave + 8 * l.rl + i;
+      near[i] = r < a.R ? a.choices[r] : -1;
+    }
   }
+  int total = 0;
+  const uint32_t flags = V > 0 ? turns.read(a.splits, a.E, a.R) : live_rows(a.splits, a.E, (int)a.R, total);
+  report_status(a.status, flags);
+  if (flags) return;
   int64_t left;
   if constexpr (V > 0) {
     int rows, first, p, tile;
@@ -549,7 +581,7 @@ __global__ __launch_bounds__(kTThreads) void dispatch_quantize_kernel(TokenQuant
   } else {
     l.row0 = m * 128 + 32 * wave;
     l.p = l.kp = l.block = 0;
-    left = a.R - l.row0;
+    left = total - l.row0;
   }
   l.live = (int)(left < 0 ? 0 : left < 32 ? left : 32);
   left -= 8 * l.rl;
@@ -559,7 +591,7 @@ __global__ __launch_bounds__(kTThreads) void dispatch_quantize_kernel(TokenQuant
   int there = 0;  // rows up to the first without a choice
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int64_t c = i < l.nl ? (int64_t)a.choices[l.row0 + 8 * l.rl + i] : -1;
+    const int64_t c = i >= l.nl ? -1 : V == 0 ? near[i] : a.choices[l.row0 + 8 * l.rl + i];
     const bool ok = c >= 0 && c < a.tokens * a.K;
     there = ok && there == i ? i + 1 : there;
     src[i] = ok ? a.in + (int64_t)((uint32_t)c / (uint32_t)a.K) * F + l.ch * 8 : nullptr;
