@@ -588,23 +588,12 @@ __global__ __launch_bounds__(kTThreads) void dispatch_quantize_kernel(TokenQuant
   l.nl = (int)(left < 0 ? 0 : left < 8 ? left : 8);
   const uint16_t* src[8];
   float weight[8];
-  int there = 0;  // rows up to the first without a choice
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t c = i >= l.nl ? -1 : V == 0 ? near[i] : a.choices[l.row0 + 8 * l.rl + i];
-    const bool ok = c >= 0 && c < a.tokens * a.K;
-    there = ok && there == i ? i + 1 : there;
+    const bool ok = c >= 0 && c < a.tokens * a.K;  // (another choice: a row of zeros)
     src[i] = ok ? a.in + (int64_t)((uint32_t)c / (uint32_t)a.K) * F + l.ch * 8 : nullptr;
     weight[i] = WEIGHTED && ok ? a.probs[c] : 1.0f;
-  }
-  if constexpr (V == 0) {  // rows without a choice are not stored
-    l.nl = there;
-    l.live = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int n = __builtin_amdgcn_readlane(there, 16 * k);
-      l.live = l.live == 8 * k ? 8 * k + n : l.live;
-    }
   }
   int turn = 0;
   const int64_t begin = seg * a.tiles * W, stop = begin + (int64_t)a.tiles * W, end = stop < F ? stop : F;

@@ -555,7 +555,8 @@ int bsfp8_dispatch(const void* x, int dtype, int64_t tokens, int64_t cols, const
  * The same rows straight into the quantized layouts of bsfp8_grouped_quantize for [capacity_rows][cols]: the bytes
  * that it writes for the rows of bsfp8_dispatch, except that weighted rows are quantized from their fp32 products.
  * x_bf16    [tokens][cols] bf16
- * choices   int32 [capacity_rows], as bsfp8_dispatch_plan writes them.  Rows at or past sum(split_sizes) are not written
+ * choices   int32 [capacity_rows], as bsfp8_dispatch_plan writes them.  Rows at or past sum(split_sizes) are not written; a
+ *           row before it whose choice lies outside [0, tokens * top_k) is one of zeros
  * recipe    BSFP8_RECIPE_MX_1X32_E8M0 or BSFP8_RECIPE_MXFP4_1X32_E8M0
  * split_sizes  as bsfp8_dispatch_plan writes them
  * capacity_rows + 127 must stay below 2^24 - 128, as for bsfp8_grouped_gemm_wgrad, here and in the two calls below that

@@ -74,3 +74,26 @@ def test_few_rows_and_many(rows, experts, recipe):
     want = bs.grouped_quantize(x[plan["choices"].long()], plan["splits"], recipe, ROW, poisoned(rows, 160, experts, recipe, ROW))
     for name in want:
         assert torch.equal(got[name], want[name]), name
+
+
+@pytest.mark.parametrize("tokens,experts,k", [(3, 1, 2), (50, 7, 3), (1365, 9, 3), (2047, 300, 2), (4096, 33, 1), (3000, 128, 4)])
+@pytest.mark.parametrize("recipe,which", [(MX, ROW), (MX4, ROW), (MX, BOTH), (MX4, BOTH)])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_a_row_without_a_choice_is_zeros(tokens, experts, k, recipe, which, weighted):
+    """Choices outside [0, tokens * top_k) before the last row: that row alone is zeros, codes and scales of the rows behind
+    it are theirs.  (Weights that are powers of two make the products exact in bf16.)"""
+    plan, x, _ = routed(tokens, experts, k, 96, 3)
+    n = tokens * k
+    g = torch.Generator(device=DEV).manual_seed(4)
+    gone = torch.rand(n, generator=g, device=DEV) < 0.3
+    gone[n // 3] = True
+    plan["choices"][gone] = torch.tensor([-1, n, -9, 1 << 30, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32, device=DEV)[
+        torch.randint(0, 6, (int(gone.sum()),), generator=g, device=DEV)]
+    w = torch.exp2(torch.randint(-3, 4, (tokens, k), generator=g, device=DEV).float()) if weighted else None
+    c = torch.where(gone, 0, plan["choices"]).long()
+    rows = x[c // k] * (w.view(-1)[c].bfloat16()[:, None] if weighted else 1)
+    rows[gone] = 0
+    got = bs.dispatch_quantize(x, plan, recipe, which, poisoned(n, 96, experts, recipe, which), weights=w)
+    want = bs.grouped_quantize(rows, plan["splits"], recipe, which, poisoned(n, 96, experts, recipe, which))
+    for name in want:
+        assert torch.equal(got[name], want[name]), name
