@@ -26,7 +26,7 @@ def routed(tokens, experts, k, cols, seed=0):
     return bs.dispatch_plan(e, experts), x, w
 
 
-@pytest.mark.parametrize("tokens", [1, 40, 2047, 2048, 3000])
+@pytest.mark.parametrize("tokens", [1, 40, 2047, 2048, 16383, 16384])
 @pytest.mark.parametrize("experts", [1, 7, 65, 257, 1024])
 @pytest.mark.parametrize("recipe,which", [(MX, ROW), (MX4, ROW), (MX, BOTH)])
 def test_bad_sizes_set_the_status_and_write_nothing(tokens, experts, recipe, which):
@@ -48,7 +48,7 @@ def test_bad_sizes_set_the_status_and_write_nothing(tokens, experts, recipe, whi
                 assert int(status) == bits and all((t == 0xEE).all() for t in q.values()), (at, bad)
 
 
-@pytest.mark.parametrize("tokens,experts,k", [(3, 2, 1), (40, 7, 3), (1000, 65, 4), (1365, 9, 3), (4096, 33, 1), (2500, 300, 2)])
+@pytest.mark.parametrize("tokens,experts,k", [(3, 2, 1), (40, 7, 3), (1000, 65, 4), (1365, 9, 3), (4096, 33, 1), (2500, 300, 2), (20000, 40, 2)])
 @pytest.mark.parametrize("recipe,which", [(MX, ROW), (MX4, ROW), (MX, BOTH)])
 @pytest.mark.parametrize("cols", [32, 160])
 def test_rows_past_the_sizes_are_left(tokens, experts, k, recipe, which, cols):
@@ -65,7 +65,7 @@ def test_rows_past_the_sizes_are_left(tokens, experts, k, recipe, which, cols):
         assert torch.equal(got[name], want[name]), name
 
 
-@pytest.mark.parametrize("rows", [1, 31, 32, 127, 129, 4095, 4096, 4097, 9000])
+@pytest.mark.parametrize("rows", [1, 31, 32, 127, 129, 4095, 4097, 32767, 32768, 40001])
 @pytest.mark.parametrize("experts", [1, 64, 65, 256, 257])
 @pytest.mark.parametrize("recipe", [MX, MX4])
 def test_few_rows_and_many(rows, experts, recipe):
@@ -76,7 +76,7 @@ def test_few_rows_and_many(rows, experts, recipe):
         assert torch.equal(got[name], want[name]), name
 
 
-@pytest.mark.parametrize("tokens,experts,k", [(3, 1, 2), (50, 7, 3), (1365, 9, 3), (2047, 300, 2), (4096, 33, 1), (3000, 128, 4)])
+@pytest.mark.parametrize("tokens,experts,k", [(3, 1, 2), (50, 7, 3), (1365, 9, 3), (2047, 300, 2), (4096, 33, 1), (3000, 128, 4), (10000, 128, 4)])
 @pytest.mark.parametrize("recipe,which", [(MX, ROW), (MX4, ROW), (MX, BOTH), (MX4, BOTH)])
 @pytest.mark.parametrize("weighted", [False, True])
 def test_a_row_without_a_choice_is_zeros(tokens, experts, k, recipe, which, weighted):
