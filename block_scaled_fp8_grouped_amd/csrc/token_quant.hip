@@ -129,7 +129,8 @@ __device__ __forceinline__ Codes<F4> codes_of(const float (&v)[8], uint32_t byte
 
 // A lane's 8 rows x 8 channels: as fp32, or (bf16 inputs as they are) pairs of channels.  Largest magnitudes are those of
 // bit patterns where the bytes have to be grouped_quantize's (a NaN block has an infinity's scale there), or (FLOAT:
-// gradients) fp32 maxima, which pass over a NaN and take the magnitude for nothing.
+// MXFP8 gradients) fp32 maxima, which pass over a NaN, whose code stays one, and take the magnitude for nothing.  e2m1 has no
+// NaN: an MXFP4 block shows one by its scale alone.
 template <bool FLOAT>
 struct Values {
   float v[8][8];
@@ -744,7 +745,7 @@ __global__ __launch_bounds__(kTThreads, mode_grad(MODE) ? 2 : 1) void act_checkp
       if (col_out) cols(a.col_q, a.col_s, C, c0, 0, y);
     } else {
       // one array of values at a time, worked out from the inputs and the sigmoids, which stay
-      Values<true> y, sg;
+      Values<!F4> y, sg;
       float d[8], h[8], b[8];
       auto inputs = [&](int i) {
         keep(x.k0[i]);

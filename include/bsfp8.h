@@ -611,7 +611,8 @@ int bsfp8_grouped_act_checkpoint(int activation, const void* h_bf16, const float
 /*
  * The gradient from what was kept.  With h the values that kept_q and kept_s stand for, r = max(h, 0),
  * sg = 1 / (1 + exp2s(-a * log2(e))), in fp32, by the operations of bsfp8_grouped_act_quantize in their order (the bytes
- * that it writes for the gradient, and for the activation, of these values):
+ * that it writes for the gradient, and for the activation, of these values; a NaN has an MXFP8 NaN code, where the scale is
+ * that of its block's other values, and gives an MXFP4 block the scale of an infinity):
  *     SReLU:   g = 2 r p dy                          quantized as [capacity_rows][cols]
  *              v = r^2
  *     SwiGLU:  (da | db) = (dy p b sg (1 + a (1 - sg)) | dy p a sg)        as [capacity_rows][2 cols]

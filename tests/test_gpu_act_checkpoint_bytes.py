@@ -60,3 +60,40 @@ def test_gradient_is_that_of_the_separate_call(splits, cols, pad, act, recipe, w
     for got, want in both_ways(act, h, dy, p, st, recipe):
         for name in want:
             assert torch.equal(got[name], want[name]), f"{name}: {int((got[name] != want[name]).sum())} bytes"
+
+
+@pytest.mark.parametrize("act", [bs.ACT_SRELU, bs.ACT_SWIGLU])
+@pytest.mark.parametrize("where", ["dy", "probs", "kept"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_values_that_are_not_finite_reach_an_mxfp4_blocks_scale(act, where, value):
+    """4-bit codes have no NaN: it shows in the block's scale, as in the separate call.  (A kept infinity is a NaN.)"""
+    h, dy, p, st = draw([300, 129], 96, act, 0, 2)
+    for r, c in ((0, 0), (45, 31), (299, 64), (300, 95), (428, 33)):
+        if where == "kept":
+            h[r, c] = value
+        elif where == "dy":
+            dy[r, c] = value
+        else:
+            p[r] = value
+    (q, want_q), (y, want_y) = both_ways(act, h, dy, p, st, MX4)
+    for got, want in ((q, want_q), (y, want_y)):
+        for name in want:
+            assert torch.equal(got[name], want[name]), f"{name}: {int((got[name] != want[name]).sum())} bytes"
+    if where != "kept" or act == bs.ACT_SWIGLU:  # (the squared ReLU of a NaN is 0)
+        marked = want_q["row_s"].max()
+        assert int(marked) >= 252 and int((want_q["row_s"] == marked).sum()) >= 5  # 2^125 and more
+
+
+@pytest.mark.parametrize("act", [bs.ACT_SRELU, bs.ACT_SWIGLU])
+def test_a_nan_keeps_its_mxfp8_code_and_its_blocks_scale(act):
+    h, dy, p, st = draw([64], 64, act, 0, 3)
+    at = dy.abs().view(64, 2, 32).argmin(2)[:, 0]  # no block's largest
+    r = torch.arange(64, device=DEV)
+    h[r, at] = h[r, at].abs() + 1  # (the squared ReLU passes it on)
+    clean = both_ways(act, h, dy, p, st, MX)[0][0]
+    dy[r, at] = float("nan")
+    got = both_ways(act, h, dy, p, st, MX)[0][0]
+    code = got["row_q"].view(torch.float8_e4m3fn).float()
+    assert code[r, at].isnan().all() and int(code.isnan().sum()) == 64 * (1 if act == bs.ACT_SRELU else 2)
+    same = ~code.isnan()
+    assert torch.equal(got["row_q"][same], clean["row_q"][same]) and torch.equal(got["row_s"], clean["row_s"])
