@@ -8,7 +8,7 @@
 // equal one more for the lowest expert that has it.
 //
 // What bounds them: 131072 tokens of 128 logits in fp32 are 67 MB, 11 us at 6.2 TB/s.  The choices' comparisons are about
-// 35 vector instructions a choice for 4 tokens, so the forward pass is bound by them: 39 us with the sums of the scores
+// 35 vector instructions a choice for 4 tokens, so the forward pass is bound by them: 40 us with the sums of the scores
 // (66 with both reductions at every choice; 49 with the scoring and the choices per lane looked up while running, 44 with
 // what is taken compared again and not kept as lane masks).  The gradient reads and writes 134 MB, 22 us; a token's
 // loads hang on each other (its choices, then their logits), so the next token's are asked for ahead and the chosen
@@ -88,9 +88,14 @@ __device__ __forceinline__ float sigmoid_stated(float l, float* other = nullptr)
   return s;
 }
 
-// exp(x) for x <= 0 from the hardware's 2^x: the product's rounding is an error of |x| 2^-24 of the result, which below
-// 2^-126 is 0.
-__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+// exp(x) for x <= 0: the hardware's 2^y, y = x log2(e) rounded, times 1 + (x - y ln 2), which makes good what the rounding took
+// (up to |x| 2^-24 of the result, as much as that of x = l - m itself).  What remains is 2 ulp at |x| = 80; below 2^-126 it
+// is 0.  A NaN stays one, minus infinity gives 0.
+__device__ __forceinline__ float exp_neg(float x) {
+  x = __builtin_elementwise_maximum(x, -150.0f);
+  const float y = x * 1.44269504f, t = __builtin_amdgcn_exp2f(y);
+  return __builtin_fmaf(t, __builtin_fmaf(-y, 0.693147182f, x), t);
+}
 
 // Orders a wave's LDS accesses before its own later ones (no other wave is involved).
 __device__ __forceinline__ void wave_order() {
@@ -134,7 +139,7 @@ __device__ __forceinline__ void scores_of(const float (&l)[V], float (&s)[V], fl
   float sum = 0.0f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    s[v] = exp_fast(l[v] - m);
+    s[v] = exp_neg(l[v] - m);
     sum += s[v];
   }
   sum = sum_over<G>(sum);
@@ -250,12 +255,12 @@ __global__ __launch_bounds__(256) void route_topk_kernel(RouteArgs a) {
         m = fmax_over<G>(m);
         if (m == -INFINITY) m = 0.0f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) sum += exp_fast(l[v] - m);
+        for (int v = 0; v < V; ++v) sum += exp_neg(l[v] - m);
         sum = sum_over<G>(sum);
       }
 #pragma unroll
       for (int i = 0; i < P; ++i)
-        p[i] = mine[i] < 0 ? 0.0f : SIGMOID ? sigmoid_stated(x[i]) : exp_fast(x[i] - m) * recip_rn(sum);
+        p[i] = mine[i] < 0 ? 0.0f : SIGMOID ? sigmoid_stated(x[i]) : exp_neg(x[i] - m) * recip_rn(sum);
     }
 #pragma unroll
     for (int i = 0; i < P; ++i) {
