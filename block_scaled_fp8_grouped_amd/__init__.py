@@ -867,6 +867,11 @@ def _arg(t, what, dtypes, shape=None):
     return p
 
 
+def _layout(q, key, what):
+    """Pointer of one of a dict's quantized buffers, or of none."""
+    return _arg(q.get(key), f"{what}[{key!r}]", _U8)
+
+
 def _here():
     """What the native calls below begin with: the current device and its stream."""
     if _raw_device is None:
@@ -1038,9 +1043,9 @@ def dispatch_quantize(x, plan, recipe, which, out, weights=None, status=None, st
     splits, choices = plan["splits"], plan["choices"]
     E = int(splits.numel())
     args = (px, T, C, _arg(choices, "plan['choices']", _I32, (N,)), K, _arg(weights, "weights", _F32, (T, K)), N,
-            _arg(splits, "plan['splits']", _I32), E, recipe, which, _quant(out, "row_q", "out"),
-            _quant(out, "row_s", "out"), _quant(out, "col_q", "out"), _quant(out, "col_s", "out"),
-            _dev(status, "status", _I32))
+            _arg(splits, "plan['splits']", _I32), E, recipe, which, _layout(out, "row_q", "out"),
+            _layout(out, "row_s", "out"), _layout(out, "col_q", "out"), _layout(out, "col_s", "out"),
+            _arg(status, "status", _I32))
     _need_quant(out, recipe, N, C, max(E, 1), which, "out")
     _check(lib().bsfp8_dispatch_quantize(*args, _stream(stream)), "dispatch_quantize")
     return out
@@ -1126,9 +1131,9 @@ def grouped_act_checkpoint(activation, h, split_sizes, recipe, which, out, kept,
     F = wide // 2 if activation == ACT_SWIGLU else wide
     E = int(split_sizes.numel())
     args = (activation, ph, _arg(probs, "probs", _F32, (R,)), R, F, _arg(split_sizes, "split_sizes", _I32), E, recipe,
-            which, _quant(out, "row_q", "out"), _quant(out, "row_s", "out"), _quant(out, "col_q", "out"),
-            _quant(out, "col_s", "out"), _quant(kept, "row_q", "kept"), _quant(kept, "row_s", "kept"),
-            _dev(status, "status", _I32))
+            which, _layout(out, "row_q", "out"), _layout(out, "row_s", "out"), _layout(out, "col_q", "out"),
+            _layout(out, "col_s", "out"), _layout(kept, "row_q", "kept"), _layout(kept, "row_s", "kept"),
+            _arg(status, "status", _I32))
     _need_quant(out, recipe, R, F, max(E, 1), which, "out")
     _need_quant(kept, RECIPE_MX, R, wide, 1, ROWWISE, "kept")
     _check(lib().bsfp8_grouped_act_checkpoint(*args, _stream(stream)), "grouped_act_checkpoint")
@@ -1159,10 +1164,10 @@ def grouped_act_checkpoint_grad(activation, kept, dy, split_sizes, recipe, which
     pd, (R, F) = _matrix(dy, "dy", _BF16)
     wide = 2 * F if activation == ACT_SWIGLU else F
     E = int(split_sizes.numel())
-    args = (activation, _quant(kept, "row_q", "kept"), _quant(kept, "row_s", "kept"), _arg(probs, "probs", _F32, (R,)), pd,
-            R, F, _arg(split_sizes, "split_sizes", _I32), E, recipe, which, _quant(out, "row_q", "out"),
-            _quant(out, "row_s", "out"), _quant(out, "col_q", "out"), _quant(out, "col_s", "out"),
-            _quant(q, "col_q", "y"), _quant(q, "col_s", "y"), _arg(dprobs, "dprobs", _F32, (R,)))
+    args = (activation, _layout(kept, "row_q", "kept"), _layout(kept, "row_s", "kept"), _arg(probs, "probs", _F32, (R,)), pd,
+            R, F, _arg(split_sizes, "split_sizes", _I32), E, recipe, which, _layout(out, "row_q", "out"),
+            _layout(out, "row_s", "out"), _layout(out, "col_q", "out"), _layout(out, "col_s", "out"),
+            _layout(q, "col_q", "y"), _layout(q, "col_s", "y"), _arg(dprobs, "dprobs", _F32, (R,)))
     _need_quant(kept, RECIPE_MX, R, wide, 1, ROWWISE, "kept")
     _need_quant(out, recipe, R, wide, max(E, 1), which, "out")
     if y is not None:
@@ -1170,6 +1175,6 @@ def grouped_act_checkpoint_grad(activation, kept, dy, split_sizes, recipe, which
     if dprobs is not None:
         workspace = _workspace(workspace, grouped_act_checkpoint_grad_workspace_bytes(R, F), dy)
     rc = lib().bsfp8_grouped_act_checkpoint_grad(*args, _ptr(workspace) if dprobs is not None else None,
-                                                 _dev(status, "status", _I32), _stream(stream))
+                                                 _arg(status, "status", _I32), _stream(stream))
     _check(rc, "grouped_act_checkpoint_grad")
     return _glu_result(out, y=y, dprobs=dprobs)
