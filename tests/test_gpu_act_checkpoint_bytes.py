@@ -97,3 +97,33 @@ def test_a_nan_keeps_its_mxfp8_code_and_its_blocks_scale(act):
     assert code[r, at].isnan().all() and int(code.isnan().sum()) == 64 * (1 if act == bs.ACT_SRELU else 2)
     same = ~code.isnan()
     assert torch.equal(got["row_q"][same], clean["row_q"][same]) and torch.equal(got["row_s"], clean["row_s"])
+
+
+@pytest.mark.parametrize("act", [bs.ACT_SRELU, bs.ACT_SWIGLU])
+@pytest.mark.parametrize("recipe", [MX, MX4])
+@pytest.mark.parametrize("which", [BOTH, COL])
+def test_several_column_tiles_a_workgroup(act, recipe, which):
+    """More row tiles than launches have segments for: a workgroup's waves meet in LDS again and again.  Random values in all
+    rows, uneven groups, a width that ends inside a tile; whole buffers against the separate calls, several times over."""
+    splits, cols, pad = [9000, 0, 1, 12345, 127, 128, 129, 7000, 4001], 4128, 33
+    h, dy, p, st = draw(splits, cols, act, pad, 4)
+    (rows, wide), experts, live = h.shape, len(splits), sum(splits)
+    kept = zeroed(rows, wide, experts, MX, ROW)
+    q = zeroed(rows, cols, experts, recipe, which)
+    want_q = bs.grouped_act_quantize(act, h, st, recipe, which, zeroed(rows, cols, experts, recipe, which), p)
+    want_kept, values = kept_of(h, live)
+    for _ in range(3):
+        bs.grouped_act_checkpoint(act, h, st, recipe, which, q, kept, p)
+        for got, want in ((q, want_q), (kept, want_kept)):
+            for name in want:
+                assert torch.equal(got[name], want[name]), name
+                got[name].zero_()
+    want_g = bs.grouped_act_quantize(GRAD[act], values, st, recipe, which, zeroed(rows, wide, experts, recipe, which), p, dy)
+    want_y = bs.grouped_act_quantize(act, values, st, recipe, COL, zeroed(rows, cols, experts, recipe, COL), p)
+    g, y = zeroed(rows, wide, experts, recipe, which), zeroed(rows, cols, experts, recipe, COL)
+    for _ in range(3):
+        bs.grouped_act_checkpoint_grad(act, want_kept, dy, st, recipe, which, g, p, y)
+        for got, want in ((g, want_g), (y, want_y)):
+            for name in want:
+                assert torch.equal(got[name], want[name]), name
+                got[name].zero_()

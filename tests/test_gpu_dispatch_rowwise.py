@@ -97,3 +97,18 @@ def test_a_row_without_a_choice_is_zeros(tokens, experts, k, recipe, which, weig
     want = bs.grouped_quantize(rows, plan["splits"], recipe, which, poisoned(n, 96, experts, recipe, which))
     for name in want:
         assert torch.equal(got[name], want[name]), name
+
+
+@pytest.mark.parametrize("recipe,which", [(MX, BOTH), (MX4, BOTH), (MX, ROW), (MX4, bs.COLWISE)])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_several_column_tiles_a_workgroup(recipe, which, weighted):
+    """A launch of more row tiles than it has segments for, random values in all rows, a width that ends inside a tile."""
+    tokens, experts, k, cols = 16400, 37, 2, 4128
+    plan, x, _ = routed(tokens, experts, k, cols, 5)
+    w = torch.exp2(torch.randint(-3, 4, (tokens, k), device=DEV).float()) if weighted else None
+    want = bs.grouped_quantize(bs.dispatch(x, plan, w), plan["splits"], recipe, which,
+                               poisoned(tokens * k, cols, experts, recipe, which))
+    for _ in range(3):
+        got = bs.dispatch_quantize(x, plan, recipe, which, poisoned(tokens * k, cols, experts, recipe, which), weights=w)
+        for name in want:
+            assert torch.equal(got[name], want[name]), name
