@@ -429,12 +429,18 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void combine_grad_kernel(Mov
   }
 }
 
-// f with how many of top_k choices are taken at a time: all of up to 4, sets of 8 above (4 of fp32, to stay within registers).
+// f with how many of top_k choices are taken at a time, all of up to 4, sets of 8 above (4 of fp32, to stay within registers),
+// and an element.
 template <class F>
 static void for_top_k(int K, bool f32, F f) {
-  if (K <= 2) f(std::integral_constant<int, 2>());
-  else if (K <= 4 || f32) f(std::integral_constant<int, 4>());
-  else f(std::integral_constant<int, 8>());
+  if (f32) {
+    if (K <= 2) f(std::integral_constant<int, 2>(), float());
+    else f(std::integral_constant<int, 4>(), float());
+  } else {
+    if (K <= 2) f(std::integral_constant<int, 2>(), uint16_t());
+    else if (K <= 4) f(std::integral_constant<int, 4>(), uint16_t());
+    else f(std::integral_constant<int, 8>(), uint16_t());
+  }
 }
 
 int launch_dispatch(const void* x, bool f32, int64_t T, int64_t C, const int32_t* rows, int K, const float* weights,
@@ -454,10 +460,9 @@ int launch_combine(const void* y, bool f32, int64_t cap, int64_t C, const int32_
   if (s.blocks > kMostThreads / kMoveThreads) return BSFP8_ERR_SHAPE;
   const MoveArgs a{T, C, cap, K, rows, weights, y, add, out, nullptr, nullptr, move_past(T, C, f32)};
   const dim3 grid((unsigned)s.blocks), block(kMoveThreads);
-  for_top_k(K, f32, [&](auto kb) {
-    constexpr int KB = decltype(kb)::value;
-    if (f32) hipLaunchKernelGGL((combine_kernel<float, KB>), grid, block, 0, stream, a, s.shift, s.segments);
-    else hipLaunchKernelGGL((combine_kernel<uint16_t, KB>), grid, block, 0, stream, a, s.shift, s.segments);
+  for_top_k(K, f32, [&](auto kb, auto element) {
+    hipLaunchKernelGGL((combine_kernel<decltype(element), decltype(kb)::value>), grid, block, 0, stream, a, s.shift,
+                       s.segments);
   });
   return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
 }
@@ -471,27 +476,26 @@ int launch_combine_grad(const void* dout, bool f32, int64_t T, int64_t C, const 
   // of 2050 101 / 94 / 92 / 118, 32768 x 4 of 1024 114 / 111 / 120 / 188, 65536 x 4 of 512 112 / 122 / 189 / 327; 16384 x 4
   // of 2048 fp32 277 / 256 / 241 / 225, of 1024 137 / 125 / 119 / 134, 65536 x 4 of 256 123 / 157 / 232 / 363).  Up to an
   // eighth more goes without waves of its own.
-  auto launch = [&](auto w, auto kb, auto y, auto o) {
+  auto launch = [&](auto w, auto kb, auto element, auto y, auto o) {
     constexpr int W = decltype(w)::value, KB = decltype(kb)::value, THREADS = W == 1 ? 256 : 64 * W;
     constexpr bool Y = decltype(y)::value, O = decltype(o)::value;
     const int64_t blocks = W == 1 ? (T + 3) / 4 : T, most = kMostThreads / THREADS;
     const dim3 grid((unsigned)(blocks < most ? blocks : most)), block(THREADS);
-    if (f32) hipLaunchKernelGGL((combine_grad_kernel<float, W, KB, Y, O>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((combine_grad_kernel<uint16_t, W, KB, Y, O>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((combine_grad_kernel<decltype(element), W, KB, Y, O>), grid, block, 0, stream, a);
   };
-  auto go = [&](auto kb, auto y, auto o) {
-    const int64_t bytes = C * (f32 ? 4 : 2);
-    if (bytes <= 1152) launch(std::integral_constant<int, 1>(), kb, y, o);
-    else if (bytes <= 2304) launch(std::integral_constant<int, 2>(), kb, y, o);
-    else if (bytes <= 4608) launch(std::integral_constant<int, 4>(), kb, y, o);
-    else launch(std::integral_constant<int, 8>(), kb, y, o);
+  auto go = [&](auto kb, auto element, auto y, auto o) {
+    const int64_t bytes = C * (int64_t)sizeof(element);
+    if (bytes <= 1152) launch(std::integral_constant<int, 1>(), kb, element, y, o);
+    else if (bytes <= 2304) launch(std::integral_constant<int, 2>(), kb, element, y, o);
+    else if (bytes <= 4608) launch(std::integral_constant<int, 4>(), kb, element, y, o);
+    else launch(std::integral_constant<int, 8>(), kb, element, y, o);
   };
   const std::integral_constant<bool, true> yes;
   const std::integral_constant<bool, false> no;
-  for_top_k(K, f32, [&](auto kb) {
-    if (dweights != nullptr && dy != nullptr) go(kb, yes, yes);
-    else if (dweights != nullptr) go(kb, yes, no);
-    else go(kb, no, yes);
+  for_top_k(K, f32, [&](auto kb, auto element) {
+    if (dweights != nullptr && dy != nullptr) go(kb, element, yes, yes);
+    else if (dweights != nullptr) go(kb, element, yes, no);
+    else go(kb, element, no, yes);
   });
   return hipGetLastError() == hipSuccess ? BSFP8_OK : BSFP8_ERR_LAUNCH;
 }

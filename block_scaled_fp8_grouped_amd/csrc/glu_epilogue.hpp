@@ -57,13 +57,6 @@ __device__ __forceinline__ uint32_t e4m3x4_scaled(float a, float b, float c, flo
   return __builtin_bit_cast(uint32_t, w);
 }
 
-// Orders a wave's LDS writes before its own later LDS reads (no other wave is involved).
-__device__ __forceinline__ void wave_lds_order() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 // Where a gated projection's outputs go; any of them may be NULL.  [R][N] outputs, N columns.
 struct GluOut {
   void* y;  // bf16 or fp32 [R][N]

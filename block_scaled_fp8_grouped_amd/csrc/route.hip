@@ -97,13 +97,6 @@ __device__ __forceinline__ float exp_neg(float x) {
   return __builtin_fmaf(t, __builtin_fmaf(-y, 0.693147182f, x), t);
 }
 
-// Orders a wave's LDS accesses before its own later ones (no other wave is involved).
-__device__ __forceinline__ void wave_order() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 // V values of a row from e0 on; past its end: -infinity.
 template <int V, class T>
 __device__ __forceinline__ void load_logits(const T* row, int e0, int E, float (&l)[V]) {
@@ -236,11 +229,11 @@ __global__ __launch_bounds__(256) void route_topk_kernel(RouteArgs a) {
       for (int v = 0; v < V; ++v) u[v] = __builtin_amdgcn_inverse_ballot_w64(hit[v]) ? 0u : u[v];
       if (__builtin_amdgcn_inverse_ballot_w64(lanes)) taken[group][j] = at;
     }
-    wave_order();
+    wave_lds_order();
     int mine[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) mine[i] = lane + i * G < a.K ? taken[group][lane + i * G] : -1;
-    wave_order();
+    wave_lds_order();
     float p[P], other[P], x[P];
     // (the chosen logits are read again: a lane holds other experts' than those it writes)
 #pragma unroll
@@ -356,10 +349,10 @@ __global__ __launch_bounds__(256) void route_topk_grad_kernel(RouteArgs a) {
       if (chosen_only) {
 #pragma unroll
         for (int v = 0; v < V; ++v) to[v] = l[v];
-        wave_order();
+        wave_lds_order();
 #pragma unroll
         for (int i = 0; i < P; ++i) x[i] = e[i] >= 0 ? row_sm[group][e[i]] : -INFINITY;
-        wave_order();
+        wave_lds_order();
       }
       scores_of<G, V, SIGMOID>(l, s, other);
     } else {
@@ -389,21 +382,21 @@ __global__ __launch_bounds__(256) void route_topk_grad_kernel(RouteArgs a) {
     float d[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) to[v] = 0.0f;
-    wave_order();
+    wave_lds_order();
     bool alone = true;
 #pragma unroll
     for (int i = 0; i < P; ++i)
       if (e[i] >= 0) row_sm[group][e[i]] = __int_as_float(lane + i * G);
-    wave_order();
+    wave_lds_order();
 #pragma unroll
     for (int i = 0; i < P; ++i)
       if (e[i] >= 0) alone &= __float_as_int(row_sm[group][e[i]]) == lane + i * G;
-    wave_order();
+    wave_lds_order();
     if (__ballot(!alone) == 0) {
 #pragma unroll
       for (int i = 0; i < P; ++i)
         if (e[i] >= 0) row_sm[group][e[i]] = g[i];
-      wave_order();
+      wave_lds_order();
 #pragma unroll
       for (int v = 0; v < V; ++v) d[v] = to[v];
     } else {
@@ -415,7 +408,7 @@ __global__ __launch_bounds__(256) void route_topk_grad_kernel(RouteArgs a) {
           part_sm[group][j] = g[i];
         }
       }
-      wave_order();
+      wave_lds_order();
 #pragma unroll
       for (int v = 0; v < V; ++v) d[v] = 0.0f;
       for (int j = 0; j < a.K; ++j) {
@@ -425,7 +418,7 @@ __global__ __launch_bounds__(256) void route_topk_grad_kernel(RouteArgs a) {
         for (int v = 0; v < V; ++v) d[v] += x == v ? y : 0.0f;
       }
     }
-    wave_order();
+    wave_lds_order();
     if constexpr (FULL) {
       float back[V], mean = 0.0f;
 #pragma unroll
@@ -462,7 +455,8 @@ __global__ __launch_bounds__(256) void route_topk_grad_kernel(RouteArgs a) {
   }
 }
 
-// f with the lanes per token, the experts and the choices per lane that E and K take, and the scoring.
+// f with the lanes per token, the experts and the choices per lane that E and K take, and the scoring.  K is at most E: one
+// expert a lane leaves one choice a lane, and a wave's lanes have more than 4 experts.
 template <class F>
 static void for_shape(int E, int K, bool sigmoid, F f) {
   auto scoring = [&](auto g, auto v, auto p) {
@@ -470,25 +464,27 @@ static void for_shape(int E, int K, bool sigmoid, F f) {
     else f(g, v, p, std::false_type());
   };
   auto choices = [&](auto g, auto v) {
-    if constexpr (decltype(g)::value < BSFP8_MAX_TOP_K) {
-      if (K > decltype(g)::value) {
-        scoring(g, v, std::integral_constant<int, BSFP8_MAX_TOP_K / decltype(g)::value>());
+    constexpr int G = decltype(g)::value;
+    if constexpr (G < BSFP8_MAX_TOP_K && decltype(v)::value > 1) {
+      if (K > G) {
+        scoring(g, v, std::integral_constant<int, BSFP8_MAX_TOP_K / G>());
         return;
       }
     }
     scoring(g, v, std::integral_constant<int, 1>());
   };
-  auto with = [&](auto g) {
-    constexpr int G = decltype(g)::value;
-    const int v = (E + G - 1) / G;
-    if (v <= 1) choices(g, std::integral_constant<int, 1>());
-    else if (v <= 2) choices(g, std::integral_constant<int, 2>());
-    else if (v <= 4) choices(g, std::integral_constant<int, 4>());
-    else if (v <= 8) choices(g, std::integral_constant<int, 8>());
+  if (route_lanes(E) == 16) {
+    const std::integral_constant<int, 16> g;
+    if (E <= 16) choices(g, std::integral_constant<int, 1>());
+    else if (E <= 32) choices(g, std::integral_constant<int, 2>());
+    else if (E <= 64) choices(g, std::integral_constant<int, 4>());
+    else if (E <= 128) choices(g, std::integral_constant<int, 8>());
     else choices(g, std::integral_constant<int, 16>());
-  };
-  if (route_lanes(E) == 16) with(std::integral_constant<int, 16>());
-  else with(std::integral_constant<int, 64>());
+  } else {
+    const std::integral_constant<int, 64> g;
+    if (E <= 512) choices(g, std::integral_constant<int, 8>());
+    else choices(g, std::integral_constant<int, 16>());
+  }
 }
 
 int launch_route_topk(const void* logits, bool f32, int64_t T, int E, int K, bool sigmoid, const float* bias,

@@ -23,7 +23,6 @@
 #include "glu_epilogue.hpp"
 #include "group_layout.hpp"
 #include "row_io.hpp"
-#include "token_layout.hpp"
 
 namespace bsfp8 {
 
