@@ -8,7 +8,8 @@
 // equal one more for the lowest expert that has it.
 //
 // What bounds them: 131072 tokens of 128 logits in fp32 are 67 MB, 11 us at 6.2 TB/s.  The choices' comparisons are about
-// 35 vector instructions a choice for 4 tokens, so the forward pass is bound by them: 40 us with the sums of the scores
+// 35 vector instructions a choice for 4 tokens, so the forward pass is bound by them: 40 us with the sums of the scores, 31
+// without, 49 by sigmoid scores with a bias
 // (66 with both reductions at every choice; 49 with the scoring and the choices per lane looked up while running, 44 with
 // what is taken compared again and not kept as lane masks).  The gradient reads and writes 134 MB, 22 us; a token's
 // loads hang on each other (its choices, then their logits), so the next token's are asked for ahead and the chosen

@@ -11,9 +11,11 @@
 //
 // What bounds them: bytes, which come and go at 6.2 TB/s at best, and the instructions that the conversions to codes in two
 // directions take.  65536 gathered rows of 4096 (32 experts, 4 a token) read 134 MB and write 553 MB, 111 us: 169 us.  The
-// SwiGLU's gradient of 65536 x 2048 reads 545 MB and writes 690 MB, 200 us: 318 us, at the 256 registers that leave two
-// waves a SIMD, and with 25 vector instructions for a sigmoid by the forward's steps (278 us with 4, from the hardware's
-// exponential and reciprocal, which put codes next to a border on its other side: 110 of 268 million).  Activation and kept input of 4099 x 4128, 88 MB: 14 us of bytes in 22 us, 1320 workgroups at 1024 places.
+// SwiGLU's gradient of 65536 x 2048 reads 545 MB and writes 690 MB, 200 us: 320 us, at the 256 registers (and 11 spilled)
+// that leave two waves a SIMD, and with 25 vector instructions for a sigmoid by the forward's steps (278 us with 4, from the
+// hardware's exponential and reciprocal, which put codes next to a border on its other side: 110 of 268 million).  The
+// activations' kernels also spill 29 to 162 scalar registers into lanes: a buffer descriptor for each of a lane's 8 rows and each
+// array.  Activation and kept input of 4099 x 4128, 88 MB: 14 us of bytes in 22 us, 1320 workgroups at 1024 places.
 #include <math.h>
 
 #include <type_traits>
@@ -27,8 +29,9 @@
 namespace bsfp8 {
 
 // Codes go past the caches (a line's 128 bytes leave together, and none is read again here): 181 -> 170 us on 65536
-// gathered rows of 4096, whose tokens then stay in them; 288 -> 279 us on the SwiGLU's gradient.  An activation's rowwise
-// codes, which the next product reads, stay in them (SReLU of 4099 x 4128 26.9 -> 22.2 us, layers the same).
+// gathered rows of 4096, whose tokens then stay in them; 288 -> 279 us on the SwiGLU's gradient (with the
+// hardware's sigmoid).  An activation's rowwise codes, which the next product reads, stay in them (SReLU of 4099 x 4128
+// 26.9 -> 22.2 us, layers the same).
 constexpr int kInCaches = 0, kPastCaches = 2;
 constexpr int kTThreads = 256;
 
@@ -708,7 +711,7 @@ __global__ __launch_bounds__(kTThreads, mode_grad(MODE) ? 2 : 1) void act_checkp
   };
 
   // (a tile asked for ahead takes registers that are worth more as waves: 400 us against 368 when the SwiGLU's gradient of
-  // 65536 x 2048 took that)
+  // 65536 x 2048 took that, with the hardware's sigmoid)
   TokenInputs<MODE> x;
   int turn = 0;
   const int64_t begin = seg * a.tiles * W, stop = begin + (int64_t)a.tiles * W, end = stop < F ? stop : F;
@@ -857,7 +860,7 @@ __global__ __launch_bounds__(256) void token_dprobs_kernel(const float* partial,
 
 // Column segments of a launch over `rows` row tiles and `cols` column tiles: as many as give kTFill workgroups, or
 // twice that for an activation's forward (2048 / 4096 / 8192 workgroups: SReLU of 65536 x 4096 300 / 278 / 264 us, its
-// gradient 352 / 335 / 328, SwiGLU's of 65536 x 2048 288 / 281 / 306, 65536 gathered rows of 4096 170 / 170 / 181).
+// gradient 350 / 335 / 329, SwiGLU's of 65536 x 2048 339 / 319 / 353, 65536 gathered rows of 4096 170 / 170 / 179).
 struct TokenSegments {
   int64_t count, tiles;
 };
