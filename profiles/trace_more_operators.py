@@ -1,4 +1,4 @@
-"""What rocprofv3 traces for kernels_tokens.md: each listed case of perf/more_operators.py, and forms beside them, prepared
+"""What rocprofv3 traces: each listed case of perf/more_operators.py, and forms beside them, prepared
 three times over and called 13 times in turn.
 
     rocprofv3 --kernel-trace --stats -d prof -o p --output-format csv -- python3 profiles/trace_more_operators.py [NAME,NAME]
